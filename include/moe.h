@@ -314,6 +314,85 @@ int moe_backward(const moe_shape* shape, const void* u, const void* centroids, c
                  size_t workspace_bytes, const moe_trace* trace, hipStream_t stream);
 
 /*
+ * Around the block: the norm in front of the layer (or of any block), and the
+ * norm, gate and residual behind it.  Rows x [T][d] of the residual stream.
+ *
+ *   moe_block_in   n = x r w,   r = (mean over the row of x^2 + eps)^(-1/2)
+ *   moe_block_out  z = y - skip                       (skip null: z = y)
+ *                  zh = z r w, r from z as above      (w null: zh = z)
+ *                  x_out = res_scale x + gate zh      (gate null: ones)
+ *                  with w_next: n_next = moe_block_in of x_out as stored, under
+ *                  w_next -- the next block's n in the same pass
+ *
+ * moe_forward adds its own input to its output (y = u + ...): called on u = n,
+ * skip = n gives the residual stream the experts' part alone.
+ *
+ * moe_block_shape:
+ *   T, d       rows (0 is a no-op) and columns
+ *   x_dtype    x and x_out: F32 or BF16
+ *   n_dtype    n, n_next and skip: F32 or BF16
+ *   y_dtype    y: F32 or BF16
+ *   gate_rows  consecutive rows that share a row of gate [ceil(T/gate_rows)][d]
+ *              (1: a gate per token; a request's length: a gate per request);
+ *              0: one row for all
+ *   eps        > 0;  res_scale: any finite value
+ * w, w_next [d], gate and every gradient are fp32; sums and statistics are
+ * fp32; bf16 outputs are rounded once (n_next is computed from x_out as it is
+ * stored).  Limits: d a multiple of 8, at most 32768; T below 2^22.
+ *
+ * moe_block_save: what the backward reads, written by the forward where the
+ * pointer is not null:
+ *   rstd       [T]          r of each row
+ *   codes      [T][d]       an 8-bit checkpoint of the normed rows (x, or z): E4M3
+ *   scales     [T][d/128]   codes of v * (448 * (1 / amax)) per 1x128 tile (rounded
+ *                           to nearest even) and scale = amax / 448; scale 1 and
+ *                           zero codes for an all-zero tile; d a multiple of 128.
+ *                           A backward without the rows themselves reads
+ *                           codes * scale in their place: 1.03 bytes per value.
+ * save may be null, and save_next (of x_out, for n_next) only with w_next.
+ * x_out may be x.
+ */
+typedef struct {
+  int32_t T, d;
+  int32_t x_dtype, n_dtype, y_dtype;
+  int32_t gate_rows;
+  float eps, res_scale;
+} moe_block_shape;
+typedef struct {
+  float* rstd;
+  uint8_t* codes;
+  float* scales;
+} moe_block_save;
+int moe_block_in(const moe_block_shape* shape, const void* x, const float* w, void* n, const moe_block_save* save,
+                 hipStream_t stream);
+int moe_block_out(const moe_block_shape* shape, const void* x, const void* y, const void* skip, const float* w,
+                  const float* gate, const float* w_next, void* x_out, void* n_next, const moe_block_save* save,
+                  const moe_block_save* save_next, hipStream_t stream);
+
+/*
+ * Their backward (everything fp32 [T][d] but dw [d] and dgate, laid out as
+ * gate; one workspace of moe_block_workspace_size bytes serves both).
+ *
+ * moe_block_out_backward: for dout, the gradient of x_out:
+ *   dy     of y (and, negated, of skip);  dw, dgate: null exactly where w and
+ *   gate are.  The gradient of x is res_scale dout; moe_block_in_backward adds it.
+ * moe_block_in_backward: for dn - dn_sub, the gradient of n (dn_sub null: dn;
+ * with skip = n, dn is moe_backward's du and dn_sub is dy):
+ *   dx     = res_scale dout + the gradient through the norm (dout null: the
+ *          latter alone);  dw
+ * Rows y (with skip) or x may be null: then save's checkpoint is read.  rstd
+ * is read wherever there is a norm.  dx may be dout or dn, dy may be dout.
+ * Sums run in a fixed order (bit-reproducible).
+ */
+int moe_block_workspace_size(const moe_block_shape* shape, size_t* bytes);
+int moe_block_in_backward(const moe_block_shape* shape, const float* dn, const float* dn_sub, const float* dout,
+                          const void* x, const float* w, const moe_block_save* save, float* dx, float* dw,
+                          void* workspace, size_t workspace_bytes, hipStream_t stream);
+int moe_block_out_backward(const moe_block_shape* shape, const float* dout, const void* y, const void* skip,
+                           const float* w, const float* gate, const moe_block_save* save, float* dy, float* dw,
+                           float* dgate, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
  * Aux-loss-free bias update (xyznot summary, section 2: b_i is lowered by
  * gamma for an overloaded expert and raised by gamma for an underloaded one),
  * in place:

@@ -5,14 +5,22 @@ ABI in include/moe.h); this package only builds and binds it.
 """
 
 from .binding import (  # noqa: F401
+    BlockSave,
+    BlockShape,
     ExpertWeights,
     LayerShape,
     MoEError,
+    alloc_block_save,
     alloc_routing,
     alloc_train_workspace,
     alloc_weight_grads,
     alloc_workspace,
+    block_workspace_size,
     load_library,
+    moe_block_in,
+    moe_block_in_backward,
+    moe_block_out,
+    moe_block_out_backward,
     moe_forward,
     moe_backward,
     moe_forward_static,

@@ -29,7 +29,9 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_LAU
 
 EXPORTED = ("moe_status_str", "moe_version", "moe_workspace_size", "moe_workspace_layout", "moe_route",
             "moe_forward", "moe_forward_static", "moe_train_workspace_size", "moe_forward_train", "moe_backward",
-            "moe_update_bias", "moe_quantize_weight_e4m3", "moe_quantize_act_e4m3")
+            "moe_update_bias", "moe_quantize_weight_e4m3", "moe_quantize_act_e4m3",
+            "moe_block_in", "moe_block_out", "moe_block_workspace_size", "moe_block_in_backward",
+            "moe_block_out_backward")
 
 STATIC_SCRATCH_BYTES = 64 << 20   # MOE_STATIC_SCRATCH_BYTES
 
@@ -78,6 +80,15 @@ class WeightGrads(ctypes.Structure):
 class Routing(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("topk_idx", "topk_gate", "expert_counts", "expert_offsets", "perm_token", "pos")]
+
+
+class CBlockShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "d", "x_dtype", "n_dtype", "y_dtype", "gate_rows")] + \
+               [(n, ctypes.c_float) for n in ("eps", "res_scale")]
+
+
+class CBlockSave(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("rstd", "codes", "scales")]
 
 
 DEBUG_LIB_PATH = os.path.join(_PKG, "libmoe_mi355x_debug.so")
@@ -143,6 +154,17 @@ def _open(path: str) -> ctypes.CDLL:
     lib.moe_quantize_weight_e4m3.argtypes = [vp, i32, i64, i32, i32, vp, vp, vp]
     lib.moe_quantize_act_e4m3.restype = ctypes.c_int
     lib.moe_quantize_act_e4m3.argtypes = [vp, i32, i32, vp, vp, vp]
+    bs, bk = ctypes.POINTER(CBlockShape), ctypes.POINTER(CBlockSave)
+    lib.moe_block_in.restype = ctypes.c_int
+    lib.moe_block_in.argtypes = [bs, vp, vp, vp, bk, vp]
+    lib.moe_block_out.restype = ctypes.c_int
+    lib.moe_block_out.argtypes = [bs, vp, vp, vp, vp, vp, vp, vp, vp, bk, bk, vp]
+    lib.moe_block_workspace_size.restype = ctypes.c_int
+    lib.moe_block_workspace_size.argtypes = [bs, ctypes.POINTER(sz)]
+    lib.moe_block_in_backward.restype = ctypes.c_int
+    lib.moe_block_in_backward.argtypes = [bs, vp, vp, vp, vp, vp, bk, vp, vp, vp, sz, vp]
+    lib.moe_block_out_backward.restype = ctypes.c_int
+    lib.moe_block_out_backward.argtypes = [bs, vp, vp, vp, vp, vp, bk, vp, vp, vp, vp, sz, vp]
     return lib
 
 
@@ -369,6 +391,162 @@ def moe_backward(shape: LayerShape, u: torch.Tensor, centroids: torch.Tensor, we
                                      ctypes.byref(trace) if trace is not None else None, _stream())
     _check(rc, "moe_backward")
     return du, dE, grads
+
+
+# ---------------------------------------------------------------- around the block
+
+
+@dataclass
+class BlockShape:
+    """Rows of the residual stream around a block (moe_block_shape): x and
+    x_out in x_dtype, n, n_next and skip in n_dtype, y in y_dtype; gate_rows
+    consecutive rows share a gate row (0: one gate row for all)."""
+    T: int
+    d: int
+    x_dtype: str = "bf16"
+    n_dtype: str = "bf16"
+    y_dtype: str = "f32"
+    gate_rows: int = 0
+    eps: float = 1e-6
+    res_scale: float = 1.0
+
+    @property
+    def gates(self) -> int:
+        return -(-self.T // self.gate_rows) if self.gate_rows > 0 else 1
+
+    def c(self) -> CBlockShape:
+        return CBlockShape(self.T, self.d, DTYPE_CODE[self.x_dtype], DTYPE_CODE[self.n_dtype],
+                           DTYPE_CODE[self.y_dtype], self.gate_rows, self.eps, self.res_scale)
+
+
+@dataclass
+class BlockSave:
+    """What the backward of moe_block_in / moe_block_out reads: each row's
+    1/rms, and with ``codes`` and ``scales`` an 8-bit (E4M3, 1x128 tiles)
+    checkpoint of the normed rows."""
+    rstd: Optional[torch.Tensor] = None     # [T] fp32
+    codes: Optional[torch.Tensor] = None    # [T, d] uint8
+    scales: Optional[torch.Tensor] = None   # [T, d/128] fp32
+
+
+def alloc_block_save(shape: BlockShape, e4m3: bool = False, device="cuda") -> BlockSave:
+    T, d = shape.T, shape.d
+    save = BlockSave(torch.empty((T,), dtype=torch.float32, device=device))
+    if e4m3:
+        save.codes = torch.empty((T, d), dtype=torch.uint8, device=device)
+        save.scales = torch.empty((T, d // 128), dtype=torch.float32, device=device)
+    return save
+
+
+def block_workspace_size(shape: BlockShape) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_block_workspace_size(ctypes.byref(shape.c()), ctypes.byref(n)),
+           "moe_block_workspace_size")
+    return n.value
+
+
+def _arg(t: Optional[torch.Tensor], name: str, dtype: str, *size: int) -> Optional[int]:
+    """Device pointer of an argument (None stays None) after a check of its type and size."""
+    if t is None:
+        return None
+    if t.dtype != _ARG_DT[dtype] or t.shape != size:
+        raise ValueError(f"{name}: expected {dtype} {list(size)}, got {t.dtype} {list(t.shape)}")
+    return _ptr(t)
+
+
+_ARG_DT = {"f32": torch.float32, "bf16": torch.bfloat16, "u8": torch.uint8, "i32": torch.int32}
+
+
+def _save_struct(shape: BlockShape, save: Optional[BlockSave]) -> Optional[CBlockSave]:
+    if save is None:
+        return None
+    T, d = shape.T, shape.d
+    return CBlockSave(_arg(save.rstd, "rstd", "f32", T), _arg(save.codes, "codes", "u8", T, d),
+                      _arg(save.scales, "scales", "f32", T, d // 128))
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def _block_workspace(shape: BlockShape, workspace: Optional[torch.Tensor], device) -> torch.Tensor:
+    if workspace is not None:
+        return workspace
+    return torch.empty(max(block_workspace_size(shape), 1), dtype=torch.uint8, device=device)
+
+
+def moe_block_in(shape: BlockShape, x: torch.Tensor, w: torch.Tensor, save: Optional[BlockSave] = None,
+                 n: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The norm in front of a block: n = x r w, r = 1 / sqrt(mean x^2 + eps).
+    ``save`` receives what the backward needs (alloc_block_save)."""
+    T, d = shape.T, shape.d
+    if n is None:
+        n = torch.empty((T, d), dtype=_ARG_DT[shape.n_dtype], device=x.device)
+    rc = load_library().moe_block_in(ctypes.byref(shape.c()), _arg(x, "x", shape.x_dtype, T, d), _arg(w, "w", "f32", d),
+                                     _arg(n, "n", shape.n_dtype, T, d), _ref(_save_struct(shape, save)), _stream())
+    _check(rc, "moe_block_in")
+    return n
+
+
+def moe_block_out(shape: BlockShape, x: torch.Tensor, y: torch.Tensor, w: Optional[torch.Tensor] = None,
+                  gate: Optional[torch.Tensor] = None, skip: Optional[torch.Tensor] = None,
+                  w_next: Optional[torch.Tensor] = None, save: Optional[BlockSave] = None,
+                  save_next: Optional[BlockSave] = None, x_out: Optional[torch.Tensor] = None,
+                  n_next: Optional[torch.Tensor] = None):
+    """x_out = res_scale x + gate norm(y - skip; w), and with ``w_next`` the next
+    block's n_next = norm(x_out; w_next).  Without ``w`` there is no norm, without
+    ``gate`` no gate.  Returns (x_out, n_next or None)."""
+    T, d = shape.T, shape.d
+    if x_out is None:
+        x_out = torch.empty((T, d), dtype=_ARG_DT[shape.x_dtype], device=x.device)
+    if n_next is None and w_next is not None:
+        n_next = torch.empty((T, d), dtype=_ARG_DT[shape.n_dtype], device=x.device)
+    rc = load_library().moe_block_out(
+        ctypes.byref(shape.c()), _arg(x, "x", shape.x_dtype, T, d), _arg(y, "y", shape.y_dtype, T, d),
+        _arg(skip, "skip", shape.n_dtype, T, d), _arg(w, "w", "f32", d), _arg(gate, "gate", "f32", shape.gates, d),
+        _arg(w_next, "w_next", "f32", d), _arg(x_out, "x_out", shape.x_dtype, T, d),
+        _arg(n_next, "n_next", shape.n_dtype, T, d), _ref(_save_struct(shape, save)),
+        _ref(_save_struct(shape, save_next)), _stream())
+    _check(rc, "moe_block_out")
+    return x_out, n_next
+
+
+def moe_block_in_backward(shape: BlockShape, dn: torch.Tensor, w: torch.Tensor, save: BlockSave,
+                          x: Optional[torch.Tensor] = None, dn_sub: Optional[torch.Tensor] = None,
+                          do: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """(dx, dw) of moe_block_in for the gradient dn - dn_sub of n; dx also takes
+    res_scale do, the gradient that reaches x beside the block.  Without ``x`` the
+    8-bit checkpoint in ``save`` is read."""
+    T, d = shape.T, shape.d
+    dx = torch.empty((T, d), dtype=torch.float32, device=dn.device)
+    dw = torch.empty((d,), dtype=torch.float32, device=dn.device)
+    ws = _block_workspace(shape, workspace, dn.device)
+    rc = load_library().moe_block_in_backward(
+        ctypes.byref(shape.c()), _arg(dn, "dn", "f32", T, d), _arg(dn_sub, "dn_sub", "f32", T, d),
+        _arg(do, "do", "f32", T, d), _arg(x, "x", shape.x_dtype, T, d), _arg(w, "w", "f32", d),
+        _ref(_save_struct(shape, save)), _ptr(dx), _ptr(dw), _ptr(ws), ws.numel(), _stream())
+    _check(rc, "moe_block_in_backward")
+    return dx, dw
+
+
+def moe_block_out_backward(shape: BlockShape, do: torch.Tensor, save: Optional[BlockSave],
+                           w: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                           y: Optional[torch.Tensor] = None, skip: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None):
+    """(dy, dw, dgate) of moe_block_out for the gradient do of x_out (dw, dgate:
+    None without w, gate).  The gradient of skip is -dy, that of x is
+    res_scale do.  Without ``y`` the 8-bit checkpoint in ``save`` is read."""
+    T, d = shape.T, shape.d
+    dy = torch.empty((T, d), dtype=torch.float32, device=do.device)
+    dw = torch.empty((d,), dtype=torch.float32, device=do.device) if w is not None else None
+    dgate = torch.empty((shape.gates, d), dtype=torch.float32, device=do.device) if gate is not None else None
+    ws = _block_workspace(shape, workspace, do.device)
+    rc = load_library().moe_block_out_backward(
+        ctypes.byref(shape.c()), _arg(do, "do", "f32", T, d), _arg(y, "y", shape.y_dtype, T, d),
+        _arg(skip, "skip", shape.n_dtype, T, d), _arg(w, "w", "f32", d), _arg(gate, "gate", "f32", shape.gates, d),
+        _ref(_save_struct(shape, save)), _ptr(dy), _ptr(dw), _ptr(dgate), _ptr(ws), ws.numel(), _stream())
+    _check(rc, "moe_block_out_backward")
+    return dy, dw, dgate
 
 
 def moe_update_bias(bias: torch.Tensor, counts: torch.Tensor, total_assignments: int, gamma: float = 0.001):

@@ -1,0 +1,517 @@
+// The norms before and after a block, with its gate and residual scale:
+//
+//   block_in   n = x r w,  r = (mean_c x^2 + eps)^(-1/2)
+//   block_out  z = y - skip,  x' = beta x + gate zh w,  zh = z r  (r = 1 and
+//              w = 1 without a norm), then optionally the next block's norm of
+//              x' as stored
+//   backward   of v r w for the upstream g:  a = g w,  vh = v r,
+//              dv = r (a - vh mean_c(a vh)),  dw = sum_t g vh
+//              (block_in: g = dn - dn_sub, v = x; block_out: g = dout gate,
+//              v = z, and dgate = w sum over the gate's rows of dout zh)
+//
+// With a checkpoint, v is also kept as E4M3 codes with one fp32 scale per
+// 1x128 tile (read as the framework's other 1x128 tiles are), and the backward reads
+// codes * scale instead of the rows: 1.03 bytes per value instead of 2 (x) or
+// 6 (an fp32 y and a bf16 skip).  r stays that of the exact rows.
+//
+// All of it is bound by HBM: each value is loaded once into registers, where
+// its row stays between the row's sum and its use, and each result is stored
+// once.  A block takes whole rows, 8 consecutive columns to a thread (16-byte
+// loads of bf16, 16 lanes to a 128-column tile).  Statistics and sums are fp32
+// throughout, in a fixed order; outputs in bf16 are rounded once, at the
+// store.
+#include "kernels.hpp"
+
+namespace moe {
+
+namespace {
+
+// Eight consecutive values at element offset o of p (f32 or bf16).
+struct Raw8 {
+  uint4 a, b;
+};
+template <int FMT>
+__device__ __forceinline__ Raw8 load8(const void* p, size_t o) {
+  Raw8 r;
+  if constexpr (FMT == FMT_F32) {
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + o);
+    r.a = q[0];
+    r.b = q[1];
+  } else {
+    r.a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + o);
+    r.b = make_uint4(0, 0, 0, 0);
+  }
+  return r;
+}
+template <int FMT>
+__device__ __forceinline__ void values8(const Raw8& r, float (&v)[8]) {
+  if constexpr (FMT == FMT_F32) {
+    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[e]);
+  } else {
+    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[2 * e] = __uint_as_float(w[e] << 16);
+      v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    }
+  }
+}
+
+__device__ __forceinline__ void load8f(const float* p, size_t o, float (&v)[8]) {
+  values8<FMT_F32>(load8<FMT_F32>(p, o), v);
+}
+
+// Stores eight values (bf16: rounded to nearest even); v becomes what was stored.
+template <int FMT>
+__device__ __forceinline__ void store8(void* p, size_t o, float (&v)[8]) {
+  if constexpr (FMT == FMT_F32) {
+    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + o);
+    q[0] = make_float4(v[0], v[1], v[2], v[3]);
+    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    Raw8 r;
+    r.a = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
+    r.b = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + o) = r.a;
+    values8<FMT_BF16>(r, v);
+  }
+}
+
+// Sum over the block's threads, the same in each of them: a butterfly in the
+// wave, then the waves' sums in order.  `red` (one float per wave) may be
+// used again after the next barrier.
+template <int TPB>
+__device__ __forceinline__ float block_sum(float v, float* red) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float s = 0.f;
+#pragma unroll
+  for (int w = 0; w < TPB / 64; ++w) s += red[w];
+  return s;
+}
+
+__device__ __forceinline__ float rstd_of(float sumsq, int d, float eps) {
+  return 1.0f / sqrtf(sumsq / static_cast<float>(d) + eps);
+}
+
+// The 1x128 tile that holds this thread's eight values (16 lanes to a tile):
+// scale amax / 448 (1 for an all-zero tile), codes of v * (448 * (1 / amax)).
+__device__ __forceinline__ void save_tile(const float (&v)[8], uint8_t* codes, float* scales, size_t row, int d, int c) {
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
+  m = wave_max_16(m);
+  const float inv = m == 0.f ? 0.f : 448.f * (1.f / m);
+  *reinterpret_cast<uint2*>(codes + row * d + c) =
+      make_uint2(e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                 e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+  if ((threadIdx.x & 15) == 0) scales[row * (d / 128) + c / 128] = m == 0.f ? 1.f : m / 448.f;
+}
+
+__device__ __forceinline__ void decode8(const uint2 q, float s, float (&v)[8]) {
+  const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(q.x, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(q.x, true);
+  const auto c = __builtin_amdgcn_cvt_pk_f32_fp8(q.y, false), e = __builtin_amdgcn_cvt_pk_f32_fp8(q.y, true);
+  v[0] = a[0] * s; v[1] = a[1] * s; v[2] = b[0] * s; v[3] = b[1] * s;
+  v[4] = c[0] * s; v[5] = c[1] * s; v[6] = e[0] * s; v[7] = e[1] * s;
+}
+
+// ------------------------------------------------------------------ forward
+
+template <int XF, int NF, int NV, int TPB>
+__global__ __launch_bounds__(TPB) void block_in_kernel(BlockInArgs a) {
+  __shared__ float red[TPB / 64];
+  const size_t row = blockIdx.x;
+  float x[NV][8];
+  Raw8 raw[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = 8 * (threadIdx.x + TPB * i);
+    if (c < a.d) raw[i] = load8<XF>(a.x, row * a.d + c);
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = 8 * (threadIdx.x + TPB * i);
+    if (c >= a.d) continue;
+    values8<XF>(raw[i], x[i]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(x[i][e], x[i][e], ss);
+  }
+  const float r = rstd_of(block_sum<TPB>(ss, red), a.d, a.eps);
+  if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = r;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = 8 * (threadIdx.x + TPB * i);
+    if (c >= a.d) continue;
+    if (a.codes != nullptr) save_tile(x[i], a.codes, a.scales, row, a.d, c);
+    float w[8];
+    load8f(a.w, c, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] *= x[i][e] * r;
+    store8<NF>(a.n, row * a.d + c, w);
+  }
+}
+
+template <int XF, int NF, int YF, int NV, int TPB>
+__global__ __launch_bounds__(TPB) void block_out_kernel(BlockOutArgs a) {
+  __shared__ float red[2][TPB / 64];
+  const size_t row = blockIdx.x;
+  Raw8 ry[NV], rs[NV], rx[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = 8 * (threadIdx.x + TPB * i);
+    if (c >= a.d) continue;
+    ry[i] = load8<YF>(a.y, row * a.d + c);
+    if (a.skip != nullptr) rs[i] = load8<NF>(a.skip, row * a.d + c);
+    rx[i] = load8<XF>(a.x, row * a.d + c);
+  }
+  float z[NV][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = 8 * (threadIdx.x + TPB * i);
+    if (c >= a.d) continue;
+    values8<YF>(ry[i], z[i]);
+    if (a.skip != nullptr) {
+      float s[8];
+      values8<NF>(rs[i], s);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[i][e] -= s[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(z[i][e], z[i][e], ss);
+  }
+  float r = 1.f;
+  if (a.w != nullptr) {
+    r = rstd_of(block_sum<TPB>(ss, red[0]), a.d, a.eps);
+    if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = r;
+  }
+  const size_t grow = a.gate != nullptr && a.gate_rows > 0 ? row / a.gate_rows : 0;
+  ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = 8 * (threadIdx.x + TPB * i);
+    if (c >= a.d) continue;
+    if (a.codes != nullptr) save_tile(z[i], a.codes, a.scales, row, a.d, c);
+    float x[8], t[8];
+    if (a.w != nullptr) {
+      load8f(a.w, c, t);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[i][e] *= r * t[e];
+    }
+    if (a.gate != nullptr) {
+      load8f(a.gate, grow * a.d + c, t);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[i][e] *= t[e];
+    }
+    values8<XF>(rx[i], x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[i][e] = fmaf(a.res_scale, x[e], z[i][e]);
+    store8<XF>(a.x_out, row * a.d + c, z[i]);   // z: x' as stored
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(z[i][e], z[i][e], ss);
+  }
+  if (a.w_next == nullptr) return;
+  r = rstd_of(block_sum<TPB>(ss, red[1]), a.d, a.eps);
+  if (a.rstd_next != nullptr && threadIdx.x == 0) a.rstd_next[row] = r;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = 8 * (threadIdx.x + TPB * i);
+    if (c >= a.d) continue;
+    if (a.codes_next != nullptr) save_tile(z[i], a.codes_next, a.scales_next, row, a.d, c);
+    float w[8];
+    load8f(a.w_next, c, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] *= z[i][e] * r;
+    store8<NF>(a.n_next, row * a.d + c, w);
+  }
+}
+
+// ------------------------------------------------------------------ backward
+
+// Block b's rows.  Gate rows of at most BLOCK_BWD_ROWS rows (whole gates to a
+// block): the block finishes their dgate itself and leaves sum g vh.  Longer
+// ones are cut into runs of BLOCK_BWD_ROWS, none across a gate, and the block
+// leaves sum dout vh of its run for the kernels below.
+struct BwdRows {
+  long long t0, t1;
+};
+__device__ __forceinline__ BwdRows bwd_rows(const BlockBwdArgs& a) {
+  const long long L = a.gate_len, b = blockIdx.x;
+  if (a.whole_gates) {
+    const long long n = L * (BLOCK_BWD_ROWS / L);
+    return {b * n, min(b * n + n, static_cast<long long>(a.T))};
+  }
+  const long long g = b / a.runs, j = b - g * a.runs;
+  const long long t0 = g * L + j * BLOCK_BWD_ROWS;
+  const long long t1 = min(min(t0 + BLOCK_BWD_ROWS, (g + 1) * L), static_cast<long long>(a.T));
+  return {t0, t1};
+}
+
+// VF: the rows v: FMT_F32 / FMT_BF16 (less `skip`, of format SF, where given) or
+// FMT_E4M3 codes.
+template <int VF, int SF, int NV, int TPB>
+__global__ __launch_bounds__(TPB) void block_bwd_kernel(BlockBwdArgs a) {
+  __shared__ float red[2][TPB / 64];
+  const BwdRows rows = bwd_rows(a);
+  float acc[NV][8], gacc[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[i][e] = gacc[i][e] = 0.f;
+
+  for (long long t = rows.t0; t < rows.t1; ++t) {
+    const size_t row = static_cast<size_t>(t), ro = row * a.d;
+    const size_t gro = a.gate != nullptr ? row / a.gate_len * a.d : 0;
+    const float r = a.w != nullptr ? a.rstd[row] : 1.f;
+    float g[NV][8], v[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = 8 * (threadIdx.x + TPB * i);
+      if (c >= a.d) continue;
+      load8f(a.g, ro + c, g[i]);
+      if (a.g_sub != nullptr) {
+        float s[8];
+        load8f(a.g_sub, ro + c, s);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[i][e] -= s[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+      if constexpr (VF == FMT_E4M3) {
+        const uint2 q = *reinterpret_cast<const uint2*>(a.codes + ro + c);
+        decode8(q, a.scales[row * (a.d / 128) + c / 128], v[i]);
+      } else if (a.v != nullptr) {   // null: neither norm nor gate
+        values8<VF>(load8<VF>(a.v, ro + c), v[i]);
+        if (a.skip != nullptr) {
+          float s[8];
+          values8<SF>(load8<SF>(a.skip, ro + c), s);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[i][e] -= s[e];
+        }
+      }
+    }
+    // v: vh; acc (whole gates: gacc, until the gate's last row) += g vh; g: a
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = 8 * (threadIdx.x + TPB * i);
+      if (c >= a.d) continue;
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[i][e] *= r;
+        gacc[i][e] = fmaf(g[i][e], v[i][e], gacc[i][e]);
+      }
+      if (a.gate != nullptr) {
+        load8f(a.gate, gro + c, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[i][e] *= f[e];
+      }
+      if (a.w != nullptr) {
+        load8f(a.w, c, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          g[i][e] *= f[e];
+          dot = fmaf(g[i][e], v[i][e], dot);
+        }
+      }
+    }
+    float mean = 0.f;
+    if (a.w != nullptr) mean = block_sum<TPB>(dot, red[t & 1]) / static_cast<float>(a.d);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = 8 * (threadIdx.x + TPB * i);
+      if (c >= a.d) continue;
+      if (a.w != nullptr) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[i][e] = r * (g[i][e] - v[i][e] * mean);
+      }
+      if (a.res != nullptr) {
+        float s[8];
+        load8f(a.res, ro + c, s);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[i][e] = fmaf(a.res_scale, s[e], g[i][e]);
+      }
+      store8<FMT_F32>(a.dv, ro + c, g[i]);
+    }
+    if (a.whole_gates && (t + 1 == rows.t1 || (t + 1) % a.gate_len == 0)) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = 8 * (threadIdx.x + TPB * i);
+        if (c >= a.d) continue;
+        float f[8];
+        load8f(a.gate, gro + c, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[i][e] = fmaf(f[e], gacc[i][e], acc[i][e]);
+        if (a.w != nullptr) {
+          load8f(a.w, c, f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) gacc[i][e] *= f[e];
+        }
+        if (a.dgate != nullptr) store8<FMT_F32>(a.dgate, gro + c, gacc[i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) gacc[i][e] = 0.f;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = 8 * (threadIdx.x + TPB * i);
+    if (c < a.d) store8<FMT_F32>(a.part, static_cast<size_t>(blockIdx.x) * a.d + c, a.whole_gates ? acc[i] : gacc[i]);
+  }
+}
+
+// Column sums of part[first .. first + n) in a fixed order: 16 threads x 4
+// columns, 64 row lanes (row lane l takes rows l, l + 64, ...), the lanes' sums
+// added in order.  Block (x, g): columns 64 x .., rows g n ...
+//   finish_gates: s_g -> dgate[g] = w s_g, q[g] = gate[g] s_g (dw's summand)
+//   otherwise:    out[g] = s_g
+struct ColSumArgs {
+  const float* part;
+  int n, d;
+  const float* w;      // nullable: ones
+  const float* gate;   // nullable: ones
+  float* dgate;        // nullable
+  float* q;            // nullable
+};
+constexpr int CS_LANES = 64;
+__global__ __launch_bounds__(1024) void block_colsum_kernel(ColSumArgs a) {
+  __shared__ float4 s[CS_LANES][16];
+  const int tc = threadIdx.x & 15, l = threadIdx.x >> 4;
+  const int c = 64 * blockIdx.x + 4 * tc;
+  const size_t g = blockIdx.y;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (c < a.d) {
+    const float* p = a.part + g * a.n * a.d + c;
+#pragma unroll 4
+    for (int r = l; r < a.n; r += CS_LANES) {
+      const float4 x = *reinterpret_cast<const float4*>(p + static_cast<size_t>(r) * a.d);
+      v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+    }
+  }
+  s[l][tc] = v;
+  __syncthreads();
+  // 64 threads, one column each
+  if (threadIdx.x >= 64) return;
+  const int col = 64 * blockIdx.x + threadIdx.x;
+  if (col >= a.d) return;
+  const float* col_s = reinterpret_cast<const float*>(&s[0][0]) + threadIdx.x;
+  float sum = 0.f;
+  const int lanes = min(a.n, CS_LANES);
+  for (int i = 0; i < lanes; ++i) sum += col_s[i * 64];
+  if (a.dgate != nullptr) a.dgate[g * a.d + col] = a.w != nullptr ? a.w[col] * sum : sum;
+  if (a.q != nullptr) a.q[g * a.d + col] = a.gate != nullptr ? a.gate[g * a.d + col] * sum : sum;
+}
+
+// Threads and 8-column vectors per thread that hold a row of d columns.
+struct RowShape {
+  int tpb, nv;
+};
+RowShape row_shape(int d) {
+  if (d <= 2048) return {256, 1};
+  if (d <= 4096) return {256, 2};
+  if (d <= 8192) return {256, 4};
+  return {1024, 4};
+}
+
+// f.template operator()<NV, TPB>() for d columns
+template <class F>
+hipError_t with_row_shape(int d, F&& f) {
+  const RowShape s = row_shape(d);
+  if (s.tpb == 256 && s.nv == 1) f.template operator()<1, 256>();
+  else if (s.tpb == 256 && s.nv == 2) f.template operator()<2, 256>();
+  else if (s.tpb == 256) f.template operator()<4, 256>();
+  else f.template operator()<4, 1024>();
+  return hipGetLastError();
+}
+
+template <class F>
+hipError_t with_fmt(int fmt, F&& f) {   // f32 or bf16
+  return fmt == FMT_F32 ? f.template operator()<FMT_F32>() : f.template operator()<FMT_BF16>();
+}
+
+}  // namespace
+
+MOE_DEBUG_FILE(block)
+
+hipError_t launch_block_in(const BlockInArgs& a, hipStream_t s) {
+  if (a.T == 0) return hipSuccess;
+  return with_fmt(a.x_fmt, [&]<int XF>() {
+    return with_fmt(a.n_fmt, [&]<int NF>() {
+      return with_row_shape(a.d, [&]<int NV, int TPB>() {
+        hipLaunchKernelGGL((block_in_kernel<XF, NF, NV, TPB>), dim3(a.T), dim3(TPB), 0, s, a);
+      });
+    });
+  });
+}
+
+hipError_t launch_block_out(const BlockOutArgs& a, hipStream_t s) {
+  if (a.T == 0) return hipSuccess;
+  return with_fmt(a.x_fmt, [&]<int XF>() {
+    return with_fmt(a.n_fmt, [&]<int NF>() {
+      return with_fmt(a.y_fmt, [&]<int YF>() {
+        return with_row_shape(a.d, [&]<int NV, int TPB>() {
+          hipLaunchKernelGGL((block_out_kernel<XF, NF, YF, NV, TPB>), dim3(a.T), dim3(TPB), 0, s, a);
+        });
+      });
+    });
+  });
+}
+
+hipError_t launch_block_bwd(BlockBwdArgs a, hipStream_t s) {
+  const BlockBwdPlan p = block_bwd_plan(a.T, a.gate_len, a.gates, a.gate != nullptr);
+  a.whole_gates = p.whole_gates;
+  a.runs = p.runs;
+  if (p.blocks > 0) {
+    const dim3 grid(static_cast<unsigned>(p.blocks));
+    hipError_t e = with_row_shape(a.d, [&]<int NV, int TPB>() {
+      if (a.codes != nullptr)
+        hipLaunchKernelGGL((block_bwd_kernel<FMT_E4M3, FMT_F32, NV, TPB>), grid, dim3(TPB), 0, s, a);
+      else if (a.v_fmt == FMT_F32 && a.skip_fmt == FMT_F32)
+        hipLaunchKernelGGL((block_bwd_kernel<FMT_F32, FMT_F32, NV, TPB>), grid, dim3(TPB), 0, s, a);
+      else if (a.v_fmt == FMT_F32)
+        hipLaunchKernelGGL((block_bwd_kernel<FMT_F32, FMT_BF16, NV, TPB>), grid, dim3(TPB), 0, s, a);
+      else if (a.skip_fmt == FMT_F32)
+        hipLaunchKernelGGL((block_bwd_kernel<FMT_BF16, FMT_F32, NV, TPB>), grid, dim3(TPB), 0, s, a);
+      else
+        hipLaunchKernelGGL((block_bwd_kernel<FMT_BF16, FMT_BF16, NV, TPB>), grid, dim3(TPB), 0, s, a);
+    });
+    if (e != hipSuccess) return e;
+  }
+  const unsigned cb = static_cast<unsigned>(ceil_div(a.d, 64));
+  if (p.whole_gates) {
+    if (a.dw == nullptr) return hipSuccess;
+    const ColSumArgs c{a.part, static_cast<int>(p.blocks), a.d, nullptr, nullptr, nullptr, a.dw};
+    hipLaunchKernelGGL(block_colsum_kernel, dim3(cb, 1), dim3(1024), 0, s, c);
+    return hipGetLastError();
+  }
+  if (a.dw == nullptr && a.dgate == nullptr) return hipSuccess;
+  // per gate: dgate and the gate's summand of dw (dw itself where there is one gate)
+  float* q = a.part + static_cast<size_t>(p.blocks) * a.d;
+  const ColSumArgs c1{a.part, p.runs, a.d, a.w, a.gate, a.dgate, a.dw == nullptr ? nullptr : (p.gates == 1 ? a.dw : q)};
+  // the grid's second dimension holds at most 65535 gates
+  for (long long g0 = 0; g0 < p.gates; g0 += 32768) {
+    ColSumArgs cg = c1;
+    const long long n = p.gates - g0 < 32768 ? p.gates - g0 : 32768;
+    const size_t go = static_cast<size_t>(g0) * a.d;
+    cg.part += go * p.runs;
+    if (cg.gate != nullptr) cg.gate += go;
+    if (cg.dgate != nullptr) cg.dgate += go;
+    if (cg.q != nullptr) cg.q += go;
+    hipLaunchKernelGGL(block_colsum_kernel, dim3(cb, static_cast<unsigned>(n)), dim3(1024), 0, s, cg);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (a.dw != nullptr && p.gates != 1) {
+    const ColSumArgs c2{q, static_cast<int>(p.gates), a.d, nullptr, nullptr, nullptr, a.dw};
+    hipLaunchKernelGGL(block_colsum_kernel, dim3(cb, 1), dim3(1024), 0, s, c2);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -183,6 +183,88 @@ struct BwdArgs {
 // blocks; kt covers the last one.
 inline long long wgrad8_kt(long long R, int n_groups) { return 128 * ((R + 127) / 128 + 2LL * n_groups + 1); }
 
+// The norm before a block (block.hip).  Null where not wanted: rstd, codes and
+// scales (the checkpoint of x).
+struct BlockInArgs {
+  const void* x;          // [T][d] x_fmt
+  const float* w;         // [d]
+  int T, d, x_fmt, n_fmt;
+  float eps;
+  void* n;                // [T][d] n_fmt
+  float* rstd;            // [T]
+  uint8_t* codes;         // [T][d]
+  float* scales;          // [T][d/128]
+};
+
+// The norm, gate and residual after a block, and the next block's norm.
+struct BlockOutArgs {
+  const void* x;          // [T][d] x_fmt
+  const void* y;          // [T][d] y_fmt
+  const void* skip;       // [T][d] n_fmt, or null: nothing to subtract
+  const float* w;         // [d], or null: no norm
+  const float* gate;      // [ceil(T / gate_rows)][d] (gate_rows 0: one row), or null: ones
+  const float* w_next;    // [d], or null: no next norm
+  int T, d, x_fmt, n_fmt, y_fmt, gate_rows;
+  float eps, res_scale;
+  void* x_out;            // [T][d] x_fmt
+  void* n_next;           // [T][d] n_fmt (with w_next)
+  float* rstd;            // the rest: null where not wanted
+  uint8_t* codes;         // checkpoint of y - skip
+  float* scales;
+  float* rstd_next;
+  uint8_t* codes_next;    // checkpoint of x_out
+  float* scales_next;
+};
+
+// The backward of either: dv = d(v r w) for g, dw, dgate.
+struct BlockBwdArgs {
+  const float* g;         // [T][d] upstream
+  const float* g_sub;     // [T][d] subtracted from g, or null
+  const float* res;       // [T][d]: dv += res_scale * res, or null
+  const void* v;          // [T][d] v_fmt rows, or null (codes; or neither norm nor gate)
+  const void* skip;       // [T][d] skip_fmt subtracted from v, or null
+  const uint8_t* codes;   // [T][d] checkpoint of v (read where v is null)
+  const float* scales;    // [T][d/128]
+  const float* w;         // [d], or null: no norm
+  const float* gate;      // [gates][d], or null: ones
+  const float* rstd;      // [T] (with w)
+  int T, d, v_fmt, skip_fmt;
+  long long gate_len;     // rows per gate (>= 1)
+  long long gates;
+  float res_scale;
+  float* dv;              // [T][d]
+  float* dw;              // [d], or null
+  float* dgate;           // [gates][d], or null
+  float* part;            // block_bwd_floats(...) of scratch
+  // set by the launcher (block_bwd_plan)
+  int whole_gates, runs;
+};
+
+// Rows a backward block takes: each block leaves one row of partial column
+// sums (d floats), so 16 rows keep that traffic near a tenth of the rows' own.
+constexpr int BLOCK_BWD_ROWS = 16;
+struct BlockBwdPlan {
+  int whole_gates;        // gates of at most BLOCK_BWD_ROWS rows, whole ones to a block
+  int runs;               // else: blocks per gate
+  long long gates, blocks;
+};
+inline BlockBwdPlan block_bwd_plan(long long T, long long gate_len, long long gates, bool has_gate) {
+  BlockBwdPlan p{};
+  p.gates = gates;
+  p.whole_gates = has_gate && T > 0 && gate_len <= BLOCK_BWD_ROWS;
+  if (p.whole_gates) {
+    const long long n = gate_len * (BLOCK_BWD_ROWS / gate_len);
+    p.blocks = (T + n - 1) / n;
+  } else {
+    p.runs = static_cast<int>((gate_len + BLOCK_BWD_ROWS - 1) / BLOCK_BWD_ROWS);
+    p.blocks = gates * p.runs;
+  }
+  return p;
+}
+inline long long block_bwd_floats(const BlockBwdPlan& p, int d) {
+  return (p.blocks + (!p.whole_gates && p.gates != 1 ? p.gates : 0)) * d;
+}
+
 hipError_t launch_route(int fmt, const RouteArgs& a, hipStream_t s);
 // The backward in six stages, launched in order 0..5: prep and dz; Dgrad of
 // the down GEMM (with the SwiGLU backward); Dgrad of the gate/up GEMM; Wgrad
@@ -197,17 +279,21 @@ hipError_t launch_bias_update(float* bias, const int32_t* counts, int n_routed, 
                               hipStream_t s);
 hipError_t launch_gateup(int fmt, const GateUpArgs& a, hipStream_t s);
 hipError_t launch_down(int fmt, const DownArgs& a, hipStream_t s);
+hipError_t launch_block_in(const BlockInArgs& a, hipStream_t s);
+hipError_t launch_block_out(const BlockOutArgs& a, hipStream_t s);
+hipError_t launch_block_bwd(BlockBwdArgs a, hipStream_t s);
 hipError_t launch_combine(int xfmt, int yfmt, int ofmt, const CombineArgs& a, hipStream_t s);
 
 #ifdef MOE_DEBUG
 // Debug build: each kernel file's first failed index check (0: none), cleared
 // when read; -1 if it could not be read.  Check ids: 1xx route, 2xx group,
-// 3xx grouped GEMMs, 4xx combine, 5xx backward.
+// 3xx grouped GEMMs, 4xx combine, 5xx backward, 6xx block norms.
 int debug_take_route();
 int debug_take_group();
 int debug_take_ggemm();
 int debug_take_combine();
 int debug_take_bwd();
+int debug_take_block();
 #endif
 
 // Tile rows of the grouped GEMMs for a weight format (m-tiles hold at most this many rows).

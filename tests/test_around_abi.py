@@ -1,0 +1,92 @@
+"""Argument checks of the entry points around the layer, on the CPU: every
+call here is refused before any GPU work."""
+
+import ctypes
+
+import pytest
+
+import mixture_experts_layer_deepseekmoe_amd as moe
+from mixture_experts_layer_deepseekmoe_amd import binding as B
+
+FAKE = 1 << 20   # 16-byte aligned, never dereferenced
+BAD = FAKE + 4
+
+
+def _bs(**kw):
+    return moe.BlockShape(**{**dict(T=5, d=256), **kw})
+
+
+def _block_ws(shape):
+    n = ctypes.c_size_t(0)
+    return moe.load_library().moe_block_workspace_size(ctypes.byref(shape.c()), ctypes.byref(n)), n.value
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(), B.MOE_OK),
+    (dict(T=0), B.MOE_OK),
+    (dict(T=-1), B.MOE_ERR_INVALID_ARG),
+    (dict(d=0), B.MOE_ERR_INVALID_ARG),
+    (dict(gate_rows=-1), B.MOE_ERR_INVALID_ARG),
+    (dict(eps=0.0), B.MOE_ERR_INVALID_ARG),
+    (dict(eps=float("nan")), B.MOE_ERR_INVALID_ARG),
+    (dict(eps=float("inf")), B.MOE_ERR_INVALID_ARG),
+    (dict(res_scale=float("inf")), B.MOE_ERR_INVALID_ARG),
+    (dict(x_dtype="e4m3"), B.MOE_ERR_INVALID_ARG),
+    (dict(n_dtype="e4m3"), B.MOE_ERR_INVALID_ARG),
+    (dict(y_dtype="e4m3"), B.MOE_ERR_INVALID_ARG),
+    (dict(d=252), B.MOE_ERR_UNSUPPORTED),
+    (dict(d=32776), B.MOE_ERR_UNSUPPORTED),
+    (dict(d=32768), B.MOE_OK),
+    (dict(T=1 << 22), B.MOE_ERR_UNSUPPORTED),
+])
+def test_block_shape_validation(kw, code):
+    assert _block_ws(_bs(**kw))[0] == code
+
+
+def test_block_workspace_covers_every_gating():
+    # one row of fp32 sums per 16 rows; per gate where gates are longer than that
+    for T, gr, rows in [(1, 0, 1), (160, 0, 10), (161, 0, 11), (160, 1, 10), (160, 5, 11), (160, 40, 4 * 3 + 4)]:
+        rc, n = _block_ws(_bs(T=T, gate_rows=gr))
+        assert rc == 0 and n >= rows * 256 * 4, (T, gr, n)
+
+
+def test_block_forward_refusals():
+    lib, sh = moe.load_library(), _bs().c()
+    r, bad = ctypes.byref, B.MOE_ERR_INVALID_ARG
+    assert lib.moe_block_in(None, FAKE, FAKE, FAKE, None, None) == bad
+    for args in [(None, FAKE, FAKE), (FAKE, None, FAKE), (FAKE, FAKE, None), (BAD, FAKE, FAKE), (FAKE, BAD, FAKE),
+                 (FAKE, FAKE, BAD)]:
+        assert lib.moe_block_in(r(sh), *args, None, None) == bad
+    half = B.CBlockSave(FAKE, FAKE, None)   # codes without scales
+    assert lib.moe_block_in(r(sh), FAKE, FAKE, FAKE, r(half), None) == bad
+    odd = _bs(d=264).c()                    # a checkpoint takes whole 128-column tiles
+    assert lib.moe_block_in(r(odd), FAKE, FAKE, FAKE, r(B.CBlockSave(FAKE, FAKE, FAKE)), None) == B.MOE_ERR_UNSUPPORTED
+    out = lambda x=FAKE, y=FAKE, skip=None, w=FAKE, gate=None, wn=None, xo=FAKE, nn=None, s=None, sn=None: lib.moe_block_out(  # noqa: E731,E501
+        r(sh), x, y, skip, w, gate, wn, xo, nn, s, sn, None)
+    for kw in (dict(x=None), dict(y=None), dict(xo=None), dict(skip=BAD), dict(w=BAD), dict(gate=BAD),
+               dict(wn=FAKE), dict(wn=BAD, nn=FAKE), dict(sn=r(B.CBlockSave(FAKE, None, None))), dict(s=r(half))):
+        assert out(**kw) == bad, kw
+
+
+def test_block_backward_refusals():
+    lib, shape = moe.load_library(), _bs()
+    sh, r, bad = shape.c(), ctypes.byref, B.MOE_ERR_INVALID_ARG
+    need = _block_ws(shape)[1]
+    save, empty = B.CBlockSave(FAKE, FAKE, FAKE), B.CBlockSave(FAKE, None, None)
+
+    def b_in(dn=FAKE, sub=None, do=None, x=FAKE, w=FAKE, s=save, dx=FAKE, dw=FAKE, ws=FAKE, n=need):
+        return lib.moe_block_in_backward(r(sh), dn, sub, do, x, w, None if s is None else r(s), dx, dw, ws, n, None)
+
+    for kw in (dict(dn=None), dict(dx=None), dict(dw=None), dict(w=None), dict(sub=BAD), dict(do=BAD), dict(s=None),
+               dict(s=B.CBlockSave(None, FAKE, FAKE)), dict(x=None, s=empty)):
+        assert b_in(**kw) == bad, kw
+    assert b_in(ws=None) == B.MOE_ERR_WORKSPACE and b_in(n=need - 1) == B.MOE_ERR_WORKSPACE
+
+    def b_out(do=FAKE, y=FAKE, skip=None, w=FAKE, gate=FAKE, s=save, dy=FAKE, dw=FAKE, dg=FAKE, ws=FAKE, n=need):
+        return lib.moe_block_out_backward(r(sh), do, y, skip, w, gate, None if s is None else r(s), dy, dw, dg, ws, n,
+                                          None)
+
+    for kw in (dict(do=None), dict(dy=None), dict(dw=None), dict(dg=None), dict(w=None), dict(gate=None), dict(s=None),
+               dict(y=None, s=empty), dict(y=None, skip=FAKE), dict(skip=BAD), dict(gate=BAD), dict(y=BAD)):
+        assert b_out(**kw) == bad, kw
+    assert b_out(ws=None) == B.MOE_ERR_WORKSPACE and b_out(n=need - 1) == B.MOE_ERR_WORKSPACE

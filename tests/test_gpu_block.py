@@ -1,0 +1,273 @@
+"""moe_block_in / moe_block_out and their backward on the GPU against the fp64
+oracle.
+
+Tolerances.  u16 = 2^-8 is the largest relative rounding of a bf16 store, E =
+2e-5 the bound on fp32 arithmetic relative to the sum of the terms' sizes: a
+sum of at most 32768 squares in the kernel's tree has at most about 4 x 8 + 6 + 16 + 3
+roundings on a path (57 x 2^-24 = 3.4e-6), as has the mean in the backward,
+and at most ten roundings more follow; the column sums add at most 16 rows in
+a block and ceil(n / 64) + 64 partial rows (n <= 64 here: 81 roundings, 4.8e-6).
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_layer_deepseekmoe_amd as moe
+from oracle import around_oracle as A
+from tests.parity import say
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+U16, E = 2.0 ** -8, 2e-5
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def _make(seed, T, d, dtype="f32", scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    ch = torch.exp(0.7 * torch.randn(d, generator=g))
+    return (scale * ch * torch.randn((T, d), generator=g)).to(DT[dtype])
+
+
+def _np(t):
+    return None if t is None else t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def _dev(t):
+    return None if t is None else t.to(DEV)
+
+
+def _close(got, ref, size, dtype="f32"):
+    """|got - ref| <= E * size + the store's rounding."""
+    got = _np(got)
+    u = U16 if dtype == "bf16" else 2.0 ** -24
+    assert got.shape == ref.shape and np.isfinite(got).all()
+    over = np.abs(got - ref) - (E * size + u * np.abs(ref) + 1e-30)
+    assert over.max(initial=-1.0) <= 0, float(over.max())
+
+
+# T, d: one token, odd row counts about the backward's 16-row runs, widths at
+# and just past each row shape's limit (2048, 4096, 8192, 32768) and not
+# multiples of anything but 8
+SIZES = [(1, 8), (1, 2048), (3, 72), (16, 2056), (17, 4096), (33, 4104), (5, 8192), (2, 8200), (2, 32768), (129, 1000)]
+
+
+@pytest.mark.parametrize("T,d", SIZES)
+@pytest.mark.parametrize("x_dtype,n_dtype", [("bf16", "bf16"), ("f32", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+def test_block_in(T, d, x_dtype, n_dtype):
+    say(f"case: block_in T={T} d={d} {x_dtype}->{n_dtype}")
+    shape = moe.BlockShape(T, d, x_dtype=x_dtype, n_dtype=n_dtype, eps=1e-5, res_scale=0.75)
+    x, w = _make(1, T, d, x_dtype), 1 + 0.2 * _make(2, 1, d)[0]
+    save = moe.alloc_block_save(shape)
+    n = moe.moe_block_in(shape, _dev(x), _dev(w), save=save)
+    ref = A.block_in(_np(x), _np(w), 1e-5)
+    r = A.rstd(_np(x), 1e-5)
+    _close(n, ref, np.abs(ref), n_dtype)
+    _close(save.rstd, r, r)
+    # backward, alone and chained
+    dn, sub, do = _make(3, T, d), _make(4, T, d, scale=0.3), _make(5, T, d)
+    for s, o in ((None, None), (sub, do)):
+        dx, dw = moe.moe_block_in_backward(shape, _dev(dn), _dev(w), save, x=_dev(x), dn_sub=_dev(s), do=_dev(o))
+        rx, rw, sx, sw = A.block_in_backward(_np(dn), _np(s), _np(o), _np(x), _np(w), r, 0.75)
+        g = np.abs(_np(dn)) + (0 if s is None else np.abs(_np(s)))   # dn - dn_sub is rounded once
+        _close(dx, rx, sx + r[:, None] * g * np.abs(_np(w)))
+        _close(dw, rw, sw + (g * np.abs(_np(x)) * r[:, None]).sum(axis=0))
+
+
+OUT_CASES = [  # T, d, x, n, y, gate_rows (None: no gate), norm, skip, next
+    (1, 8, "bf16", "bf16", "f32", 0, True, True, True),
+    (1, 7168, "bf16", "bf16", "bf16", 0, True, True, True),
+    (37, 264, "f32", "bf16", "f32", 1, True, False, True),
+    (37, 264, "bf16", "f32", "bf16", 1, True, True, False),
+    (50, 1000, "bf16", "bf16", "f32", 5, True, True, True),
+    (50, 1000, "f32", "f32", "bf16", 16, True, True, True),
+    (50, 1000, "f32", "f32", "f32", 17, True, False, False),
+    (67, 2056, "bf16", "bf16", "f32", 40, False, True, True),
+    (67, 2056, "f32", "bf16", "bf16", None, True, True, True),
+    (16, 520, "bf16", "bf16", "f32", None, True, False, False),
+    (33, 520, "bf16", "bf16", "f32", 100, True, False, False),
+    (20, 4104, "bf16", "bf16", "f32", None, False, True, False),
+    (3, 8200, "bf16", "bf16", "f32", 2, True, True, True),
+]
+
+
+@pytest.mark.parametrize("case", OUT_CASES, ids=[f"{c[0]}x{c[1]}g{c[5]}" for c in OUT_CASES])
+def test_block_out(case):
+    T, d, xd, nd, yd, gr, norm, skip, nxt = case
+    say(f"case: block_out {case}")
+    shape = moe.BlockShape(T, d, x_dtype=xd, n_dtype=nd, y_dtype=yd, gate_rows=gr or 0, eps=1e-5, res_scale=0.9)
+    x, y = _make(1, T, d, xd), _make(2, T, d, yd)
+    sk = _make(3, T, d, nd, 0.5) if skip else None
+    w = 1 + 0.2 * _make(4, 1, d)[0] if norm else None
+    gate = 0.5 * _make(5, shape.gates, d) if gr is not None else None
+    wn = 1 + 0.2 * _make(6, 1, d)[0] if nxt else None
+    save, save_next = moe.alloc_block_save(shape), moe.alloc_block_save(shape) if nxt else None
+    xo, nn = moe.moe_block_out(shape, _dev(x), _dev(y), w=_dev(w), gate=_dev(gate), skip=_dev(sk), w_next=_dev(wn),
+                               save=save, save_next=save_next)
+    ref, zn = A.block_out(_np(x), _np(y), _np(sk), _np(w), _np(gate), gr or 0, 1e-5, 0.9)
+    gt = np.abs(A.gate_rows_of(_np(gate), T, d, gr or 0))
+    # y - skip is rounded once: its error is relative to both
+    z = _np(y) - (0 if sk is None else _np(sk))
+    zs = np.abs(_np(y)) + (0 if sk is None else np.abs(_np(sk)))
+    rz = A.rstd(z, 1e-5)
+    zsize = zs if w is None else zs * rz[:, None] * np.abs(_np(w))
+    _close(xo, ref, np.abs(0.9 * _np(x)) + gt * zsize, xd)
+    if nxt:
+        nref = A.block_in(_np(xo), _np(wn), 1e-5)   # from x_out as stored
+        _close(nn, nref, np.abs(nref), nd)
+        # and bit for bit what moe_block_in gives on x_out
+        s2 = moe.alloc_block_save(shape)
+        assert torch.equal(nn, moe.moe_block_in(shape, xo, _dev(wn), save=s2)) and torch.equal(s2.rstd, save_next.rstd)
+    do = _make(7, T, d)
+    dy, dw, dgate = moe.moe_block_out_backward(shape, _dev(do), save, w=_dev(w), gate=_dev(gate), y=_dev(y), skip=_dev(sk))
+    ry, rw, rg, sy, _, _ = A.block_out_backward(_np(do), z, _np(w), _np(gate), gr or 0, rz)
+    term = np.abs(_np(do)) * zs * (rz[:, None] if norm else 1)
+    a = np.abs(_np(do)) * gt * (np.abs(_np(w)) if norm else 1)
+    if norm:   # the sizes with the rounding of y - skip
+        sy = sy + rz[:, None] * zs * rz[:, None] * (a * zs * rz[:, None]).mean(axis=1, keepdims=True)
+    _close(dy, ry, sy)
+    if norm:
+        _close(dw, rw, (term * gt).sum(axis=0))
+    else:
+        assert dw is None
+    if gate is None:
+        assert dgate is None
+    else:
+        sg = np.zeros_like(rg)
+        np.add.at(sg, np.arange(T) // (gr or T), term * (np.abs(_np(w)) if norm else 1))
+        _close(dgate, rg, sg)
+
+
+@pytest.mark.parametrize("T,d,y_dtype,skip", [(1, 128, "f32", True), (19, 1152, "bf16", False), (40, 4224, "f32", True),
+                                              (3, 8320, "f32", False)])
+def test_checkpoints(T, d, y_dtype, skip):
+    """Codes and scales bit for bit, and the backward reads what they stand for."""
+    say(f"case: block checkpoints T={T} d={d} {y_dtype}")
+    shape = moe.BlockShape(T, d, y_dtype=y_dtype, gate_rows=0, eps=1e-5)
+    x, y, sk = _make(1, T, d, "bf16"), _make(2, T, d, y_dtype), _make(3, T, d, "bf16") if skip else None
+    y[0, :128] = 0
+    if skip:
+        sk[0, :128] = 0   # an all-zero tile of z
+    w, wn, gate = 1 + 0.2 * _make(4, 1, d)[0], 1 + 0.2 * _make(5, 1, d)[0], 0.5 * _make(6, 1, d)
+    s0, s1, s2 = (moe.alloc_block_save(shape, e4m3=True) for _ in range(3))
+    moe.moe_block_in(shape, _dev(x), _dev(w), save=s0)
+    xo, _ = moe.moe_block_out(shape, _dev(x), _dev(y), w=_dev(w), gate=_dev(gate), skip=_dev(sk), w_next=_dev(wn), save=s1,
+                              save_next=s2)
+    z = (y.float() - (0 if sk is None else sk.float())).numpy()   # fp32, as the kernel forms it
+    vals = []
+    for s, v in ((s0, x.float().numpy()), (s1, z), (s2, xo.float().cpu().numpy())):
+        c, sc, val = A.checkpoint(v)
+        assert (s.codes.cpu().numpy() == c).all() and (s.scales.cpu().numpy() == sc).all()
+        vals.append(val)
+    do = _make(7, T, d)
+    dx, dw = moe.moe_block_in_backward(shape, _dev(do), _dev(w), s0)
+    rx, rw, sx, sw = A.block_in_backward(_np(do), None, None, vals[0], _np(w), A.rstd(_np(x), 1e-5), 1.0)
+    _close(dx, rx, sx)
+    _close(dw, rw, sw)
+    dy, dw, dgate = moe.moe_block_out_backward(shape, _dev(do), s1, w=_dev(w), gate=_dev(gate))
+    ry, rw, rg, sy, sw, sg = A.block_out_backward(_np(do), vals[1], _np(w), _np(gate), 0, A.rstd(z, 1e-5))
+    _close(dy, ry, sy)
+    _close(dw, rw, sw)
+    _close(dgate, rg, sg)
+
+
+def test_backward_is_the_difference_quotient():
+    """<dx, v>, <dw, u>, <dgate, q>, <dy, v> against central differences of the
+    GPU's own fp32 forward.  f is a sum of T d products of relative error E at
+    most; with a step h along unit-size directions the quotient's error is at
+    most E * sum |terms| / h plus the third-order term, h^2 times at most
+    sum |terms|."""
+    say("case: block backward against differences")
+    T, d, h = 9, 264, 2e-2
+    shape = moe.BlockShape(T, d, x_dtype="f32", n_dtype="f32", y_dtype="f32", gate_rows=4, eps=1e-2, res_scale=0.8)
+    rn = lambda s, *sz: torch.randn(sz, generator=torch.Generator().manual_seed(s)).to(DEV)  # noqa: E731
+    x, y, do, dn = rn(1, T, d), rn(2, T, d), rn(3, T, d), rn(4, T, d)
+    w, wn, gate = 1 + 0.2 * rn(5, d), 1 + 0.2 * rn(6, d), 0.5 * rn(7, shape.gates, d)
+
+    def f(x, y, w, gate, wn):
+        xo, n = moe.moe_block_out(shape, x, y, w=w, gate=gate, w_next=wn)
+        return float((xo.double() * do.double()).sum() + (n.double() * dn.double()).sum())
+
+    s, sn = moe.alloc_block_save(shape), moe.alloc_block_save(shape)
+    xo, n = moe.moe_block_out(shape, x, y, w=w, gate=gate, w_next=wn, save=s, save_next=sn)
+    size = float((xo * do).abs().sum() + (n * dn).abs().sum())
+    one = moe.BlockShape(T, d, x_dtype="f32", n_dtype="f32", y_dtype="f32", eps=1e-2, res_scale=1.0)
+    dxo, dwn = moe.moe_block_in_backward(one, dn, wn, sn, x=xo, do=do)
+    dy, dw, dgate = moe.moe_block_out_backward(shape, dxo, s, w=w, gate=gate, y=y)
+    args = dict(x=x, y=y, w=w, gate=gate, wn=wn)
+    grads = dict(x=0.8 * dxo, y=dy, w=dw, gate=dgate, wn=dwn)
+    for k in args:
+        v = rn(20 + len(k) + ord(k[0]), *args[k].shape)
+        num = (f(**{**args, k: args[k] + h * v}) - f(**{**args, k: args[k] - h * v})) / (2 * h)
+        ana = float((grads[k].double() * v.double()).sum())
+        assert abs(num - ana) <= size * (E / h + h * h), (k, num, ana, size)
+
+
+def test_block_zero_rows_and_in_place():
+    say("case: block ops on no rows, and in place")
+    d = 256
+    for gr in (0, 3):
+        shape = moe.BlockShape(0, d, gate_rows=gr)
+        e = lambda dt: torch.empty((0, d), dtype=dt, device=DEV)  # noqa: E731
+        w = torch.ones(d, device=DEV)
+        gate = torch.ones((shape.gates, d), device=DEV)
+        save = moe.alloc_block_save(shape, e4m3=True)
+        assert moe.moe_block_in(shape, e(torch.bfloat16), w, save=save).shape == (0, d)
+        dx, dw = moe.moe_block_in_backward(shape, e(torch.float32), w, save)
+        assert dx.shape == (0, d) and (dw == 0).all()
+        moe.moe_block_out(shape, e(torch.bfloat16), e(torch.float32), w=w, gate=gate, save=save)
+        dy, dw, dgate = moe.moe_block_out_backward(shape, e(torch.float32), save, w=w, gate=gate)
+        assert (dw == 0).all() and (dgate == 0).all() and dgate.shape == gate.shape
+    # an all-zero row: r = eps^(-1/2), n = 0; in place x_out = x
+    shape = moe.BlockShape(2, d)
+    x = torch.zeros((2, d), dtype=torch.bfloat16, device=DEV)
+    x[1] = 3
+    y = torch.randn((2, d), device=DEV)
+    w = torch.ones(d, device=DEV)
+    n = moe.moe_block_in(shape, x, w)
+    assert (n[0] == 0).all() and (n[1] == 1).all()
+    want, _ = moe.moe_block_out(shape, x, y, w=w)
+    got, _ = moe.moe_block_out(shape, x, y, w=w, x_out=x)
+    assert got.data_ptr() == x.data_ptr() and torch.equal(want, got)
+
+
+def test_block_repeats_and_streams():
+    """Bit-identical repeats, and the same on a side stream."""
+    say("case: block repeats")
+    T, d = 300, 1024
+    shape = moe.BlockShape(T, d, gate_rows=70)
+    x, y = _make(1, T, d, "bf16").to(DEV), _make(2, T, d).to(DEV)
+    w, gate, do = torch.ones(d, device=DEV), _make(3, shape.gates, d).to(DEV), _make(4, T, d).to(DEV)
+
+    def step():
+        save = moe.alloc_block_save(shape, e4m3=True)
+        xo, nn = moe.moe_block_out(shape, x, y, w=w, gate=gate, w_next=w, save=save)
+        return (xo, nn, save.codes) + moe.moe_block_out_backward(shape, do, save, w=w, gate=gate)
+
+    first = step()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        second = step()
+    side.synchronize()
+    third = step()
+    for a, b, c in zip(first, second, third):
+        assert torch.equal(a, b) and torch.equal(a, c)
+
+
+def test_block_binding_refuses():
+    shape = moe.BlockShape(4, 256)
+    x = torch.zeros((4, 256), dtype=torch.bfloat16, device=DEV)
+    w = torch.ones(256, device=DEV)
+    with pytest.raises(ValueError):
+        moe.moe_block_in(shape, x.float(), w)                      # not x_dtype
+    with pytest.raises(ValueError):
+        moe.moe_block_in(shape, x[:3], w)                          # not T rows
+    with pytest.raises(ValueError):
+        moe.moe_block_in(shape, x.t().contiguous().t(), w)         # strided
+    with pytest.raises(ValueError):
+        moe.moe_block_in(shape, x.cpu(), w)
+    with pytest.raises(moe.MoEError):
+        moe.moe_block_in_backward(shape, x.float(), w, moe.BlockSave())   # no rows, no checkpoint
+    with pytest.raises(moe.MoEError):
+        moe.moe_block_in(moe.BlockShape(4, 250), x[:, :250].contiguous(), w[:250].contiguous())
