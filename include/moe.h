@@ -393,6 +393,42 @@ int moe_block_out_backward(const moe_block_shape* shape, const float* dout, cons
                            float* dgate, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
+ * Cross entropy over a vocabulary, without keeping the logits l = h w^T:
+ *   lse_t  = log sum_v exp l_tv
+ *   loss_t = lse_t - l_t,label
+ * for hidden rows h [T][d] and a vocabulary matrix w [V][d], both bf16, and
+ * labels [T].  A token whose label lies outside [0, V) (-100, say) is ignored:
+ * its loss, lse and row of dh are zero, it adds nothing to dw, its row of h is
+ * not read, and it costs nothing.  T of 1 scores a single token.
+ *
+ * moe_vocab_loss: loss, lse [T] fp32.
+ * moe_vocab_loss_backward: for dloss and dlse [T] fp32, the gradients of loss
+ *   and of lse (dlse null: zero; it is what a penalty on lse needs), and the lse
+ *   of the forward:
+ *     G_tv = (dloss_t + dlse_t) exp(l_tv - lse_t) - dloss_t [v = label_t]
+ *     dh   = G w    [T][d] in dh_dtype (F32 or BF16)
+ *     dw   = G^T h  [V][d] in dw_dtype; overwritten, not added to
+ *   The logits are computed again, in pieces of the vocabulary; a piece of G
+ *   (at most 512 MB but for very long batches, bf16: the operand of the two
+ *   products) and fp32 sums of dh live in the workspace.
+ * Products are bf16 with fp32 accumulation; every sum runs in a fixed order
+ * (bit-reproducible).  The forward and the backward may use different
+ * workspaces.
+ * Limits: d a multiple of 64, at most 32768; V at most 2^24; T below 2^22,
+ * (T + 64) * d * 2 below 2^32, ceil(T/256) * ceil(V/256) below about 5.5 million.
+ */
+typedef struct {
+  int32_t T, d, V;
+  int32_t dh_dtype, dw_dtype;
+} moe_loss_shape;
+int moe_vocab_loss_workspace_size(const moe_loss_shape* shape, size_t* forward_bytes, size_t* backward_bytes);
+int moe_vocab_loss(const moe_loss_shape* shape, const void* h, const void* w, const int32_t* labels, float* loss,
+                   float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream);
+int moe_vocab_loss_backward(const moe_loss_shape* shape, const void* h, const void* w, const int32_t* labels,
+                            const float* lse, const float* dloss, const float* dlse, void* dh, void* dw,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
  * Aux-loss-free bias update (xyznot summary, section 2: b_i is lowered by
  * gamma for an overloaded expert and raised by gamma for an underloaded one),
  * in place:

@@ -9,6 +9,7 @@ from .binding import (  # noqa: F401
     BlockShape,
     ExpertWeights,
     LayerShape,
+    LossShape,
     MoEError,
     alloc_block_save,
     alloc_routing,
@@ -17,6 +18,7 @@ from .binding import (  # noqa: F401
     alloc_workspace,
     block_workspace_size,
     load_library,
+    loss_workspace_size,
     moe_block_in,
     moe_block_in_backward,
     moe_block_out,
@@ -29,6 +31,8 @@ from .binding import (  # noqa: F401
     moe_quantize_weight_e4m3,
     moe_route,
     moe_update_bias,
+    moe_vocab_loss,
+    moe_vocab_loss_backward,
     prepare_weights,
     status_str,
     version,

@@ -31,7 +31,7 @@ EXPORTED = ("moe_status_str", "moe_version", "moe_workspace_size", "moe_workspac
             "moe_forward", "moe_forward_static", "moe_train_workspace_size", "moe_forward_train", "moe_backward",
             "moe_update_bias", "moe_quantize_weight_e4m3", "moe_quantize_act_e4m3",
             "moe_block_in", "moe_block_out", "moe_block_workspace_size", "moe_block_in_backward",
-            "moe_block_out_backward")
+            "moe_block_out_backward", "moe_vocab_loss_workspace_size", "moe_vocab_loss", "moe_vocab_loss_backward")
 
 STATIC_SCRATCH_BYTES = 64 << 20   # MOE_STATIC_SCRATCH_BYTES
 
@@ -85,6 +85,10 @@ class Routing(ctypes.Structure):
 class CBlockShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "d", "x_dtype", "n_dtype", "y_dtype", "gate_rows")] + \
                [(n, ctypes.c_float) for n in ("eps", "res_scale")]
+
+
+class CLossShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "d", "V", "dh_dtype", "dw_dtype")]
 
 
 class CBlockSave(ctypes.Structure):
@@ -165,6 +169,13 @@ def _open(path: str) -> ctypes.CDLL:
     lib.moe_block_in_backward.argtypes = [bs, vp, vp, vp, vp, vp, bk, vp, vp, vp, sz, vp]
     lib.moe_block_out_backward.restype = ctypes.c_int
     lib.moe_block_out_backward.argtypes = [bs, vp, vp, vp, vp, vp, bk, vp, vp, vp, vp, sz, vp]
+    ls, szp = ctypes.POINTER(CLossShape), ctypes.POINTER(sz)
+    lib.moe_vocab_loss_workspace_size.restype = ctypes.c_int
+    lib.moe_vocab_loss_workspace_size.argtypes = [ls, szp, szp]
+    lib.moe_vocab_loss.restype = ctypes.c_int
+    lib.moe_vocab_loss.argtypes = [ls, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_vocab_loss_backward.restype = ctypes.c_int
+    lib.moe_vocab_loss_backward.argtypes = [ls, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     return lib
 
 
@@ -547,6 +558,73 @@ def moe_block_out_backward(shape: BlockShape, do: torch.Tensor, save: Optional[B
         _ref(_save_struct(shape, save)), _ptr(dy), _ptr(dw), _ptr(dgate), _ptr(ws), ws.numel(), _stream())
     _check(rc, "moe_block_out_backward")
     return dy, dw, dgate
+
+
+# ---------------------------------------------------------------- cross entropy over a vocabulary
+
+
+@dataclass
+class LossShape:
+    """Cross entropy of T hidden rows of d columns over V entries
+    (moe_loss_shape); dh_dtype and dw_dtype: "f32" or "bf16"."""
+    T: int
+    d: int
+    V: int
+    dh_dtype: str = "f32"
+    dw_dtype: str = "f32"
+
+    def c(self) -> CLossShape:
+        return CLossShape(self.T, self.d, self.V, DTYPE_CODE[self.dh_dtype], DTYPE_CODE[self.dw_dtype])
+
+
+def loss_workspace_size(shape: LossShape, backward: bool = False) -> int:
+    f, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(load_library().moe_vocab_loss_workspace_size(ctypes.byref(shape.c()), ctypes.byref(f), ctypes.byref(b)),
+           "moe_vocab_loss_workspace_size")
+    return b.value if backward else f.value
+
+
+def _loss_workspace(shape: LossShape, backward: bool, workspace: Optional[torch.Tensor], device) -> torch.Tensor:
+    if workspace is not None:
+        return workspace
+    return torch.empty(max(loss_workspace_size(shape, backward), 1), dtype=torch.uint8, device=device)
+
+
+def moe_vocab_loss(shape: LossShape, h: torch.Tensor, w: torch.Tensor, labels: torch.Tensor,
+                   workspace: Optional[torch.Tensor] = None):
+    """Per-token cross entropy of bf16 rows ``h`` [T, d] over the bf16 vocabulary
+    matrix ``w`` [V, d], without keeping the logits.  Returns (loss, lse), fp32
+    [T]; tokens whose int32 label lies outside [0, V) are ignored (zeros)."""
+    T, d, V = shape.T, shape.d, shape.V
+    loss = torch.empty((T,), dtype=torch.float32, device=h.device)
+    lse = torch.empty((T,), dtype=torch.float32, device=h.device)
+    ws = _loss_workspace(shape, False, workspace, h.device)
+    rc = load_library().moe_vocab_loss(ctypes.byref(shape.c()), _arg(h, "h", "bf16", T, d), _arg(w, "w", "bf16", V, d),
+                                       _arg(labels, "labels", "i32", T), _ptr(loss), _ptr(lse), _ptr(ws), ws.numel(),
+                                       _stream())
+    _check(rc, "moe_vocab_loss")
+    return loss, lse
+
+
+def moe_vocab_loss_backward(shape: LossShape, h: torch.Tensor, w: torch.Tensor, labels: torch.Tensor,
+                            lse: torch.Tensor, dloss: torch.Tensor, dlse: Optional[torch.Tensor] = None,
+                            dh: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None):
+    """(dh, dw) for the per-token gradients ``dloss`` of loss and ``dlse`` (or None)
+    of lse, with the forward's ``lse``."""
+    T, d, V = shape.T, shape.d, shape.V
+    if dh is None:
+        dh = torch.empty((T, d), dtype=_ARG_DT[shape.dh_dtype], device=h.device)
+    if dw is None:
+        dw = torch.empty((V, d), dtype=_ARG_DT[shape.dw_dtype], device=h.device)
+    ws = _loss_workspace(shape, True, workspace, h.device)
+    rc = load_library().moe_vocab_loss_backward(
+        ctypes.byref(shape.c()), _arg(h, "h", "bf16", T, d), _arg(w, "w", "bf16", V, d),
+        _arg(labels, "labels", "i32", T), _arg(lse, "lse", "f32", T), _arg(dloss, "dloss", "f32", T),
+        _arg(dlse, "dlse", "f32", T), _arg(dh, "dh", shape.dh_dtype, T, d), _arg(dw, "dw", shape.dw_dtype, V, d),
+        _ptr(ws), ws.numel(), _stream())
+    _check(rc, "moe_vocab_loss_backward")
+    return dh, dw
 
 
 def moe_update_bias(bias: torch.Tensor, counts: torch.Tensor, total_assignments: int, gamma: float = 0.001):

@@ -38,8 +38,8 @@ inline int check_launch(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ER
 inline int debug_status(int rc, hipStream_t st, const char* what) {
   if (rc != MOE_OK) return rc;
   if (hipStreamSynchronize(st) != hipSuccess) return MOE_ERR_LAUNCH;
-  const int flags[] = {debug_take_route(),   debug_take_group(), debug_take_ggemm(),
-                       debug_take_combine(), debug_take_bwd(),   debug_take_block()};
+  const int flags[] = {debug_take_route(), debug_take_group(), debug_take_ggemm(), debug_take_combine(),
+                       debug_take_bwd(),   debug_take_block(), debug_take_loss()};
   for (const int f : flags) {
     if (f != 0) {
       std::fprintf(stderr, "moe debug build: %s: index check %d failed\n", what, f);

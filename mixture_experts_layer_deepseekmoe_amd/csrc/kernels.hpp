@@ -265,6 +265,59 @@ inline long long block_bwd_floats(const BlockBwdPlan& p, int d) {
   return (p.blocks + (!p.whole_gates && p.gates != 1 ? p.gates : 0)) * d;
 }
 
+// Cross entropy over the vocabulary (loss.hip).  "Row" r is the r-th token with
+// a label in [0, V); the other tokens take no part.
+struct LossArgs {
+  const uint16_t* h;      // [T][d] bf16 hidden rows
+  const uint16_t* w;      // [V][d] bf16 vocabulary matrix
+  const int32_t* labels;  // [T]
+  int T, d, V;
+  int32_t* rows;          // [T] token of each row
+  int32_t* pos;           // [T] row of each token, or -1
+  int32_t* count;         // [1] rows
+  float* loss;            // [T] (forward)
+  float* lse;             // [T] (backward: read)
+  // forward
+  float2* part;           // [ceil(V / 256)][T] each tile's (max, sum exp(l - max)) by row
+  float* zlab;            // [T] the label's logit by row
+  // backward
+  const float* dloss;     // [T]
+  const float* dlse;      // [T], or null
+  uint16_t* hc;           // [T][d] the rows' hidden rows, one after the other
+  uint16_t* g;            // [T][ldg] a piece's G = dlogits
+  float* acc;             // [splits][T][d] dh by row
+  int ldg, splits;        // loss_plan(...)
+  int dh_fmt, dw_fmt;
+  void* dh;               // [T][d]
+  void* dw;               // [V][d]
+  // the piece of the vocabulary: columns v_first .. v_first + v_len - 1
+  int v_first, v_len;
+};
+
+constexpr int LOSS_TILE = 256;    // rows and columns of a tile
+
+// The backward's pieces of the vocabulary: as many whole tiles of columns as
+// keep G within LOSS_G_BYTES (and a piece of w within 2^31 bytes).
+constexpr long long LOSS_G_BYTES = 512LL << 20;
+inline int loss_piece(long long T, long long d, long long V) {
+  const long long vt = (V + LOSS_TILE - 1) / LOSS_TILE * LOSS_TILE;
+  long long n = LOSS_G_BYTES / (2 * (T > LOSS_TILE ? T : LOSS_TILE)) / LOSS_TILE * LOSS_TILE;
+  const long long nw = (1LL << 30) / d / LOSS_TILE * LOSS_TILE;
+  if (n > nw) n = nw;
+  if (n < LOSS_TILE) n = LOSS_TILE;
+  return static_cast<int>(n < vt ? n : vt);
+}
+
+// dh = G w sums over the whole piece: few rows make few tiles, so the piece is
+// cut into `splits` runs of columns with an fp32 copy of dh each.
+int loss_splits(long long T, long long d, long long piece);
+
+hipError_t launch_loss_rows(const LossArgs& a, hipStream_t s);
+hipError_t launch_loss_forward(const LossArgs& a, hipStream_t s);
+hipError_t launch_loss_gather(const LossArgs& a, hipStream_t s);
+hipError_t launch_loss_piece(const LossArgs& a, hipStream_t s);
+hipError_t launch_loss_dh(const LossArgs& a, hipStream_t s);
+
 hipError_t launch_route(int fmt, const RouteArgs& a, hipStream_t s);
 // The backward in six stages, launched in order 0..5: prep and dz; Dgrad of
 // the down GEMM (with the SwiGLU backward); Dgrad of the gate/up GEMM; Wgrad
@@ -287,13 +340,14 @@ hipError_t launch_combine(int xfmt, int yfmt, int ofmt, const CombineArgs& a, hi
 #ifdef MOE_DEBUG
 // Debug build: each kernel file's first failed index check (0: none), cleared
 // when read; -1 if it could not be read.  Check ids: 1xx route, 2xx group,
-// 3xx grouped GEMMs, 4xx combine, 5xx backward, 6xx block norms.
+// 3xx grouped GEMMs, 4xx combine, 5xx backward, 6xx block norms, 7xx loss.
 int debug_take_route();
 int debug_take_group();
 int debug_take_ggemm();
 int debug_take_combine();
 int debug_take_bwd();
 int debug_take_block();
+int debug_take_loss();
 #endif
 
 // Tile rows of the grouped GEMMs for a weight format (m-tiles hold at most this many rows).

@@ -90,3 +90,66 @@ def test_block_backward_refusals():
                dict(y=None, s=empty), dict(y=None, skip=FAKE), dict(skip=BAD), dict(gate=BAD), dict(y=BAD)):
         assert b_out(**kw) == bad, kw
     assert b_out(ws=None) == B.MOE_ERR_WORKSPACE and b_out(n=need - 1) == B.MOE_ERR_WORKSPACE
+
+
+# ---------------------------------------------------------------- cross entropy over a vocabulary
+
+
+def _loss_ws(**kw):
+    shape = moe.LossShape(**{**dict(T=100, d=128, V=1000), **kw})
+    f, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    rc = moe.load_library().moe_vocab_loss_workspace_size(ctypes.byref(shape.c()), ctypes.byref(f), ctypes.byref(b))
+    return rc, f.value, b.value
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(), B.MOE_OK),
+    (dict(T=0), B.MOE_OK),
+    (dict(V=1), B.MOE_OK),
+    (dict(dh_dtype="bf16", dw_dtype="bf16"), B.MOE_OK),
+    (dict(T=-1), B.MOE_ERR_INVALID_ARG),
+    (dict(d=0), B.MOE_ERR_INVALID_ARG),
+    (dict(V=0), B.MOE_ERR_INVALID_ARG),
+    (dict(dh_dtype="e4m3"), B.MOE_ERR_INVALID_ARG),
+    (dict(dw_dtype="e4m3"), B.MOE_ERR_INVALID_ARG),
+    (dict(d=96), B.MOE_ERR_UNSUPPORTED),
+    (dict(d=32832), B.MOE_ERR_UNSUPPORTED),
+    (dict(V=(1 << 24) + 1), B.MOE_ERR_UNSUPPORTED),
+    (dict(T=1 << 22, d=64), B.MOE_ERR_UNSUPPORTED),
+    (dict(T=299_530, d=7168, V=256), B.MOE_ERR_UNSUPPORTED),   # (T + 64) d 2 reaches 2^32
+    (dict(T=299_529, d=7168, V=256), B.MOE_OK),
+    (dict(T=(1 << 22) - 1, d=64, V=1 << 24), B.MOE_ERR_UNSUPPORTED),   # blocks of one launch
+])
+def test_loss_shape_validation(kw, code):
+    assert _loss_ws(**kw)[0] == code
+
+
+def test_loss_workspace_keeps_no_logits():
+    # T = 8192, d = 7168, V = 131072: 2 GB of bf16 logits; the backward holds a 512 MB piece,
+    # the rows (117 MB) and fp32 sums of dh (235 MB, twice: two splits fill the chip)
+    rc, f, b = _loss_ws(T=8192, d=7168, V=131072)
+    assert rc == 0 and f < 64 << 20 and b < (512 + 112 + 2 * 224 + 1) << 20
+    # G's piece is never wider than the vocabulary
+    assert _loss_ws(T=1, d=64, V=256)[2] < 1 << 20
+
+
+def test_loss_refusals():
+    lib, shape = moe.load_library(), moe.LossShape(100, 128, 1000)
+    sh, r, bad = shape.c(), ctypes.byref, B.MOE_ERR_INVALID_ARG
+    _, nf, nb = _loss_ws()
+
+    def fwd(h=FAKE, w=FAKE, lab=FAKE, loss=FAKE, lse=FAKE, ws=FAKE, n=nf):
+        return lib.moe_vocab_loss(r(sh), h, w, lab, loss, lse, ws, n, None)
+
+    for kw in (dict(h=None), dict(h=BAD), dict(w=None), dict(w=BAD), dict(lab=None), dict(loss=None), dict(lse=None)):
+        assert fwd(**kw) == bad, kw
+    assert fwd(ws=None) == fwd(n=nf - 1) == fwd(ws=BAD) == B.MOE_ERR_WORKSPACE
+
+    def bwd(h=FAKE, w=FAKE, lab=FAKE, lse=FAKE, dl=FAKE, dz=None, dh=FAKE, dw=FAKE, ws=FAKE, n=nb):
+        return lib.moe_vocab_loss_backward(r(sh), h, w, lab, lse, dl, dz, dh, dw, ws, n, None)
+
+    for kw in (dict(h=None), dict(h=BAD), dict(w=None), dict(w=BAD), dict(lab=None), dict(lse=None), dict(dl=None),
+               dict(dh=None), dict(dh=BAD), dict(dw=None), dict(dw=BAD)):
+        assert bwd(**kw) == bad, kw
+    assert bwd(ws=None) == bwd(n=nb - 1) == bwd(ws=BAD) == B.MOE_ERR_WORKSPACE
+    assert lib.moe_vocab_loss_workspace_size(r(sh), None, None) == bad
