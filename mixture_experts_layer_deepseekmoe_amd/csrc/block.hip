@@ -80,10 +80,10 @@ __device__ __forceinline__ void store8(void* p, size_t o, float (&v)[8]) {
 }
 
 // Sum over the block's threads, the same in each of them: a butterfly in the
-// wave, then the waves' sums in order.  `red` (one float per wave) may be
-// used again after the next barrier.
+// wave, then the waves' sums in order.  `red` may be used again after the next
+// barrier.
 template <int TPB>
-__device__ __forceinline__ float block_sum(float v, float* red) {
+__device__ __forceinline__ float block_sum(float v, float (&red)[TPB / 64]) {
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
@@ -233,32 +233,32 @@ __global__ __launch_bounds__(TPB) void block_out_kernel(BlockOutArgs a) {
 
 // ------------------------------------------------------------------ backward
 
-// Block b's rows.  Gate rows of at most BLOCK_BWD_ROWS rows (whole gates to a
-// block): the block finishes their dgate itself and leaves sum g vh.  Longer
-// ones are cut into runs of BLOCK_BWD_ROWS, none across a gate, and the block
-// leaves sum dout vh of its run for the kernels below.
+// Block b's rows.  Gate rows of at most a.rows rows (whole gates to a block):
+// the block finishes their dgate itself and leaves sum g vh.  Longer ones are
+// cut into runs of a.rows, none across a gate, and the block leaves sum dout vh
+// of its run for the kernels below.
 struct BwdRows {
   long long t0, t1;
 };
 __device__ __forceinline__ BwdRows bwd_rows(const BlockBwdArgs& a) {
   const long long L = a.gate_len, b = blockIdx.x;
   if (a.whole_gates) {
-    const long long n = L * (BLOCK_BWD_ROWS / L);
+    const long long n = L * (a.rows / L);
     return {b * n, min(b * n + n, static_cast<long long>(a.T))};
   }
   const long long g = b / a.runs, j = b - g * a.runs;
-  const long long t0 = g * L + j * BLOCK_BWD_ROWS;
-  const long long t1 = min(min(t0 + BLOCK_BWD_ROWS, (g + 1) * L), static_cast<long long>(a.T));
+  const long long t0 = g * L + j * a.rows;
+  const long long t1 = min(min(t0 + a.rows, (g + 1) * L), static_cast<long long>(a.T));
   return {t0, t1};
 }
 
 // VF: the rows v: FMT_F32 / FMT_BF16 (less `skip`, of format SF, where given) or
-// FMT_E4M3 codes.
+// FMT_E4M3 codes.  gate w, the same for all rows of a gate, stays in registers.
 template <int VF, int SF, int NV, int TPB>
 __global__ __launch_bounds__(TPB) void block_bwd_kernel(BlockBwdArgs a) {
   __shared__ float red[2][TPB / 64];
   const BwdRows rows = bwd_rows(a);
-  float acc[NV][8], gacc[NV][8];
+  float acc[NV][8], gacc[NV][8], gw[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -267,84 +267,71 @@ __global__ __launch_bounds__(TPB) void block_bwd_kernel(BlockBwdArgs a) {
   for (long long t = rows.t0; t < rows.t1; ++t) {
     const size_t row = static_cast<size_t>(t), ro = row * a.d;
     const size_t gro = a.gate != nullptr ? row / a.gate_len * a.d : 0;
+    const bool first = t == rows.t0 || (a.whole_gates && t % a.gate_len == 0);   // of its gate, here
     const float r = a.w != nullptr ? a.rstd[row] : 1.f;
-    float g[NV][8], v[NV][8];
+    Raw8 rg[NV], rs[NV], rv[NV], rk[NV], rr[NV];
+    float sc[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = 8 * (threadIdx.x + TPB * i);
       if (c >= a.d) continue;
-      load8f(a.g, ro + c, g[i]);
-      if (a.g_sub != nullptr) {
-        float s[8];
-        load8f(a.g_sub, ro + c, s);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[i][e] -= s[e];
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+      rg[i] = load8<FMT_F32>(a.g, ro + c);
+      if (a.g_sub != nullptr) rs[i] = load8<FMT_F32>(a.g_sub, ro + c);
+      if (a.res != nullptr) rr[i] = load8<FMT_F32>(a.res, ro + c);
       if constexpr (VF == FMT_E4M3) {
         const uint2 q = *reinterpret_cast<const uint2*>(a.codes + ro + c);
-        decode8(q, a.scales[row * (a.d / 128) + c / 128], v[i]);
+        rv[i].a = make_uint4(q.x, q.y, 0, 0);
+        sc[i] = a.scales[row * (a.d / 128) + c / 128];
       } else if (a.v != nullptr) {   // null: neither norm nor gate
-        values8<VF>(load8<VF>(a.v, ro + c), v[i]);
-        if (a.skip != nullptr) {
-          float s[8];
-          values8<SF>(load8<SF>(a.skip, ro + c), s);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[i][e] -= s[e];
-        }
+        rv[i] = load8<VF>(a.v, ro + c);
+        if (a.skip != nullptr) rk[i] = load8<SF>(a.skip, ro + c);
       }
     }
-    // v: vh; acc (whole gates: gacc, until the gate's last row) += g vh; g: a
-    float dot = 0.f;
+    float g[NV][8], v[NV][8], dot = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = 8 * (threadIdx.x + TPB * i);
       if (c >= a.d) continue;
       float f[8];
+      if (first) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) gw[i][e] = 1.f;
+        if (a.w != nullptr) load8f(a.w, c, gw[i]);
+        if (a.gate != nullptr) {
+          load8f(a.gate, gro + c, f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) gw[i][e] *= f[e];
+        }
+      }
+      values8<FMT_F32>(rg[i], g[i]);
+      if (a.g_sub != nullptr) {
+        values8<FMT_F32>(rs[i], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[i][e] -= f[e];
+      }
+      if constexpr (VF == FMT_E4M3) {
+        decode8(make_uint2(rv[i].a.x, rv[i].a.y), sc[i], v[i]);
+      } else if (a.v != nullptr) {
+        values8<VF>(rv[i], v[i]);
+        if (a.skip != nullptr) {
+          values8<SF>(rk[i], f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[i][e] -= f[e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+      }
+      // v: vh; gacc += g vh; g: a
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         v[i][e] *= r;
         gacc[i][e] = fmaf(g[i][e], v[i][e], gacc[i][e]);
+        g[i][e] *= gw[i][e];
+        dot = fmaf(g[i][e], v[i][e], dot);
       }
-      if (a.gate != nullptr) {
-        load8f(a.gate, gro + c, f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[i][e] *= f[e];
-      }
-      if (a.w != nullptr) {
-        load8f(a.w, c, f);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          g[i][e] *= f[e];
-          dot = fmaf(g[i][e], v[i][e], dot);
-        }
-      }
-    }
-    float mean = 0.f;
-    if (a.w != nullptr) mean = block_sum<TPB>(dot, red[t & 1]) / static_cast<float>(a.d);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = 8 * (threadIdx.x + TPB * i);
-      if (c >= a.d) continue;
-      if (a.w != nullptr) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[i][e] = r * (g[i][e] - v[i][e] * mean);
-      }
-      if (a.res != nullptr) {
-        float s[8];
-        load8f(a.res, ro + c, s);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[i][e] = fmaf(a.res_scale, s[e], g[i][e]);
-      }
-      store8<FMT_F32>(a.dv, ro + c, g[i]);
-    }
-    if (a.whole_gates && (t + 1 == rows.t1 || (t + 1) % a.gate_len == 0)) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = 8 * (threadIdx.x + TPB * i);
-        if (c >= a.d) continue;
-        float f[8];
+      // the row ends its gate (whole gates): gate gacc joins acc, w gacc is dgate
+      if (a.whole_gates && (t + 1 == rows.t1 || (t + 1) % a.gate_len == 0)) {
         load8f(a.gate, gro + c, f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[i][e] = fmaf(f[e], gacc[i][e], acc[i][e]);
@@ -357,6 +344,23 @@ __global__ __launch_bounds__(TPB) void block_bwd_kernel(BlockBwdArgs a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) gacc[i][e] = 0.f;
       }
+    }
+    const float mean = a.w != nullptr ? block_sum<TPB>(dot, red[t & 1]) / static_cast<float>(a.d) : 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = 8 * (threadIdx.x + TPB * i);
+      if (c >= a.d) continue;
+      if (a.w != nullptr) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[i][e] = r * (g[i][e] - v[i][e] * mean);
+      }
+      if (a.res != nullptr) {
+        float s[8];
+        values8<FMT_F32>(rr[i], s);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[i][e] = fmaf(a.res_scale, s[e], g[i][e]);
+      }
+      store8<FMT_F32>(a.dv, ro + c, g[i]);
     }
   }
 #pragma unroll
@@ -408,24 +412,25 @@ __global__ __launch_bounds__(1024) void block_colsum_kernel(ColSumArgs a) {
   if (a.q != nullptr) a.q[g * a.d + col] = a.gate != nullptr ? a.gate[g * a.d + col] * sum : sum;
 }
 
-// Threads and 8-column vectors per thread that hold a row of d columns.
-struct RowShape {
-  int tpb, nv;
-};
-RowShape row_shape(int d) {
-  if (d <= 2048) return {256, 1};
-  if (d <= 4096) return {256, 2};
-  if (d <= 8192) return {256, 4};
-  return {1024, 4};
+// f.template operator()<NV, TPB>() with TPB threads x NV vectors of 8 columns
+// for rows of d columns.  Few rows (up to 512, two to a CU) are spread over
+// as many threads as they fill: a call's time is then its chain of loads.
+template <class F>
+hipError_t with_row_shape(int T, int d, F&& f) {
+  if (d <= 2048) f.template operator()<1, 256>();
+  else if (d <= 8192 && T <= 512) f.template operator()<1, 1024>();
+  else if (d <= 4096) f.template operator()<2, 256>();
+  else if (d <= 8192) f.template operator()<4, 256>();
+  else f.template operator()<4, 1024>();
+  return hipGetLastError();
 }
 
-// f.template operator()<NV, TPB>() for d columns
+// The same for the backward, whose blocks take several rows in turn.
 template <class F>
-hipError_t with_row_shape(int d, F&& f) {
-  const RowShape s = row_shape(d);
-  if (s.tpb == 256 && s.nv == 1) f.template operator()<1, 256>();
-  else if (s.tpb == 256 && s.nv == 2) f.template operator()<2, 256>();
-  else if (s.tpb == 256) f.template operator()<4, 256>();
+hipError_t with_bwd_shape(int d, F&& f) {
+  if (d <= 2048) f.template operator()<1, 256>();
+  else if (d <= 4096) f.template operator()<1, 512>();
+  else if (d <= 8192) f.template operator()<1, 1024>();
   else f.template operator()<4, 1024>();
   return hipGetLastError();
 }
@@ -443,7 +448,7 @@ hipError_t launch_block_in(const BlockInArgs& a, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
   return with_fmt(a.x_fmt, [&]<int XF>() {
     return with_fmt(a.n_fmt, [&]<int NF>() {
-      return with_row_shape(a.d, [&]<int NV, int TPB>() {
+      return with_row_shape(a.T, a.d, [&]<int NV, int TPB>() {
         hipLaunchKernelGGL((block_in_kernel<XF, NF, NV, TPB>), dim3(a.T), dim3(TPB), 0, s, a);
       });
     });
@@ -455,7 +460,7 @@ hipError_t launch_block_out(const BlockOutArgs& a, hipStream_t s) {
   return with_fmt(a.x_fmt, [&]<int XF>() {
     return with_fmt(a.n_fmt, [&]<int NF>() {
       return with_fmt(a.y_fmt, [&]<int YF>() {
-        return with_row_shape(a.d, [&]<int NV, int TPB>() {
+        return with_row_shape(a.T, a.d, [&]<int NV, int TPB>() {
           hipLaunchKernelGGL((block_out_kernel<XF, NF, YF, NV, TPB>), dim3(a.T), dim3(TPB), 0, s, a);
         });
       });
@@ -467,9 +472,10 @@ hipError_t launch_block_bwd(BlockBwdArgs a, hipStream_t s) {
   const BlockBwdPlan p = block_bwd_plan(a.T, a.gate_len, a.gates, a.gate != nullptr);
   a.whole_gates = p.whole_gates;
   a.runs = p.runs;
+  a.rows = p.rows;
   if (p.blocks > 0) {
     const dim3 grid(static_cast<unsigned>(p.blocks));
-    hipError_t e = with_row_shape(a.d, [&]<int NV, int TPB>() {
+    hipError_t e = with_bwd_shape(a.d, [&]<int NV, int TPB>() {
       if (a.codes != nullptr)
         hipLaunchKernelGGL((block_bwd_kernel<FMT_E4M3, FMT_F32, NV, TPB>), grid, dim3(TPB), 0, s, a);
       else if (a.v_fmt == FMT_F32 && a.skip_fmt == FMT_F32)

@@ -237,26 +237,29 @@ struct BlockBwdArgs {
   float* dgate;           // [gates][d], or null
   float* part;            // block_bwd_floats(...) of scratch
   // set by the launcher (block_bwd_plan)
-  int whole_gates, runs;
+  int whole_gates, runs, rows;
 };
 
-// Rows a backward block takes: each block leaves one row of partial column
-// sums (d floats), so 16 rows keep that traffic near a tenth of the rows' own.
-constexpr int BLOCK_BWD_ROWS = 16;
+// A backward block takes `rows` rows and leaves one row of partial column sums
+// (d floats): 512 blocks (two to a CU) for short batches, and at most 16 rows,
+// which keep the partial sums' traffic near a tenth of the rows' own.
 struct BlockBwdPlan {
-  int whole_gates;        // gates of at most BLOCK_BWD_ROWS rows, whole ones to a block
+  int rows;
+  int whole_gates;        // gates of at most `rows` rows, whole ones to a block
   int runs;               // else: blocks per gate
   long long gates, blocks;
 };
 inline BlockBwdPlan block_bwd_plan(long long T, long long gate_len, long long gates, bool has_gate) {
   BlockBwdPlan p{};
   p.gates = gates;
-  p.whole_gates = has_gate && T > 0 && gate_len <= BLOCK_BWD_ROWS;
+  p.rows = static_cast<int>(T <= 512 ? 1 : (T + 511) / 512);
+  if (p.rows > 16) p.rows = 16;
+  p.whole_gates = has_gate && T > 0 && gate_len <= p.rows;
   if (p.whole_gates) {
-    const long long n = gate_len * (BLOCK_BWD_ROWS / gate_len);
+    const long long n = gate_len * (p.rows / gate_len);
     p.blocks = (T + n - 1) / n;
   } else {
-    p.runs = static_cast<int>((gate_len + BLOCK_BWD_ROWS - 1) / BLOCK_BWD_ROWS);
+    p.runs = static_cast<int>((gate_len + p.rows - 1) / p.rows);
     p.blocks = gates * p.runs;
   }
   return p;
@@ -278,7 +281,7 @@ struct LossArgs {
   float* loss;            // [T] (forward)
   float* lse;             // [T] (backward: read)
   // forward
-  float2* part;           // [ceil(V / 256)][T] each tile's (max, sum exp(l - max)) by row
+  float2* part;           // [T][ceil(V / 256)] each row's (max, sum exp(l - max)) by tile
   float* zlab;            // [T] the label's logit by row
   // backward
   const float* dloss;     // [T]

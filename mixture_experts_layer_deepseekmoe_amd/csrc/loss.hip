@@ -174,7 +174,7 @@ __device__ __forceinline__ void stats_epilogue(const LossArgs& a, const f32x4 (&
       const float2 p = red[k][r];
       s += p.x == NEG_INF ? p.y : p.y * __expf(p.x - m);
     }
-    a.part[static_cast<size_t>(vt) * a.T + rt.row0 + r] = make_float2(m, s);
+    a.part[static_cast<size_t>(rt.row0 + r) * ceil_div(a.V, LT) + vt] = make_float2(m, s);
   }
   if (w >= LP::N_COMPUTE) return;
 #pragma unroll
@@ -298,13 +298,14 @@ __global__ __launch_bounds__(LTHREADS, 1) void loss_logits_kernel(LossArgs a) {
   });
 }
 
-// Joins a row's tiles: 16 rows to a block, 16 lanes over a row's tiles (lane k
-// takes tiles k, k + 16, ...), the lanes' results in order.
+// Joins a row's tiles, one wave per row: lane k takes tiles k, k + 64, ..., and
+// a butterfly joins the lanes (max and rescaled sum: the same in either order).
 __global__ __launch_bounds__(256) void loss_finish_kernel(LossArgs a) {
-  __shared__ float2 s[16][17];
   const int count = a.count[0];
-  const int r = blockIdx.x * 16 + (threadIdx.x & 15), k = threadIdx.x >> 4;
+  const int r = blockIdx.x * 4 + wave_id(), lane = threadIdx.x & 63;
+  if (r >= count) return;
   const int nv = ceil_div(a.V, LT);
+  const float2* p = a.part + static_cast<size_t>(r) * nv;
   auto join = [](float2 p, float2 q) {
     const float m = fmaxf(p.x, q.x);
     const float sp = p.x == NEG_INF ? p.y : p.y * expf(p.x - m);
@@ -312,13 +313,11 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(LossArgs a) {
     return make_float2(m, sp + sq);
   };
   float2 v = make_float2(NEG_INF, 0.f);
-  if (r < count)
-    for (int t = k; t < nv; t += 16) v = join(v, a.part[static_cast<size_t>(t) * a.T + r]);
-  s[threadIdx.x & 15][k] = v;
-  __syncthreads();
-  if (threadIdx.x >= 16 || r >= count) return;
-  v = s[threadIdx.x][0];
-  for (int i = 1; i < 16; ++i) v = join(v, s[threadIdx.x][i]);
+#pragma unroll 4
+  for (int t = lane; t < nv; t += 64) v = join(v, p[t]);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v = join(v, make_float2(__shfl_xor(v.x, off), __shfl_xor(v.y, off)));
+  if (lane != 0) return;
   const float lse = v.x + logf(v.y);
   const int t = a.rows[r];
   if (!MOE_CHECK(t >= 0 && t < a.T, 706)) return;
@@ -551,7 +550,7 @@ hipError_t launch_loss_rows(const LossArgs& a, hipStream_t s) {
 hipError_t launch_loss_forward(const LossArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(loss_logits_kernel<false>, dim3(loss_grid(ceil_div(a.T, LT), ceil_div(a.v_len, LT))),
                      dim3(LTHREADS), 0, s, a);
-  hipLaunchKernelGGL(loss_finish_kernel, dim3(ceil_div(a.T, 16)), dim3(256), 0, s, a);
+  hipLaunchKernelGGL(loss_finish_kernel, dim3(ceil_div(a.T, 4)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -44,8 +44,9 @@ def test_block_shape_validation(kw, code):
 
 
 def test_block_workspace_covers_every_gating():
-    # one row of fp32 sums per 16 rows; per gate where gates are longer than that
-    for T, gr, rows in [(1, 0, 1), (160, 0, 10), (161, 0, 11), (160, 1, 10), (160, 5, 11), (160, 40, 4 * 3 + 4)]:
+    # one row of fp32 sums per block of T / 512 rows (1 to 16); per gate where gates are longer than that
+    for T, gr, rows in [(1, 0, 1), (160, 0, 160), (1024, 0, 512), (160, 1, 160), (8192, 5, 547), (20480, 0, 1280),
+                        (8192, 40, 205 * 3 + 205)]:
         rc, n = _block_ws(_bs(T=T, gate_rows=gr))
         assert rc == 0 and n >= rows * 256 * 4, (T, gr, n)
 

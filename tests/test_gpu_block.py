@@ -6,7 +6,9 @@ Tolerances.  u16 = 2^-8 is the largest relative rounding of a bf16 store, E =
 sum of at most 32768 squares in the kernel's tree has at most about 4 x 8 + 6 + 16 + 3
 roundings on a path (57 x 2^-24 = 3.4e-6), as has the mean in the backward,
 and at most ten roundings more follow; the column sums add at most 16 rows in
-a block and ceil(n / 64) + 64 partial rows (n <= 64 here: 81 roundings, 4.8e-6).
+a block and ceil(n / 64) + 64 partial rows, twice where there are many gates
+(n <= 8200 here: at most 16 + 2 x 193 roundings, 2.4e-5 if all were of one sign
+and full size; 2e-5 is kept for them, E for the rest).
 """
 
 import numpy as np
@@ -49,7 +51,8 @@ def _close(got, ref, size, dtype="f32"):
 # T, d: one token, odd row counts about the backward's 16-row runs, widths at
 # and just past each row shape's limit (2048, 4096, 8192, 32768) and not
 # multiples of anything but 8
-SIZES = [(1, 8), (1, 2048), (3, 72), (16, 2056), (17, 4096), (33, 4104), (5, 8192), (2, 8200), (2, 32768), (129, 1000)]
+SIZES = [(1, 8), (1, 2048), (3, 72), (16, 2056), (17, 4096), (33, 4104), (5, 8192), (2, 8200), (2, 32768), (129, 1000),
+         (1100, 72), (8200, 136)]   # several rows to a backward block: 3, and the most, 16
 
 
 @pytest.mark.parametrize("T,d", SIZES)
@@ -88,6 +91,15 @@ OUT_CASES = [  # T, d, x, n, y, gate_rows (None: no gate), norm, skip, next
     (33, 520, "bf16", "bf16", "f32", 100, True, False, False),
     (20, 4104, "bf16", "bf16", "f32", None, False, True, False),
     (3, 8200, "bf16", "bf16", "f32", 2, True, True, True),
+    # several rows to a backward block (T / 512, at most 16): whole gates, and gates cut into runs
+    (1100, 72, "bf16", "bf16", "f32", 1, True, True, True),
+    (1100, 72, "bf16", "bf16", "f32", 2, True, False, False),
+    (1100, 72, "bf16", "bf16", "f32", 3, False, True, False),
+    (1100, 2056, "bf16", "bf16", "f32", 4, True, True, False),
+    (8200, 40, "f32", "bf16", "bf16", 5, True, True, True),
+    (8200, 40, "bf16", "bf16", "f32", 16, True, False, True),
+    (8200, 40, "bf16", "bf16", "f32", 17, True, True, False),
+    (8200, 40, "bf16", "bf16", "f32", 0, True, True, False),
 ]
 
 
