@@ -277,7 +277,7 @@ struct LossArgs {
   int T, d, V;
   int32_t* rows;          // [T] token of each row
   int32_t* pos;           // [T] row of each token, or -1
-  int32_t* count;         // [1] rows
+  int32_t* count;         // [2] rows; splits of dh's sum (backward)
   float* loss;            // [T] (forward)
   float* lse;             // [T] (backward: read)
   // forward
@@ -288,8 +288,8 @@ struct LossArgs {
   const float* dlse;      // [T], or null
   uint16_t* hc;           // [T][d] the rows' hidden rows, one after the other
   uint16_t* g;            // [T][ldg] a piece's G = dlogits
-  float* acc;             // [splits][T][d] dh by row
-  int ldg, splits;        // loss_plan(...)
+  float* acc;             // [splits][row tiles of 256][d] dh by row (loss_acc_rows)
+  int ldg;                // loss_piece
   int dh_fmt, dw_fmt;
   void* dh;               // [T][d]
   void* dw;               // [V][d]
@@ -312,8 +312,17 @@ inline int loss_piece(long long T, long long d, long long V) {
 }
 
 // dh = G w sums over the whole piece: few rows make few tiles, so the piece is
-// cut into `splits` runs of columns with an fp32 copy of dh each.
-int loss_splits(long long T, long long d, long long piece);
+// cut into up to 64 runs of columns, of a tile's width at least, with an fp32
+// copy of dh each; their number is chosen on the device, where the rows are
+// known, and keeps the copies' tiles within LOSS_SPLIT_TILES (512 MB).
+constexpr int LOSS_SPLITS = 64, LOSS_SPLIT_TILES = 2048;
+inline long long loss_acc_rows(long long T, long long d, long long piece) {   // rows of the copies together
+  const long long nm = (T + LOSS_TILE - 1) / LOSS_TILE, nn = (d + LOSS_TILE - 1) / LOSS_TILE;
+  const long long s = piece / LOSS_TILE < LOSS_SPLITS ? piece / LOSS_TILE : LOSS_SPLITS;
+  long long tiles = nm * s < LOSS_SPLIT_TILES / nn ? nm * s : LOSS_SPLIT_TILES / nn;
+  if (tiles < nm) tiles = nm;
+  return tiles * LOSS_TILE;
+}
 
 hipError_t launch_loss_rows(const LossArgs& a, hipStream_t s);
 hipError_t launch_loss_forward(const LossArgs& a, hipStream_t s);

@@ -20,7 +20,7 @@
 // fp32 accumulation; statistics and dh's sums are fp32; G is rounded to bf16
 // once, as the operand of the two products that follow (a relative error of
 // 2^-9 per element, as for the bf16 operands of the layer's backward).
-#include "bwd_core.hpp"
+#include "dense_core.hpp"
 #include "kernels.hpp"
 
 namespace moe {
@@ -30,24 +30,35 @@ namespace {
 constexpr int LT = LOSS_TILE;
 constexpr int NXCDS = 8;
 
-// Tile j of nm x nn, walked in groups of 8 m-tiles (m fastest): the 32 tiles
-// an XCD's CUs hold at once share 8 row blocks and 4 column blocks in its L2.
-// XCD x (blocks x, x + 8, ...) takes a contiguous eighth of the walk.
-// Returns false where the block has no tile.
-__device__ __forceinline__ bool loss_tile(int nm, int nn, int& m, int& n) {
-  const long long total = static_cast<long long>(nm) * nn;
-  const long long chunk = (total + NXCDS - 1) / NXCDS;
-  const long long l = blockIdx.x / NXCDS, j = blockIdx.x % NXCDS * chunk + l;
-  if (l >= chunk || j >= total) return false;
-  constexpr int GM = 8;
-  const int per = GM * nn, g = static_cast<int>(j / per), rem = static_cast<int>(j - static_cast<long long>(g) * per);
-  const int gm = min(GM, nm - g * GM);
-  m = g * GM + rem % gm;
-  n = rem / gm;
-  return true;
-}
+// The tiles of nm x nn that this block takes.  They are walked in groups of 8
+// m-tiles (m fastest), so that the 32 tiles an XCD's CUs hold at once share 8
+// row blocks and 4 column blocks in its L2; XCD x (blocks x, x + 8, ...) has a
+// contiguous eighth of the walk, and its P blocks take every P-th tile of that.
+struct TileWalk {
+  int nm, nn;
+  long long j0, n;   // the XCD's first tile and its number of them
+  int l, P;
+  __device__ TileWalk(int nm_, int nn_) : nm(nm_), nn(nn_) {
+    const long long total = static_cast<long long>(nm) * nn, chunk = (total + NXCDS - 1) / NXCDS;
+    j0 = blockIdx.x % NXCDS * chunk;
+    n = max(0LL, min(chunk, total - j0));
+    l = blockIdx.x / NXCDS;
+    P = gridDim.x / NXCDS;
+  }
+  __device__ int count() const { return l < n ? static_cast<int>((n - l + P - 1) / P) : 0; }
+  __device__ void tile(int i, int& m, int& k) const {
+    constexpr int GM = 8;
+    const long long j = j0 + l + static_cast<long long>(i) * P;
+    const int per = GM * nn, g = static_cast<int>(j / per), rem = static_cast<int>(j - static_cast<long long>(g) * per);
+    const int gm = min(GM, nm - g * GM);
+    m = g * GM + rem % gm;
+    k = rem / gm;
+  }
+};
+constexpr int NBLOCKS = 256;   // one per CU
 inline unsigned loss_grid(long long nm, long long nn) {
-  return static_cast<unsigned>(NXCDS * ((nm * nn + NXCDS - 1) / NXCDS));
+  const long long per = (nm * nn + NXCDS - 1) / NXCDS;
+  return static_cast<unsigned>(NXCDS * (per < NBLOCKS / NXCDS ? per : NBLOCKS / NXCDS));
 }
 
 // m-tile m of `count` rows cut into nm = ceil(count / 256) nearly equal tiles
@@ -60,6 +71,17 @@ __device__ __forceinline__ RowTile row_tile(int count, int nm, int m) {
   const int per = ((count + nm - 1) / nm + 15) / 16 * 16;   // at most 256
   const int r0 = m * per;
   return {r0, min(per, count - r0)};
+}
+
+// Cost of s splits of dh's sum for nm x nn tiles: rounds of 256 tiles at about
+// 0.75 us per 32-column step, and the splits' fp32 tiles written and read at
+// about 4 TB/s.  The least cost (the fewest splits of equal ones) is taken; the
+// limits are those of loss_acc_rows.
+__device__ inline float split_cost(int s, int nm, int nn, int piece) {
+  const int tiles = nm * nn;   // below 2^17
+  if (s > 1 && (s * LT > piece || s * tiles > LOSS_SPLIT_TILES)) return 1e30f;
+  const float rounds = static_cast<float>((tiles * s + NBLOCKS - 1) / NBLOCKS);
+  return rounds * static_cast<float>(((piece + s - 1) / s + 31) / 32) * 0.75f + static_cast<float>(s) * tiles * 0.13f;
 }
 
 // ------------------------------------------------------------------ rows
@@ -97,6 +119,21 @@ __global__ __launch_bounds__(1024) void loss_rows_kernel(LossArgs a) {
     __syncthreads();
   }
   if (threadIdx.x == 0) a.count[0] = base;
+  if (a.acc == nullptr || w > 0) return;
+  // one lane per number of splits
+  int best = lane + 1;
+  static_assert(LOSS_SPLITS == 64, "one lane each");
+  float cost = split_cost(best, row_tiles(base), ceil_div(a.d, LT), a.ldg);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) {
+    const float c = __shfl_xor(cost, off);
+    const int o = __shfl_xor(best, off);
+    if (c < cost || (c == cost && o < best)) {
+      cost = c;
+      best = o;
+    }
+  }
+  if (lane == 0) a.count[1] = best;
 }
 
 // hc[r] = h[rows[r]]
@@ -112,59 +149,50 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
 
 // ------------------------------------------------------------------ logits
 
-// The forward's grouped-GEMM pipeline: 8 MFMA waves (2 x 4) + 4 load waves, a
-// ring of 5 stages of 32 K (all of the LDS).
-using LP = Pipe<FMT_BF16, LT, LT, 5, 2, ACC_TIED, 8, 4>;
-constexpr int LTHREADS = 768;
-constexpr int LMI = LP::MI, LNJ = LP::NJ;
-
 constexpr float NEG_INF = -__builtin_inff();
+using Acc = f32x4[bt::MI][bt::NJ];   // a wave's accumulators (dense_core.hpp)
+
+// What the epilogues need of a tile's rows, in SPARE after the waves' staging:
+// one entry per row, written by the load waves.
+//   forward   the label's column in the tile (or outside it)
+//   backward  lse, dloss + dlse, dloss, and the label's column (bits)
+constexpr int ROW_DATA = dense::SPARE + dense::NMW * dense::STAGING;
+static_assert(ROW_DATA + LT * 16 <= dense::RING_BYTES && 4 * LT * 8 <= dense::NMW * dense::STAGING,
+              "the forward's (max, sum) and the row data fit the spare buffer");
 
 // Forward epilogue: per row of the tile (m, s) = (max, sum exp(l - m)) over its
-// columns, and the label's logit where the label is one of them.
-template <int NSUBC>
-__device__ __forceinline__ void stats_epilogue(const LossArgs& a, const f32x4 (&acc)[LMI][LNJ], uint8_t* lds, int vt,
-                                               RowTile rt, int ncol) {
-  float2(*red)[LT] = reinterpret_cast<float2(*)[LT]>(lds);                 // [4][256]
-  int* lab = reinterpret_cast<int*>(lds + 4 * LT * sizeof(float2));        // [256]
-  const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4, wm = w % 2, wn = w / 2;
-  wait_vm_lgkm0<0>();
-  block_barrier();   // every wave is done with the stage ring
-  if (w >= LP::N_COMPUTE) {
-    const int r = threadIdx.x - 64 * LP::N_COMPUTE;
-    int l = -1;
-    if (r < rt.rows) {
-      const int t = a.rows[rt.row0 + r];
-      if (MOE_CHECK(t >= 0 && t < a.T, 702)) l = a.labels[t] - vt * LT;
-    }
-    lab[r] = l;
-  } else {
+// columns, and the label's logit where the label is one of them.  One barrier.
+template <int NSUB>
+__device__ __forceinline__ void stats_epilogue(const LossArgs& a, const Acc& acc, uint8_t* ring, int vt, RowTile rt,
+                                               int ncol) {
+  float2(*red)[LT] = reinterpret_cast<float2(*)[LT]>(ring + dense::SPARE);   // [4][256]
+  const int* lab = reinterpret_cast<const int*>(ring + ROW_DATA);            // [256]
+  const int w = wave_id(), lane = dense::fresh_lane(), lr = lane & 15, lg = lane >> 4, wm = w % 2, wn = w / 2;
 #pragma unroll
-    for (int i = 0; i < NSUBC; ++i) {
-      float m = NEG_INF;
+  for (int i = 0; i < NSUB; ++i) {
+    float m = NEG_INF;
 #pragma unroll
-      for (int j = 0; j < LNJ; ++j)
+    for (int j = 0; j < bt::NJ; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (64 * wn + 16 * j + 4 * lg + e < ncol) m = fmaxf(m, acc[i][j][e]);
-      m = fmaxf(m, __shfl_xor(m, 16));
-      m = fmaxf(m, __shfl_xor(m, 32));
-      const float mb = m == NEG_INF ? 0.f : m;   // no column, or all of them -inf: the sum is 0
-      float s = 0.f;
+      for (int e = 0; e < 4; ++e)
+        if (64 * wn + 16 * j + 4 * lg + e < ncol) m = fmaxf(m, acc[i][j][e]);
+    m = fmaxf(m, __shfl_xor(m, 16));
+    m = fmaxf(m, __shfl_xor(m, 32));
+    const float mb = m == NEG_INF ? 0.f : m;   // no column, or all of them -inf: the sum is 0
+    float s = 0.f;
 #pragma unroll
-      for (int j = 0; j < LNJ; ++j)
+    for (int j = 0; j < bt::NJ; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (64 * wn + 16 * j + 4 * lg + e < ncol) s += __expf(acc[i][j][e] - mb);
-      s += __shfl_xor(s, 16);
-      s += __shfl_xor(s, 32);
-      if (lg == 0) red[wn][16 * (2 * i + wm) + lr] = make_float2(m, s);
-    }
+      for (int e = 0; e < 4; ++e)
+        if (64 * wn + 16 * j + 4 * lg + e < ncol) s += __expf(acc[i][j][e] - mb);
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (lg == 0) red[wn][16 * (2 * i + wm) + lr] = make_float2(m, s);
   }
   wait_vm_lgkm0<0>();
-  block_barrier();
-  if (static_cast<int>(threadIdx.x) < rt.rows) {
-    const int r = threadIdx.x;
+  block_barrier();   // red and the row data are written
+  const int r = 64 * w + lane;
+  if (r < rt.rows) {
     float m = red[0][r].x;
 #pragma unroll
     for (int k = 1; k < 4; ++k) m = fmaxf(m, red[k][r].x);
@@ -176,126 +204,123 @@ __device__ __forceinline__ void stats_epilogue(const LossArgs& a, const f32x4 (&
     }
     a.part[static_cast<size_t>(rt.row0 + r) * ceil_div(a.V, LT) + vt] = make_float2(m, s);
   }
-  if (w >= LP::N_COMPUTE) return;
 #pragma unroll
-  for (int i = 0; i < NSUBC; ++i) {
+  for (int i = 0; i < NSUB; ++i) {
     const int row = 16 * (2 * i + wm) + lr;
     if (row >= rt.rows) continue;
-    const int l = lab[row];
-    if (l < 0 || l >= ncol || l / 64 != wn || l / 4 % 4 != lg) continue;
+    const int c = lab[row];
+    if (c < 0 || c >= ncol || c / 64 != wn || c / 4 % 4 != lg) continue;
 #pragma unroll
-    for (int j = 0; j < LNJ; ++j)
+    for (int j = 0; j < bt::NJ; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (l % 64 / 16 == j && l % 4 == e) a.zlab[rt.row0 + row] = acc[i][j][e];
+        if (c % 64 / 16 == j && c % 4 == e) a.zlab[rt.row0 + row] = acc[i][j][e];
   }
 }
 
-// Backward epilogue: the tile of G, through LDS (whole lines per store).
-template <int NSUBC>
-__device__ __forceinline__ void grad_epilogue(const LossArgs& a, const f32x4 (&acc)[LMI][LNJ], uint8_t* lds, int vt,
-                                              RowTile rt, int ncol) {
-  constexpr int PITCH = LT * 2 + 16;   // padded rows: the 16 rows of a subtile hit different banks
-  static_assert(LT * PITCH + LT * 16 <= 5 * LP::STAGE_BYTES, "tile and row data fit the stage ring");
-  float4* rd = reinterpret_cast<float4*>(lds + LT * PITCH);   // lse, dloss + dlse, dloss, label's column (bits)
-  const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4, wm = w % 2, wn = w / 2;
-  wait_vm_lgkm0<0>();
-  block_barrier();   // every wave is done with the stage ring
-  if (w >= LP::N_COMPUTE) {
-    const int r = threadIdx.x - 64 * LP::N_COMPUTE;
-    float4 v = make_float4(0.f, 0.f, 0.f, __int_as_float(-1));
-    if (r < rt.rows) {
-      const int t = a.rows[rt.row0 + r];
-      if (MOE_CHECK(t >= 0 && t < a.T, 703)) {
-        const float dl = a.dloss[t];
-        v = make_float4(a.lse[t], a.dlse != nullptr ? dl + a.dlse[t] : dl, dl,
-                        __int_as_float(a.labels[t] - a.v_first - vt * LT));
-      }
-    }
-    rd[r] = v;
-  }
-  wait_vm_lgkm0<0>();
-  block_barrier();
-  if (w < LP::N_COMPUTE) {
-#pragma unroll
-    for (int i = 0; i < NSUBC; ++i) {
-      const int row = 16 * (2 * i + wm) + lr;
-      const float4 v = rd[row];
-      const int l = __float_as_int(v.w);
-#pragma unroll
-      for (int j = 0; j < LNJ; ++j) {
-        const int col = 64 * wn + 16 * j + 4 * lg;
+// Backward epilogue: the tile of G.  One barrier.
+template <int NSUB>
+__device__ __forceinline__ void grad_epilogue(const LossArgs& a, const Acc& acc, uint8_t* ring, int vt, RowTile rt,
+                                              int ncol) {
+  const float4* rd = reinterpret_cast<const float4*>(ring + ROW_DATA);
+  const int w = wave_id(), lane = dense::fresh_lane(), lr = lane & 15, lg = lane >> 4, wm = w % 2, wn = w / 2;
+  block_barrier();   // the row data are written
+  float4 d;
+  dense::store_bf16_tile<NSUB>(
+      ring, 64,
+      [&](int i, int j) {
+        if (j == 0) d = rd[16 * (2 * i + wm) + lr];
+        const int l = __float_as_int(d.w), col = 64 * wn + 16 * j + 4 * lg;
         float g[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          g[e] = v.y * __expf(acc[i][j][e] - v.x);
-          if (col + e == l) g[e] -= v.z;
+          g[e] = d.y * __expf(acc[i][j][e] - d.x);
+          if (col + e == l) g[e] -= d.z;
           if (col + e >= ncol) g[e] = 0.f;
         }
-        *reinterpret_cast<uint2*>(lds + row * PITCH + col * 2) = pack_bf16x4(g[0], g[1], g[2], g[3]);
-      }
-    }
-  }
-  wait_vm_lgkm0<0>();
-  block_barrier();
-  store_tile_from_lds<LT, PITCH, LTHREADS>(lds, rt.rows, LT, a.g + static_cast<size_t>(rt.row0) * a.ldg + vt * LT, a.ldg);
+        return pack_bf16x4(g[0], g[1], g[2], g[3]);
+      },
+      [&](int row) -> uint16_t* {
+        return row < rt.rows ? a.g + static_cast<size_t>(rt.row0 + row) * a.ldg + vt * LT + 64 * wn : nullptr;
+      });
 }
 
 template <bool GRAD>
-__global__ __launch_bounds__(LTHREADS, 1) void loss_logits_kernel(LossArgs a) {
-  __shared__ __attribute__((aligned(1024))) uint8_t ring_lds[5 * LP::STAGE_BYTES];
+__global__ __launch_bounds__(dense::THREADS, 1) void loss_logits_kernel(LossArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[dense::RING_BYTES];
   const int count = a.count[0];
   if (!MOE_CHECK(count >= 0 && count <= a.T, 704)) return;
-  const int nm = row_tiles(count);
-  int mt, vt;
-  if (!loss_tile(nm, ceil_div(a.v_len, LT), mt, vt)) return;
-  const RowTile rt = row_tile(count, nm, mt);
-  const int v0 = a.v_first + vt * LT, ncol = min(LT, a.V - v0);
+  const int nm = row_tiles(count), nk = a.d / 32;
+  const TileWalk walk(nm, ceil_div(a.v_len, LT));
+  const int n = walk.count();
   const uint32_t ld = a.d * 2;
-
-  auto make_pipe = [&]() {
-    LP p;
-    // rows past the tile's: an offset past the resource, so their loads
-    // return zeros without touching memory
-    if constexpr (GRAD) {
-      p.init(make_rsrc(a.hc + static_cast<size_t>(rt.row0) * a.d, rt.rows * ld),
-             [&](int r) { return static_cast<uint32_t>((r < rt.rows ? r : rt.rows) * ld); },
-             make_rsrc(a.w + static_cast<size_t>(v0) * a.d, ncol * ld),
-             [&](int r) { return static_cast<uint32_t>(r * ld); }, make_rsrc(a.w, 0), [](int) { return 0u; });
-    } else {
-      p.init(make_rsrc(a.h, a.T * ld),
-             [&](int r) {
-               const int t = r < rt.rows ? a.rows[rt.row0 + r] : a.T;
-               return static_cast<uint32_t>((MOE_CHECK(t >= 0 && t <= a.T, 705) ? t : a.T) * ld);
-             },
-             make_rsrc(a.w + static_cast<size_t>(v0) * a.d, ncol * ld),
-             [&](int r) { return static_cast<uint32_t>(r * ld); }, make_rsrc(a.w, 0), [](int) { return 0u; });
+  if (wave_id() >= dense::NMW) {
+    const int r = threadIdx.x - 64 * dense::NMW;   // the tile row whose data this thread fetches
+    dense::Opnd oa, ob;
+    float4 rd;
+    RowTile rt;
+    auto head = [&](int i) {
+      int mt, vt;
+      walk.tile(i, mt, vt);
+      rt = row_tile(count, nm, mt);
+      const int v0 = a.v_first + vt * LT;
+      // rows past the tile's: an offset past the resource, so their loads
+      // return zeros without touching memory
+      if constexpr (GRAD) {
+        oa = dense::opnd_kc(make_rsrc(a.hc + static_cast<size_t>(rt.row0) * a.d, rt.rows * ld),
+                            [&](int m) { return static_cast<uint32_t>((m < rt.rows ? m : rt.rows) * ld); });
+      } else {
+        oa = dense::opnd_kc(make_rsrc(a.h, a.T * ld), [&](int m) {
+          const int t = m < rt.rows ? a.rows[rt.row0 + m] : a.T;
+          return static_cast<uint32_t>((MOE_CHECK(t >= 0 && t <= a.T, 705) ? t : a.T) * ld);
+        });
+      }
+      ob = dense::opnd_kc(make_rsrc(a.w + static_cast<size_t>(v0) * a.d, min(LT, a.V - v0) * ld),
+                          [&](int m) { return static_cast<uint32_t>(m * ld); });
+      dense::with_rows(rt.rows, [&]<int NSUB>() { dense::load_head<NSUB / 2>(ring, oa, ob, nk); });
+      rd = make_float4(0.f, 0.f, 0.f, __int_as_float(-1));
+      if (r < rt.rows) {
+        const int t = a.rows[rt.row0 + r];
+        if (MOE_CHECK(t >= 0 && t < a.T, 702)) {
+          rd.w = __int_as_float(a.labels[t] - v0);
+          if constexpr (GRAD) {
+            rd.x = a.lse[t];
+            rd.z = a.dloss[t];
+            rd.y = a.dlse != nullptr ? rd.z + a.dlse[t] : rd.z;
+          }
+        }
+      }
+    };
+    if (n > 0) head(0);
+    for (int i = 0; i < n; ++i) {
+      dense::with_rows(rt.rows, [&]<int NSUB>() { dense::load_body<NSUB / 2>(ring, oa, ob, nk); });
+      block_barrier();   // the tile's stages are read
+      if constexpr (GRAD)
+        reinterpret_cast<float4*>(ring + ROW_DATA)[r] = rd;
+      else
+        reinterpret_cast<int*>(ring + ROW_DATA)[r] = __float_as_int(rd.w);
+      wait_lgkm0();
+      if constexpr (GRAD) block_barrier();
+      if (i + 1 < n) head(i + 1);
+      if constexpr (!GRAD) block_barrier();
     }
-    p.nks = a.d / 32;
-    return p;
-  };
-
-  const Ring<5> ring = make_ring<5, LP::STAGE_BYTES>(ring_lds);
-  const int w = wave_id(), wn = w / 2;
-  const WRows<0> wr{16 * LNJ * wn};
-  const int sub = (rt.rows + 15) / 16;
-  // a wave row whose last subtile lies past the rows computes one fewer
-  const bool short_row = w % 2 + 2 * ((sub + 1) / 2 - 1) >= sub;
-  auto tile = [&]<int NSUB, int NSUBC>() {
-    f32x4 acc[LMI][LNJ];
-    zero_acc(acc);
-    pipe_mainloop_ws<LP, NSUB, NSUBC>(make_pipe(), ring.s, a.d / 32, wr, acc);
-    if constexpr (GRAD)
-      grad_epilogue<NSUBC>(a, acc, ring_lds, vt, rt, ncol);
-    else
-      stats_epilogue<NSUBC>(a, acc, ring_lds, vt, rt, ncol);
-  };
-  dispatch_rows<LMI, 2>(rt.rows, [&]<int NSUB>() {
-    if (short_row)
-      tile.template operator()<NSUB, NSUB - 1>();
-    else
-      tile.template operator()<NSUB, NSUB>();
-  });
+    return;
+  }
+  for (int i = 0; i < n; ++i) {
+    int mt, vt;
+    walk.tile(i, mt, vt);
+    const RowTile rt = row_tile(count, nm, mt);
+    const int ncol = min(LT, a.V - a.v_first - vt * LT);
+    dense::with_rows(rt.rows, [&]<int NSUB>() {
+      Acc acc;
+      dense::mfma_loop<bt::KC, bt::KC, NSUB>(ring, nk, acc);
+      block_barrier();   // the tile's stages are read
+      if constexpr (GRAD)
+        grad_epilogue<NSUB>(a, acc, ring, vt, rt, ncol);
+      else
+        stats_epilogue<NSUB>(a, acc, ring, vt, rt, ncol);
+    });
+  }
 }
 
 // Joins a row's tiles, one wave per row: lane k takes tiles k, k + 64, ..., and
@@ -337,57 +362,81 @@ __device__ __forceinline__ Run split_run(int n, int splits, int s) {
   return {s * per, max(0, min(per, n - s * per))};
 }
 
-__global__ __launch_bounds__(bt::THREADS, 1) void loss_dh_kernel(LossArgs a) {
-  using namespace bt;
-  __shared__ __attribute__((aligned(1024))) uint8_t ring[NSTG * STB];
-  const int count = a.count[0];
-  if (!MOE_CHECK(count >= 0 && count <= a.T, 707)) return;
-  const int nm = row_tiles(count), nn = ceil_div(a.d, BT);
-  int mt, ns;
-  if (!loss_tile(nm, nn * a.splits, mt, ns)) return;
-  const int s = ns / nn, n0 = (ns - s * nn) * BT;
-  const RowTile rt = row_tile(count, nm, mt);
-  const Run run = split_run(a.v_len, a.splits, s);
-  const uint32_t ldg = a.ldg * 2, ldw = a.d * 2;
-  const int nk = ceil_div(run.len, 32);
-  f32x4 acc[MI][NJ];
-  zero_acc(acc);
-  if (wave_id() >= NMW) {
-    // G's columns past V are zero, w's rows past V lie past the resource
-    const Opnd oa = opnd_kc(make_rsrc(a.g + static_cast<size_t>(rt.row0) * a.ldg + run.k0, rt.rows * ldg - run.k0 * 2),
-                            [&](int m) { return static_cast<uint32_t>((m < rt.rows ? m : rt.rows) * ldg); });
-    const Opnd ob = opnd_ko(make_rsrc(a.w + static_cast<size_t>(a.v_first + run.k0) * a.d, run.len * ldw), ldw, n0);
-    mainloop_pa(ring, oa, ob, nk, acc);
+__global__ __launch_bounds__(dense::THREADS, 1) void loss_dh_kernel(LossArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[dense::RING_BYTES];
+  const int count = a.count[0], splits = a.count[1];
+  if (!MOE_CHECK(count >= 0 && count <= a.T && splits >= 1 && splits <= LOSS_SPLITS, 707)) return;
+  const int nm = row_tiles(count), nn = ceil_div(a.d, LT);
+  const TileWalk walk(nm, nn * splits);
+  const int n = walk.count();
+  auto tile = [&](int i, RowTile& rt, Run& run, int& s, int& n0) {
+    int mt, k;
+    walk.tile(i, mt, k);
+    s = k / nn;
+    n0 = (k - s * nn) * LT;
+    rt = row_tile(count, nm, mt);
+    run = split_run(a.v_len, splits, s);
+  };
+  RowTile rt;
+  Run run;
+  int s, n0;
+  if (wave_id() >= dense::NMW) {
+    const uint32_t ldg = a.ldg * 2, ldw = a.d * 2;
+    dense::Opnd oa, ob;
+    auto head = [&](int i) {
+      tile(i, rt, run, s, n0);
+      // G's columns past V are zero, w's rows past V lie past the resource
+      oa = dense::opnd_kc(make_rsrc(a.g + static_cast<size_t>(rt.row0) * a.ldg + run.k0, rt.rows * ldg - run.k0 * 2),
+                          [&](int m) { return static_cast<uint32_t>((m < rt.rows ? m : rt.rows) * ldg); });
+      ob = dense::opnd_ko(make_rsrc(a.w + static_cast<size_t>(a.v_first + run.k0) * a.d, run.len * ldw), ldw, n0);
+      dense::with_rows(rt.rows,
+                       [&]<int NSUB>() { dense::load_head<NSUB / 2>(ring, oa, ob, ceil_div(run.len, 32)); });
+    };
+    if (n > 0) head(0);
+    for (int i = 0; i < n; ++i) {
+      dense::with_rows(rt.rows,
+                       [&]<int NSUB>() { dense::load_body<NSUB / 2>(ring, oa, ob, ceil_div(run.len, 32)); });
+      block_barrier();   // the tile's stages are read
+      if (i + 1 < n) head(i + 1);
+    }
     return;
   }
-  with_row_subtiles(rt.rows, [&]<int NS>() { mainloop_pa<NS>(ring, Opnd{}, Opnd{}, nk, acc); });
-  const int w = wave_id(), lane = threadIdx.x & 63, wm = w % 2, wn = w / 2;
+  const int w = wave_id(), wm = w % 2, wn = w / 2;
   const bool first = a.v_first == 0;
+  for (int t = 0; t < n; ++t) {
+    tile(t, rt, run, s, n0);
+    dense::with_rows(rt.rows, [&]<int NSUB>() {
+      Acc acc;
+      dense::mfma_loop<bt::KC, bt::KO, NSUB>(ring, ceil_div(run.len, 32), acc);
+      block_barrier();   // the tile's stages are read
+      const int lane = dense::fresh_lane();
 #pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const int row = 16 * (2 * i + wm) + (lane & 15);
-    if (row >= rt.rows) continue;
-    float* dst = a.acc + (static_cast<size_t>(s) * a.T + rt.row0 + row) * a.d;
+      for (int i = 0; i < NSUB; ++i) {
+        const int row = 16 * (2 * i + wm) + (lane & 15);
+        if (row >= rt.rows) continue;
+        float* dst = a.acc + (static_cast<size_t>(s) * nm * LT + rt.row0 + row) * a.d;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int col = n0 + 64 * wn + 16 * j + 4 * (lane >> 4);
-      if (col >= a.d) continue;
-      f32x4* p = reinterpret_cast<f32x4*>(dst + col);
-      *p = first ? acc[i][j] : *p + acc[i][j];
-    }
+        for (int j = 0; j < bt::NJ; ++j) {
+          const int col = n0 + 64 * wn + 16 * j + 4 * (lane >> 4);
+          if (col >= a.d) continue;
+          f32x4* p = reinterpret_cast<f32x4*>(dst + col);
+          *p = first ? acc[i][j] : *p + acc[i][j];
+        }
+      }
+    });
   }
 }
 
 // dh[t] = the sum of its row's splits, in order; zero for a token that is no row.
 __global__ __launch_bounds__(256) void loss_dh_out_kernel(LossArgs a) {
   const size_t t = blockIdx.x;
-  const int r = a.pos[t];
-  if (!MOE_CHECK(r >= -1 && r < a.T, 708)) return;
+  const int r = a.pos[t], nm = row_tiles(a.count[0]), splits = a.count[1];
+  if (!MOE_CHECK(r >= -1 && r < a.T && splits <= LOSS_SPLITS, 708)) return;
   for (int c = 4 * threadIdx.x; c < a.d; c += 1024) {
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
     if (r >= 0)
-      for (int s = 0; s < a.splits; ++s)
-        v += *reinterpret_cast<const f32x4*>(a.acc + (static_cast<size_t>(s) * a.T + r) * a.d + c);
+      for (int s = 0; s < splits; ++s)
+        v += *reinterpret_cast<const f32x4*>(a.acc + (static_cast<size_t>(s) * nm * LT + r) * a.d + c);
     if (a.dh_fmt == FMT_F32)
       *reinterpret_cast<f32x4*>(static_cast<float*>(a.dh) + t * a.d + c) = v;
     else
@@ -397,125 +446,68 @@ __global__ __launch_bounds__(256) void loss_dh_out_kernel(LossArgs a) {
 
 // ------------------------------------------------------------------ dw = G^T h
 
-// Both operands K-outer (K: the rows): the load waves keep four stages of the
-// ring of five ahead, two of them landed before each barrier.
-__device__ __forceinline__ void mainloop_ko(uint8_t* ring, const bt::Opnd& a, const bt::Opnd& b, int nk,
-                                            f32x4 (&acc)[bt::MI][bt::NJ]) {
+__global__ __launch_bounds__(dense::THREADS, 1) void loss_dw_kernel(LossArgs a) {
   using namespace bt;
-  const int w = wave_id();
-  if (nk <= 0) return;
-  if (w >= NMW) {
-    for (int s = 0; s < 4 && s < nk; ++s) issue_stage(a, b, ring + s * STB, s);
-    if (nk >= 4)
-      wait_vm_lgkm0<2 * NLS>();   // stages 0 and 1
-    else
-      wait_vm_lgkm0<0>();
-    for (int ks = 0; ks < nk; ++ks) {
-      block_barrier();
-      if (ks + 4 < nk) {
-        issue_stage(a, b, ring + (ks + 4) % NSTG * STB, ks + 4);
-        wait_vm_lgkm0<2 * NLS>();   // stage ks + 2
-      } else {
-        wait_vm_lgkm0<0>();
-      }
-    }
-    return;
-  }
-  const int wm = w % 2, wn = w / 2;
-  KoLane kl = ko_lane();
-  i32x4 wf[NJ], xf;
-  block_barrier();   // stages 0 and 1 have landed
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) wf[j] = frag_ko(ring + OPB, 64 * wn + 16 * j, kl);
-  xf = frag_ko(ring, 16 * wm, kl);
-  acc_fence(acc);
-  for (int ks = 0; ks < nk; ++ks) {
-    asm volatile("" : "+v"(kl.base), "+v"(kl.y));
-    const uint8_t* sa = ring + ks % NSTG * STB;
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      i32x4 xn;
-      if (i + 1 < MI) xn = frag_ko(sa, 16 * (2 * (i + 1) + wm), kl);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) mfma_bf16_tied(acc[i][j], wf[j], xf);
-      __builtin_amdgcn_sched_barrier(0);
-      if (i + 1 < MI) xf = xn;
-    }
-    if (ks + 1 < nk) {
-      const uint8_t* na = ring + (ks + 1) % NSTG * STB;
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) wf[j] = frag_ko(na + OPB, 64 * wn + 16 * j, kl);
-      xf = frag_ko(na, 16 * wm, kl);
-      block_barrier();
-    }
-  }
-  acc_fence(acc);
-}
-
-__global__ __launch_bounds__(bt::THREADS, 1) void loss_dw_kernel(LossArgs a) {
-  using namespace bt;
-  __shared__ __attribute__((aligned(1024))) uint8_t ring[NSTG * STB];
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[dense::RING_BYTES];
   const int count = a.count[0];
   if (!MOE_CHECK(count >= 0 && count <= a.T, 709)) return;
+  const TileWalk walk(ceil_div(a.v_len, LT), ceil_div(a.d, LT));
+  const int n = walk.count(), nk = ceil_div(count, 32);
   int vt, nt;
-  if (!loss_tile(ceil_div(a.v_len, BT), ceil_div(a.d, BT), vt, nt)) return;
-  const int n0 = nt * BT, v0 = a.v_first + vt * BT, vrows = min(BT, a.V - v0), ncols = min(BT, a.d - n0);
-  const uint32_t ldg = a.ldg * 2, ldh = a.d * 2;
-  const int nk = ceil_div(count, 32);
-  f32x4 acc[MI][NJ];
-  zero_acc(acc);
-  if (wave_id() >= NMW) {
-    const Opnd oa = opnd_ko(make_rsrc(a.g, count * ldg), ldg, vt * BT);
-    const Opnd ob = opnd_ko(make_rsrc(a.hc, count * ldh), ldh, n0);
-    mainloop_ko(ring, oa, ob, nk, acc);
-  } else {
-    mainloop_ko(ring, Opnd{}, Opnd{}, nk, acc);
-  }
-  const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4, wm = w % 2, wn = w / 2;
-  wait_vm_lgkm0<0>();
-  block_barrier();   // every wave is done with the ring
-  if (a.dw_fmt == FMT_BF16) {
-    constexpr int PITCH = BT * 2 + 16;
-    if (w < NMW) {
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-          *reinterpret_cast<uint2*>(ring + (16 * (2 * i + wm) + lr) * PITCH + (64 * wn + 16 * j + 4 * lg) * 2) =
-              pack4(acc[i][j]);
+  if (wave_id() >= dense::NMW) {
+    const uint32_t ldg = a.ldg * 2, ldh = a.d * 2;
+    dense::Opnd oa, ob;
+    auto head = [&](int i) {
+      walk.tile(i, vt, nt);
+      oa = dense::opnd_ko(make_rsrc(a.g, count * ldg), ldg, vt * LT);
+      ob = dense::opnd_ko(make_rsrc(a.hc, count * ldh), ldh, nt * LT);
+      dense::load_head<4>(ring, oa, ob, nk);
+    };
+    if (n > 0) head(0);
+    for (int i = 0; i < n; ++i) {
+      dense::load_body<4>(ring, oa, ob, nk);
+      block_barrier();   // the tile's stages are read
+      if (i + 1 < n) head(i + 1);
     }
-    wait_vm_lgkm0<0>();
-    block_barrier();
-    store_tile_from_lds<BT, PITCH, THREADS>(ring, vrows, ncols,
-                                            static_cast<uint16_t*>(a.dw) + static_cast<size_t>(v0) * a.d + n0, a.d);
     return;
   }
-  // fp32: rows 0-127, then 128-255
-  constexpr int PITCH = BT * 4 + 16;
-  static_assert(128 * PITCH <= NSTG * STB, "half a tile fits the ring");
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    if (half > 0) {
-      wait_vm_lgkm0<0>();
-      block_barrier();
+  const int w = wave_id(), wm = w % 2, wn = w / 2;
+  for (int i = 0; i < n; ++i) {
+    walk.tile(i, vt, nt);
+    const int v0 = a.v_first + vt * LT, vrows = min(LT, a.V - v0), n0 = nt * LT + 64 * wn, ncols = min(64, a.d - n0);
+    Acc acc;
+    dense::mfma_loop<KO, KO, 8>(ring, nk, acc);
+    block_barrier();   // the tile's stages are read
+    if (ncols <= 0) continue;
+    if (a.dw_fmt == FMT_BF16) {
+      uint16_t* dst = static_cast<uint16_t*>(a.dw) + static_cast<size_t>(v0) * a.d + n0;
+      dense::store_bf16_tile<8>(
+          ring, ncols, [&](int k, int j) { return pack4(acc[k][j]); },
+          [&](int row) -> uint16_t* { return row < vrows ? dst + static_cast<size_t>(row) * a.d : nullptr; });
+      continue;
     }
-    if (w < NMW) {
+    // fp32: 16 rows x 64 columns at a time through the wave's staging, 256-byte rows
+    float* dst = static_cast<float*>(a.dw) + static_cast<size_t>(v0) * a.d + n0;
+    uint8_t* sg = ring + dense::SPARE + 4096 * w;
+    const int lane = dense::fresh_lane(), lr = lane & 15, lg = lane >> 4;
 #pragma unroll
-      for (int i = 0; i < MI / 2; ++i)
+    for (int k = 0; k < MI; ++k) {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
-          *reinterpret_cast<f32x4*>(ring + (16 * (2 * i + wm) + lr) * PITCH + (64 * wn + 16 * j + 4 * lg) * 4) =
-              acc[i + half * MI / 2][j];
-    }
-    wait_vm_lgkm0<0>();
-    block_barrier();
-    float* dst = static_cast<float*>(a.dw) + static_cast<size_t>(v0 + 128 * half) * a.d + n0;
-    for (int idx = threadIdx.x; idx < 128 * 64; idx += THREADS) {
-      const int r = idx / 64, c = 4 * (idx % 64);
-      if (128 * half + r < vrows && c < ncols)
-        *reinterpret_cast<f32x4*>(dst + static_cast<size_t>(r) * a.d + c) =
-            *reinterpret_cast<const f32x4*>(ring + r * PITCH + c * 4);
+      for (int j = 0; j < NJ; ++j)
+        *reinterpret_cast<f32x4*>(sg + lr * 256 + (((4 * j + lg) ^ lr) << 4)) = acc[k][j];
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int rr = 4 * q + (lane >> 4), c = lane & 15, row = 16 * (2 * k + wm) + rr;
+        const f32x4 v = *reinterpret_cast<const f32x4*>(sg + rr * 256 + ((c ^ rr) << 4));
+        if (row < vrows && 4 * c < ncols)
+          *reinterpret_cast<f32x4*>(dst + static_cast<size_t>(row) * a.d + 4 * c) = v;
+      }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     }
   }
 }
@@ -524,24 +516,6 @@ __global__ __launch_bounds__(bt::THREADS, 1) void loss_dw_kernel(LossArgs a) {
 
 MOE_DEBUG_FILE(loss)
 
-int loss_splits(long long T, long long d, long long piece) {
-  // the split count with the least of: rounds of 256 tiles at about 0.9 us per
-  // 32-column step, and the splits' fp32 rows written and read at 4 TB/s
-  const long long tiles = ((T + LT - 1) / LT) * ((d + LT - 1) / LT);
-  int best = 1;
-  double least = 0;
-  for (int s = 1; s <= 64 && s * 256 <= piece; ++s) {
-    const double rounds = static_cast<double>((tiles * s + 255) / 256);
-    const double steps = static_cast<double>((piece + s - 1) / s + 31) / 32;
-    const double us = rounds * steps * 0.9 + static_cast<double>(s) * T * d * 8 / 4e6;
-    if (s == 1 || us < least) {
-      best = s;
-      least = us;
-    }
-  }
-  return best;
-}
-
 hipError_t launch_loss_rows(const LossArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(loss_rows_kernel, dim3(1), dim3(1024), 0, s, a);
   return hipGetLastError();
@@ -549,7 +523,7 @@ hipError_t launch_loss_rows(const LossArgs& a, hipStream_t s) {
 
 hipError_t launch_loss_forward(const LossArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(loss_logits_kernel<false>, dim3(loss_grid(ceil_div(a.T, LT), ceil_div(a.v_len, LT))),
-                     dim3(LTHREADS), 0, s, a);
+                     dim3(dense::THREADS), 0, s, a);
   hipLaunchKernelGGL(loss_finish_kernel, dim3(ceil_div(a.T, 4)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
@@ -563,10 +537,10 @@ hipError_t launch_loss_gather(const LossArgs& a, hipStream_t s) {
 hipError_t launch_loss_piece(const LossArgs& a, hipStream_t s) {
   const long long nm = ceil_div(a.T, LT), nv = ceil_div(a.v_len, LT), nn = ceil_div(a.d, LT);
   if (a.T > 0) {
-    hipLaunchKernelGGL(loss_logits_kernel<true>, dim3(loss_grid(nm, nv)), dim3(LTHREADS), 0, s, a);
-    hipLaunchKernelGGL(loss_dh_kernel, dim3(loss_grid(nm, nn * a.splits)), dim3(bt::THREADS), 0, s, a);
+    hipLaunchKernelGGL(loss_logits_kernel<true>, dim3(loss_grid(nm, nv)), dim3(dense::THREADS), 0, s, a);
+    hipLaunchKernelGGL(loss_dh_kernel, dim3(loss_grid(nm, nn * LOSS_SPLITS)), dim3(dense::THREADS), 0, s, a);
   }
-  hipLaunchKernelGGL(loss_dw_kernel, dim3(loss_grid(nv, nn)), dim3(bt::THREADS), 0, s, a);
+  hipLaunchKernelGGL(loss_dw_kernel, dim3(loss_grid(nv, nn)), dim3(dense::THREADS), 0, s, a);
   return hipGetLastError();
 }
 

@@ -25,7 +25,7 @@ int validate_shape(const moe_loss_shape* s) {
 struct Layout {
   size_t rows, pos, count, part, zlab, forward_total;
   size_t hc, g, acc, backward_total;
-  int piece, splits;
+  int piece;
 };
 
 Layout make_layout(const moe_loss_shape& s) {
@@ -33,7 +33,7 @@ Layout make_layout(const moe_loss_shape& s) {
   const size_t T = static_cast<size_t>(s.T), nv = (static_cast<size_t>(s.V) + 255) / 256;
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o += align_up(bytes); return at; };
-  L.count = take(4);
+  L.count = take(8);
   L.rows = take(T * 4);
   L.pos = take(T * 4);
   const size_t shared = o;
@@ -42,10 +42,9 @@ Layout make_layout(const moe_loss_shape& s) {
   L.forward_total = o;
   o = shared;
   L.piece = moe::loss_piece(s.T, s.d, s.V);
-  L.splits = moe::loss_splits(s.T, s.d, L.piece);
   L.hc = take(T * s.d * 2);
   L.g = take(T * L.piece * 2);
-  L.acc = take(static_cast<size_t>(L.splits) * T * s.d * 4);
+  L.acc = take(static_cast<size_t>(moe::loss_acc_rows(s.T, s.d, L.piece)) * s.d * 4);
   L.backward_total = o;
   return L;
 }
@@ -121,7 +120,6 @@ int moe_vocab_loss_backward(const moe_loss_shape* shape, const void* h, const vo
   a.g = at<uint16_t>(workspace, L.g);
   a.acc = at<float>(workspace, L.acc);
   a.ldg = L.piece;
-  a.splits = L.splits;
   a.dh_fmt = fmt_of(s.dh_dtype);
   a.dw_fmt = fmt_of(s.dw_dtype);
   a.dh = dh;
