@@ -90,19 +90,20 @@ __device__ __forceinline__ Opnd opnd_ko(rsrc_t r, uint32_t ld, int col0) {
 __device__ __forceinline__ uint8_t* stage(uint8_t* ring, int s) { return ring + (s % NST) * STB; }
 
 // The pair of K-steps s, s + 1: its first (HALF 0) or second half.  Of A only
-// the first NA groups of 64 rows are loaded (KC, for a tile of at most 64 NA rows).
+// the first NA groups of 64 rows are loaded (KC, for a tile of at most 64 NA
+// rows).  A tile of up to 64 rows is bound by memory, not by the loads' issue:
+// all of a pair is its first half.
 template <int NA>
-constexpr int half_ops(int half) {
-  return 2 * ((half + 1) * (NA + NLI) / 2 - half * (NA + NLI) / 2);
+constexpr int first_ops() {
+  return NA == 1 ? NA + NLI : (NA + NLI) / 2;
 }
 template <int HALF, int NA>
 __device__ __forceinline__ void issue_half(const Opnd& a, const Opnd& b, uint8_t* ring, int s) {
   const int w = wave_id() - NMW;
   uint8_t* s0 = stage(ring, s) + 1024 * w;
   uint8_t* s1 = stage(ring, s + 1) + 1024 * w;
-  constexpr int N = NA + NLI;
 #pragma unroll
-  for (int k = HALF * N / 2; k < (HALF + 1) * N / 2; ++k) {
+  for (int k = HALF == 0 ? 0 : first_ops<NA>(); k < (HALF == 0 ? first_ops<NA>() : NA + NLI); ++k) {
     // B's groups between A's
     const bool is_a = NA == NLI ? k % 2 == 0 : k < NA;
     const int q = NA == NLI ? k / 2 : (is_a ? k : k - NA);
@@ -219,11 +220,11 @@ __device__ __forceinline__ void load_head(uint8_t* ring, const Opnd& a, const Op
 }
 template <int NA>
 __device__ __forceinline__ void load_body(uint8_t* ring, const Opnd& a, const Opnd& b, int nk) {
-  constexpr int H0 = half_ops<NA>(0), H1 = half_ops<NA>(1);
+  constexpr int H0 = 2 * first_ops<NA>(), N = 2 * (NA + NLI);
   const int np = (nk + 1) / 2;
   if (np <= 0) return;
   if (np > 1)
-    wait_vm<H0 + H1>();   // pair 0
+    wait_vm<N>();   // pair 0
   else
     wait_vm<0>();
   block_barrier();

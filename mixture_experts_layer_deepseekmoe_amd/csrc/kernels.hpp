@@ -281,7 +281,8 @@ struct LossArgs {
   float* loss;            // [T] (forward)
   float* lse;             // [T] (backward: read)
   // forward
-  float2* part;           // [T][ceil(V / 256)] each row's (max, sum exp(l - max)) by tile
+  float2* part;           // [T][tiles] each row's (max, sum exp(l - max)) by tile
+  int tiles;              // loss_tiles(...)
   float* zlab;            // [T] the label's logit by row
   // backward
   const float* dloss;     // [T]
@@ -298,6 +299,14 @@ struct LossArgs {
 };
 
 constexpr int LOSS_TILE = 256;    // rows and columns of a tile
+// The forward of few tokens (loss_stream_kernel, tiles of 64 entries) against
+// the tile pipeline, measured: 1 token, V = 32000, d = 2048: 34 / 47 us; 20,
+// 65536, 2048: 66 / 73; 40, 16000, 2048: 21 / 33; 40, 24000, 2048: 37 / 39; but
+// 64, 32000, 4096: 79 / 73 and 37, 50001, 7168: 192 / 140 (its blocks read the
+// hidden rows again for every 64 entries).
+constexpr int LOSS_STREAM_TILE = 64;
+inline bool loss_stream(int T, int V) { return T <= 32 || (T <= 64 && V <= 16384); }
+inline int loss_tiles(int T, int V) { return ceil_div(V, loss_stream(T, V) ? LOSS_STREAM_TILE : LOSS_TILE); }
 
 // The backward's pieces of the vocabulary: as many whole tiles of columns as
 // keep G within LOSS_G_BYTES (and a piece of w within 2^31 bytes).

@@ -4,13 +4,13 @@
 //   G_tv = (dloss_t + dlse_t) exp(l_tv - lse_t) - dloss_t [v = label_t]
 //   dh = G w,  dw = G^T h
 //
-// forward   256 x 256 tiles of logits stay in the accumulators; a tile leaves
-//           one (max, sum of exponentials) per row, which a second kernel
-//           joins in tile order.
-// backward  the vocabulary in pieces: the piece's logits are computed again
-//           (bit for bit as in the forward), turned into G (bf16, a piece of
-//           at most 512 MB) in the epilogue, and multiplied into dh (fp32, added
-//           up over the pieces) and the piece's rows of dw.
+// forward   256 x 256 tiles of logits (64 entries for few tokens) stay in
+//           the accumulators; a tile leaves one (max, sum of exponentials) per
+//           row, which a second kernel joins.
+// backward  the vocabulary in pieces: the piece's logits are computed again,
+//           turned into G (bf16, a piece of at most 512 MB) in the epilogue, and
+//           multiplied into dh (fp32, added up over the pieces) and the piece's
+//           rows of dw.
 //
 // Only tokens with a label in [0, V) are rows of these products; the others
 // (their hidden rows may hold anything) cost nothing, and their loss, lse and
@@ -202,7 +202,7 @@ __device__ __forceinline__ void stats_epilogue(const LossArgs& a, const Acc& acc
       const float2 p = red[k][r];
       s += p.x == NEG_INF ? p.y : p.y * __expf(p.x - m);
     }
-    a.part[static_cast<size_t>(rt.row0 + r) * ceil_div(a.V, LT) + vt] = make_float2(m, s);
+    a.part[static_cast<size_t>(rt.row0 + r) * a.tiles + vt] = make_float2(m, s);
   }
 #pragma unroll
   for (int i = 0; i < NSUB; ++i) {
@@ -323,26 +323,136 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_logits_kernel(LossArgs
   }
 }
 
-// Joins a row's tiles, one wave per row: lane k takes tiles k, k + 64, ..., and
-// a butterfly joins the lanes (max and rescaled sum: the same in either order).
+// ------------------------------------------------------------------ logits of few tokens
+
+// Up to 64 tokens (scoring, decoding): the time is that of reading w once.  A
+// block takes 64 entries of the vocabulary; its 8 waves share K, pairs of
+// K-steps (the 128-byte lines of 64 rows) in turn, straight from memory into
+// MFMA fragments, and add their partial logits through LDS in order.  Several
+// such blocks fit a CU, with a pair of every wave in flight (8 KB); the tile
+// pipeline has one block to a CU and at most 64 KB of w in flight.  (Two pairs
+// in flight per wave cost a block its place on the CU: 20 tokens 66 -> 71 us.)
+constexpr int SV = LOSS_STREAM_TILE, STHREADS = 512;
+
+template <int NT>
+__global__ __launch_bounds__(STHREADS) void loss_stream_kernel(LossArgs a) {
+  __shared__ float red[8][16 * NT][SV + 4];
+  __shared__ int rows[16 * NT], labs[16 * NT];
+  const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  // the rows, as loss_rows_kernel lists them (one lane a token)
+  const int lab = lane < a.T ? a.labels[lane] : -1;
+  const bool ok = lab >= 0 && lab < a.V;
+  const unsigned long long valid = __ballot(ok);
+  const int count = __popcll(valid), at = __popcll(valid & ((1ULL << lane) - 1));
+  if (w == 0 && ok) {
+    rows[at] = lane;
+    labs[at] = lab;
+  }
+  if (blockIdx.x == 0 && w == 0) {
+    if (ok)
+      a.rows[at] = lane;
+    else if (lane < a.T)
+      a.loss[lane] = a.lse[lane] = 0.f;
+    if (lane == 0) a.count[0] = count;
+  }
+  __syncthreads();
+  if (count == 0) return;
+
+  const int v0 = blockIdx.x * SV, nv = min(SV, a.V - v0);
+  const uint32_t ld = a.d * 2;
+  const rsrc_t rw = make_rsrc(a.w + static_cast<size_t>(v0) * a.d, nv * ld);   // entries past V: zeros
+  const rsrc_t rh = make_rsrc(a.h, a.T * ld);
+  uint32_t ow[4], oh[NT];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) ow[s] = (16 * s + lr) * ld + 16 * lg;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) oh[t] = (16 * t + lr < count ? rows[16 * t + lr] : a.T) * ld + 16 * lg;   // past: zeros
+  f32x4 acc[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int s = 0; s < 4; ++s) acc[t][s] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto load = [](rsrc_t r, uint32_t off, uint32_t soff) {
+    return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, 0));
+  };
+  const int np = a.d / 64;
+#pragma unroll 2
+  for (int p = w; p < np; p += 8) {
+    i32x4 wf[2][4], hf[2][NT];
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) wf[k][s] = load(rw, ow[s], 128 * p + 64 * k);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) hf[k][t] = load(rh, oh[t], 128 * p + 64 * k);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) acc[t][s] = mfma_bf16(wf[k][s], hf[k][t], acc[t][s]);
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int s = 0; s < 4; ++s) *reinterpret_cast<f32x4*>(&red[w][16 * t + lr][16 * s + 4 * lg]) = acc[t][s];
+  __syncthreads();
+  // 16 lanes to a row, 4 columns each
+  for (int r = threadIdx.x >> 4; r < count; r += STHREADS / 16) {
+    const int c = 4 * (threadIdx.x & 15);
+    f32x4 l = *reinterpret_cast<const f32x4*>(&red[0][r][c]);
+#pragma unroll
+    for (int k = 1; k < 8; ++k) l += *reinterpret_cast<const f32x4*>(&red[k][r][c]);
+    float m = NEG_INF;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + e < nv) m = fmaxf(m, l[e]);
+    m = wave_max_16(m);
+    const float mb = m == NEG_INF ? 0.f : m;
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + e < nv) s += __expf(l[e] - mb);
+#pragma unroll
+    for (int off = 1; off < 16; off <<= 1) s += __shfl_xor(s, off);
+    if (c == 0) a.part[static_cast<size_t>(r) * a.tiles + blockIdx.x] = make_float2(m, s);
+    const int z = labs[r] - v0 - c;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (z == e) a.zlab[r] = l[e];
+  }
+}
+
+// Joins a row's tiles, WPR waves to a row: a thread takes every 64 WPR-th tile, a
+// butterfly joins the lanes and the waves follow in order (max and rescaled
+// sum: a butterfly's halves give the same).
+template <int WPR>
 __global__ __launch_bounds__(256) void loss_finish_kernel(LossArgs a) {
+  __shared__ float2 s[4];
   const int count = a.count[0];
-  const int r = blockIdx.x * 4 + wave_id(), lane = threadIdx.x & 63;
-  if (r >= count) return;
-  const int nv = ceil_div(a.V, LT);
-  const float2* p = a.part + static_cast<size_t>(r) * nv;
+  const int w = wave_id(), lane = threadIdx.x & 63, r = blockIdx.x * (4 / WPR) + w / WPR;
   auto join = [](float2 p, float2 q) {
     const float m = fmaxf(p.x, q.x);
     const float sp = p.x == NEG_INF ? p.y : p.y * expf(p.x - m);
     const float sq = q.x == NEG_INF ? q.y : q.y * expf(q.x - m);
     return make_float2(m, sp + sq);
   };
-  float2 v = make_float2(NEG_INF, 0.f);
+  if (r < count) {
+    const float2* p = a.part + static_cast<size_t>(r) * a.tiles;
+    float2 v = make_float2(NEG_INF, 0.f);
 #pragma unroll 4
-  for (int t = lane; t < nv; t += 64) v = join(v, p[t]);
+    for (int t = 64 * (w % WPR) + lane; t < a.tiles; t += 64 * WPR) v = join(v, p[t]);
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v = join(v, make_float2(__shfl_xor(v.x, off), __shfl_xor(v.y, off)));
-  if (lane != 0) return;
+    for (int off = 32; off >= 1; off >>= 1) v = join(v, make_float2(__shfl_xor(v.x, off), __shfl_xor(v.y, off)));
+    if (lane == 0) s[w] = v;
+  }
+  if constexpr (WPR > 1) __syncthreads();
+  if (r >= count || lane != 0 || w % WPR != 0) return;
+  float2 v = s[w];
+#pragma unroll
+  for (int k = 1; k < WPR; ++k) v = join(v, s[w + k]);
   const float lse = v.x + logf(v.y);
   const int t = a.rows[r];
   if (!MOE_CHECK(t >= 0 && t < a.T, 706)) return;
@@ -435,6 +545,7 @@ __global__ __launch_bounds__(256) void loss_dh_out_kernel(LossArgs a) {
   for (int c = 4 * threadIdx.x; c < a.d; c += 1024) {
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
     if (r >= 0)
+#pragma unroll 8
       for (int s = 0; s < splits; ++s)
         v += *reinterpret_cast<const f32x4*>(a.acc + (static_cast<size_t>(s) * nm * LT + r) * a.d + c);
     if (a.dh_fmt == FMT_F32)
@@ -522,9 +633,23 @@ hipError_t launch_loss_rows(const LossArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_loss_forward(const LossArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(loss_logits_kernel<false>, dim3(loss_grid(ceil_div(a.T, LT), ceil_div(a.v_len, LT))),
-                     dim3(dense::THREADS), 0, s, a);
-  hipLaunchKernelGGL(loss_finish_kernel, dim3(ceil_div(a.T, 4)), dim3(256), 0, s, a);
+  if (loss_stream(a.T, a.V)) {
+    if (a.T <= 16)
+      hipLaunchKernelGGL(loss_stream_kernel<1>, dim3(a.tiles), dim3(STHREADS), 0, s, a);
+    else if (a.T <= 32)
+      hipLaunchKernelGGL(loss_stream_kernel<2>, dim3(a.tiles), dim3(STHREADS), 0, s, a);
+    else if (a.T <= 48)
+      hipLaunchKernelGGL(loss_stream_kernel<3>, dim3(a.tiles), dim3(STHREADS), 0, s, a);
+    else
+      hipLaunchKernelGGL(loss_stream_kernel<4>, dim3(a.tiles), dim3(STHREADS), 0, s, a);
+    hipLaunchKernelGGL(loss_finish_kernel<4>, dim3(a.T), dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
+  const hipError_t e = launch_loss_rows(a, s);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(loss_logits_kernel<false>, dim3(loss_grid(ceil_div(a.T, LT), a.tiles)), dim3(dense::THREADS), 0, s,
+                     a);
+  hipLaunchKernelGGL(loss_finish_kernel<1>, dim3(ceil_div(a.T, 4)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -30,7 +30,7 @@ struct Layout {
 
 Layout make_layout(const moe_loss_shape& s) {
   Layout L{};
-  const size_t T = static_cast<size_t>(s.T), nv = (static_cast<size_t>(s.V) + 255) / 256;
+  const size_t T = static_cast<size_t>(s.T), nv = static_cast<size_t>(moe::loss_tiles(s.T, s.V));
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o += align_up(bytes); return at; };
   L.count = take(8);
@@ -94,10 +94,9 @@ int moe_vocab_loss(const moe_loss_shape* shape, const void* h, const void* w, co
   a.lse = lse;
   a.part = at<float2>(workspace, L.part);
   a.zlab = at<float>(workspace, L.zlab);
+  a.tiles = moe::loss_tiles(s.T, s.V);
   a.v_len = s.V;
-  int r = check_launch(moe::launch_loss_rows(a, stream));
-  if (r == MOE_OK) r = check_launch(moe::launch_loss_forward(a, stream));
-  return debug_status(r, stream, "moe_vocab_loss");
+  return debug_status(check_launch(moe::launch_loss_forward(a, stream)), stream, "moe_vocab_loss");
 }
 
 int moe_vocab_loss_backward(const moe_loss_shape* shape, const void* h, const void* w, const int32_t* labels,

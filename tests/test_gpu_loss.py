@@ -72,10 +72,13 @@ def _check(h, w, labels, dloss, dlse, dh_dtype="f32", dw_dtype="f32"):
     assert (_np(dh)[~keep] == 0).all()
 
 
-# one token; vocabularies of one entry, about a tile's 256 and not multiples of
-# anything; row counts about the 16-row subtiles and 256-row tiles
-SIZES = [(1, 64, 1), (1, 64, 256), (3, 128, 257), (15, 64, 1000), (17, 192, 255), (33, 2048, 300), (256, 256, 512),
-         (257, 320, 777), (300, 512, 4099), (513, 64, 300), (770, 192, 65), (40, 7168, 600)]
+# one token; vocabularies of one entry, about a tile's 64 and 256 and not
+# multiples of anything; row counts about the 16-row subtiles, the 64-row steps
+# and the 256-row tiles; few tokens on either forward (up to 64 with at most
+# 16384 entries, and more entries than that)
+SIZES = [(1, 64, 1), (1, 64, 256), (3, 128, 257), (15, 64, 1000), (17, 192, 255), (33, 2048, 300), (48, 64, 65),
+         (64, 320, 191), (50, 64, 16700), (100, 128, 300), (200, 64, 520), (256, 256, 512), (257, 320, 777),
+         (300, 512, 4099), (513, 64, 300), (770, 192, 65), (40, 7168, 600)]
 
 
 @pytest.mark.parametrize("T,d,V", SIZES)
