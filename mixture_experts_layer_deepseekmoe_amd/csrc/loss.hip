@@ -61,17 +61,25 @@ inline unsigned loss_grid(long long nm, long long nn) {
   return static_cast<unsigned>(NXCDS * (per < NBLOCKS / NXCDS ? per : NBLOCKS / NXCDS));
 }
 
-// m-tile m of `count` rows cut into nm = ceil(count / 256) nearly equal tiles
-// (whole 16-row subtiles but for the last).
+// The rows in n nearly equal tiles of `per` rows (whole 16-row subtiles; the last
+// takes what is left, at least one row): of at most 256 rows, and of down to 64
+// while the tiles, with nn column tiles, still fit one round of the CUs (207
+// rows, 10007 entries, d = 512, forward + backward: 90 -> 69 us; 256 rows over
+// 50001 entries in two rounds of 128-row tiles: 197 -> 259 us).
 struct RowTile {
   int row0, rows;
 };
-__device__ __forceinline__ int row_tiles(int count) { return (count + LT - 1) / LT; }
-__device__ __forceinline__ RowTile row_tile(int count, int nm, int m) {
-  const int per = ((count + nm - 1) / nm + 15) / 16 * 16;   // at most 256
-  const int r0 = m * per;
-  return {r0, min(per, count - r0)};
-}
+struct RowCut {
+  int n, per, count;
+  __device__ RowCut(int count_, int nn) : count(count_) {
+    const int least = (count + LT - 1) / LT, most = (count + 63) / 64;
+    const int want = max(least, min(most, NBLOCKS / nn));
+    per = want > 0 ? ((count + want - 1) / want + 15) / 16 * 16 : LT;
+    n = (count + per - 1) / per;
+  }
+  __device__ RowTile tile(int m) const { return {m * per, min(per, count - m * per)}; }
+};
+__device__ __forceinline__ int padded_rows(int count) { return (count + LT - 1) / LT * LT; }
 
 // Cost of s splits of dh's sum for nm x nn tiles: rounds of 256 tiles at about
 // 0.75 us per 32-column step, and the splits' fp32 tiles written and read at
@@ -82,6 +90,12 @@ __device__ inline float split_cost(int s, int nm, int nn, int piece) {
   if (s > 1 && (s * LT > piece || s * tiles > LOSS_SPLIT_TILES)) return 1e30f;
   const float rounds = static_cast<float>((tiles * s + NBLOCKS - 1) / NBLOCKS);
   return rounds * static_cast<float>(((piece + s - 1) / s + 31) / 32) * 0.75f + static_cast<float>(s) * tiles * 0.13f;
+}
+
+// dh's row tiles: fine ones would read w's piece again for every 64 rows, which
+// pays only where a piece is short.
+__device__ __forceinline__ RowCut dh_cut(int count, int d, int piece) {
+  return RowCut(count, piece <= 16384 ? min(4 * ceil_div(d, LT), NBLOCKS) : NBLOCKS);
 }
 
 // ------------------------------------------------------------------ rows
@@ -123,7 +137,7 @@ __global__ __launch_bounds__(1024) void loss_rows_kernel(LossArgs a) {
   // one lane per number of splits
   int best = lane + 1;
   static_assert(LOSS_SPLITS == 64, "one lane each");
-  float cost = split_cost(best, row_tiles(base), ceil_div(a.d, LT), a.ldg);
+  float cost = split_cost(best, dh_cut(base, a.d, a.ldg).n, ceil_div(a.d, LT), a.ldg);
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) {
     const float c = __shfl_xor(cost, off);
@@ -250,8 +264,9 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_logits_kernel(LossArgs
   __shared__ __attribute__((aligned(1024))) uint8_t ring[dense::RING_BYTES];
   const int count = a.count[0];
   if (!MOE_CHECK(count >= 0 && count <= a.T, 704)) return;
-  const int nm = row_tiles(count), nk = a.d / 32;
-  const TileWalk walk(nm, ceil_div(a.v_len, LT));
+  const int nk = a.d / 32;
+  const RowCut cut(count, ceil_div(a.v_len, LT));
+  const TileWalk walk(cut.n, ceil_div(a.v_len, LT));
   const int n = walk.count();
   const uint32_t ld = a.d * 2;
   if (wave_id() >= dense::NMW) {
@@ -262,7 +277,7 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_logits_kernel(LossArgs
     auto head = [&](int i) {
       int mt, vt;
       walk.tile(i, mt, vt);
-      rt = row_tile(count, nm, mt);
+      rt = cut.tile(mt);
       const int v0 = a.v_first + vt * LT;
       // rows past the tile's: an offset past the resource, so their loads
       // return zeros without touching memory
@@ -309,7 +324,7 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_logits_kernel(LossArgs
   for (int i = 0; i < n; ++i) {
     int mt, vt;
     walk.tile(i, mt, vt);
-    const RowTile rt = row_tile(count, nm, mt);
+    const RowTile rt = cut.tile(mt);
     const int ncol = min(LT, a.V - a.v_first - vt * LT);
     dense::with_rows(rt.rows, [&]<int NSUB>() {
       Acc acc;
@@ -476,15 +491,16 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_dh_kernel(LossArgs a) 
   __shared__ __attribute__((aligned(1024))) uint8_t ring[dense::RING_BYTES];
   const int count = a.count[0], splits = a.count[1];
   if (!MOE_CHECK(count >= 0 && count <= a.T && splits >= 1 && splits <= LOSS_SPLITS, 707)) return;
-  const int nm = row_tiles(count), nn = ceil_div(a.d, LT);
-  const TileWalk walk(nm, nn * splits);
+  const int nn = ceil_div(a.d, LT);
+  const RowCut cut = dh_cut(count, a.d, a.ldg);
+  const TileWalk walk(cut.n, nn * splits);
   const int n = walk.count();
   auto tile = [&](int i, RowTile& rt, Run& run, int& s, int& n0) {
     int mt, k;
     walk.tile(i, mt, k);
     s = k / nn;
     n0 = (k - s * nn) * LT;
-    rt = row_tile(count, nm, mt);
+    rt = cut.tile(mt);
     run = split_run(a.v_len, splits, s);
   };
   RowTile rt;
@@ -524,7 +540,7 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_dh_kernel(LossArgs a) 
       for (int i = 0; i < NSUB; ++i) {
         const int row = 16 * (2 * i + wm) + (lane & 15);
         if (row >= rt.rows) continue;
-        float* dst = a.acc + (static_cast<size_t>(s) * nm * LT + rt.row0 + row) * a.d;
+        float* dst = a.acc + (static_cast<size_t>(s) * padded_rows(count) + rt.row0 + row) * a.d;
 #pragma unroll
         for (int j = 0; j < bt::NJ; ++j) {
           const int col = n0 + 64 * wn + 16 * j + 4 * (lane >> 4);
@@ -540,14 +556,14 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_dh_kernel(LossArgs a) 
 // dh[t] = the sum of its row's splits, in order; zero for a token that is no row.
 __global__ __launch_bounds__(256) void loss_dh_out_kernel(LossArgs a) {
   const size_t t = blockIdx.x;
-  const int r = a.pos[t], nm = row_tiles(a.count[0]), splits = a.count[1];
+  const int r = a.pos[t], rows = padded_rows(a.count[0]), splits = a.count[1];
   if (!MOE_CHECK(r >= -1 && r < a.T && splits <= LOSS_SPLITS, 708)) return;
   for (int c = 4 * threadIdx.x; c < a.d; c += 1024) {
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
     if (r >= 0)
 #pragma unroll 8
       for (int s = 0; s < splits; ++s)
-        v += *reinterpret_cast<const f32x4*>(a.acc + (static_cast<size_t>(s) * nm * LT + r) * a.d + c);
+        v += *reinterpret_cast<const f32x4*>(a.acc + (static_cast<size_t>(s) * rows + r) * a.d + c);
     if (a.dh_fmt == FMT_F32)
       *reinterpret_cast<f32x4*>(static_cast<float*>(a.dh) + t * a.d + c) = v;
     else
@@ -647,7 +663,7 @@ hipError_t launch_loss_forward(const LossArgs& a, hipStream_t s) {
   }
   const hipError_t e = launch_loss_rows(a, s);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(loss_logits_kernel<false>, dim3(loss_grid(ceil_div(a.T, LT), a.tiles)), dim3(dense::THREADS), 0, s,
+  hipLaunchKernelGGL(loss_logits_kernel<false>, dim3(loss_grid(ceil_div(a.T, 64), a.tiles)), dim3(dense::THREADS), 0, s,
                      a);
   hipLaunchKernelGGL(loss_finish_kernel<1>, dim3(ceil_div(a.T, 4)), dim3(256), 0, s, a);
   return hipGetLastError();
@@ -660,7 +676,7 @@ hipError_t launch_loss_gather(const LossArgs& a, hipStream_t s) {
 
 // One piece: G, its part of dh, its rows of dw.
 hipError_t launch_loss_piece(const LossArgs& a, hipStream_t s) {
-  const long long nm = ceil_div(a.T, LT), nv = ceil_div(a.v_len, LT), nn = ceil_div(a.d, LT);
+  const long long nm = ceil_div(a.T, 64), nv = ceil_div(a.v_len, LT), nn = ceil_div(a.d, LT);
   if (a.T > 0) {
     hipLaunchKernelGGL(loss_logits_kernel<true>, dim3(loss_grid(nm, nv)), dim3(dense::THREADS), 0, s, a);
     hipLaunchKernelGGL(loss_dh_kernel, dim3(loss_grid(nm, nn * LOSS_SPLITS)), dim3(dense::THREADS), 0, s, a);

@@ -16,6 +16,7 @@ import pytest
 import torch
 
 import mixture_experts_layer_deepseekmoe_amd as moe
+from mixture_experts_layer_deepseekmoe_amd import binding as B
 from oracle import around_oracle as A
 from tests.parity import say
 
@@ -283,3 +284,27 @@ def test_block_binding_refuses():
         moe.moe_block_in_backward(shape, x.float(), w, moe.BlockSave())   # no rows, no checkpoint
     with pytest.raises(moe.MoEError):
         moe.moe_block_in(moe.BlockShape(4, 250), x[:, :250].contiguous(), w[:250].contiguous())
+
+
+def test_block_debug_build():
+    """The bounds-checked build gives the same bits."""
+    say("case: debug build, block ops")
+    T, d = 700, 640
+    shape = moe.BlockShape(T, d, gate_rows=90)
+    x, y, do = _make(1, T, d, "bf16").to(DEV), _make(2, T, d).to(DEV), _make(3, T, d).to(DEV)
+    w, gate = 1 + 0.1 * _make(4, 1, d)[0].to(DEV), _make(5, shape.gates, d).to(DEV)
+
+    def step():
+        save, nxt = moe.alloc_block_save(shape, e4m3=True), moe.alloc_block_save(shape, e4m3=True)
+        xo, nn = moe.moe_block_out(shape, x, y, w=w, gate=gate, skip=x, w_next=w, save=save, save_next=nxt)
+        return (xo, nn, save.codes, nxt.codes) + moe.moe_block_out_backward(shape, do, save, w=w, gate=gate) + \
+            moe.moe_block_in_backward(shape, do, w, nxt, dn_sub=do, do=do)
+
+    a = step()
+    prev = B.use_library(B.DEBUG_LIB_PATH)
+    try:
+        b = step()
+    finally:
+        B.restore_library(prev)
+    for p, q in zip(a, b):
+        assert torch.equal(p, q)

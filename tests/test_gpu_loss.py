@@ -270,3 +270,19 @@ def test_loss_binding_refuses():
     with pytest.raises(moe.MoEError) as e:
         moe.moe_vocab_loss(shape, h, w, labels, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
     assert e.value.code == B.MOE_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("T,d,V,masked", [(7, 128, 300, 0.3), (100, 192, 777, 0.3), (600, 512, 20000, 0.5),
+                                          (4096, 256, 2000, 0.1)])
+def test_loss_debug_build(T, d, V, masked):
+    """The bounds-checked build passes its index checks and gives the same bits."""
+    say(f"case: debug build, vocab_loss T={T} d={d} V={V}")
+    args = _make(T, T, d, V, masked)
+    a = _run(*args)
+    prev = B.use_library(B.DEBUG_LIB_PATH)
+    try:
+        b = _run(*args)
+    finally:
+        B.restore_library(prev)
+    for x, y in zip(a, b):
+        assert torch.equal(x, y)
