@@ -182,27 +182,33 @@ __device__ __forceinline__ void stats_epilogue(const LossArgs& a, const Acc& acc
   float2(*red)[LT] = reinterpret_cast<float2(*)[LT]>(ring + dense::SPARE);   // [4][256]
   const int* lab = reinterpret_cast<const int*>(ring + ROW_DATA);            // [256]
   const int w = wave_id(), lane = dense::fresh_lane(), lr = lane & 15, lg = lane >> 4, wm = w % 2, wn = w / 2;
+  auto stats = [&]<bool FULL>() {   // FULL: all 256 columns are there
 #pragma unroll
-  for (int i = 0; i < NSUB; ++i) {
-    float m = NEG_INF;
+    for (int i = 0; i < NSUB; ++i) {
+      float m = NEG_INF;
 #pragma unroll
-    for (int j = 0; j < bt::NJ; ++j)
+      for (int j = 0; j < bt::NJ; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (64 * wn + 16 * j + 4 * lg + e < ncol) m = fmaxf(m, acc[i][j][e]);
-    m = fmaxf(m, __shfl_xor(m, 16));
-    m = fmaxf(m, __shfl_xor(m, 32));
-    const float mb = m == NEG_INF ? 0.f : m;   // no column, or all of them -inf: the sum is 0
-    float s = 0.f;
+        for (int e = 0; e < 4; ++e)
+          if (FULL || 64 * wn + 16 * j + 4 * lg + e < ncol) m = fmaxf(m, acc[i][j][e]);
+      m = fmaxf(m, __shfl_xor(m, 16));
+      m = fmaxf(m, __shfl_xor(m, 32));
+      const float mb = m == NEG_INF ? 0.f : m;   // no column, or all of them -inf: the sum is 0
+      float s = 0.f;
 #pragma unroll
-    for (int j = 0; j < bt::NJ; ++j)
+      for (int j = 0; j < bt::NJ; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (64 * wn + 16 * j + 4 * lg + e < ncol) s += __expf(acc[i][j][e] - mb);
-    s += __shfl_xor(s, 16);
-    s += __shfl_xor(s, 32);
-    if (lg == 0) red[wn][16 * (2 * i + wm) + lr] = make_float2(m, s);
-  }
+        for (int e = 0; e < 4; ++e)
+          if (FULL || 64 * wn + 16 * j + 4 * lg + e < ncol) s += __expf(acc[i][j][e] - mb);
+      s += __shfl_xor(s, 16);
+      s += __shfl_xor(s, 32);
+      if (lg == 0) red[wn][16 * (2 * i + wm) + lr] = make_float2(m, s);
+    }
+  };
+  if (ncol == LT)
+    stats.template operator()<true>();
+  else
+    stats.template operator()<false>();
   wait_vm_lgkm0<0>();
   block_barrier();   // red and the row data are written
   const int r = 64 * w + lane;
@@ -239,24 +245,38 @@ __device__ __forceinline__ void grad_epilogue(const LossArgs& a, const Acc& acc,
   const float4* rd = reinterpret_cast<const float4*>(ring + ROW_DATA);
   const int w = wave_id(), lane = dense::fresh_lane(), lr = lane & 15, lg = lane >> 4, wm = w % 2, wn = w / 2;
   block_barrier();   // the row data are written
-  float4 d;
-  dense::store_bf16_tile<NSUB>(
-      ring, 64,
-      [&](int i, int j) {
-        if (j == 0) d = rd[16 * (2 * i + wm) + lr];
-        const int l = __float_as_int(d.w), col = 64 * wn + 16 * j + 4 * lg;
-        float g[4];
+  auto store = [&]<bool FULL>() {   // FULL: all 256 columns are there
+    float4 d;
+    int l = 0;
+    dense::store_bf16_tile<NSUB>(
+        ring, 64,
+        [&](int i, int j) {
+          const int col = 64 * wn + 16 * j + 4 * lg;
+          if (j == 0) {
+            d = rd[16 * (2 * i + wm) + lr];
+            l = __float_as_int(d.w);
+          }
+          float g[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          g[e] = d.y * __expf(acc[i][j][e] - d.x);
-          if (col + e == l) g[e] -= d.z;
-          if (col + e >= ncol) g[e] = 0.f;
-        }
-        return pack_bf16x4(g[0], g[1], g[2], g[3]);
-      },
-      [&](int row) -> uint16_t* {
-        return row < rt.rows ? a.g + static_cast<size_t>(rt.row0 + row) * a.ldg + vt * LT + 64 * wn : nullptr;
-      });
+          for (int e = 0; e < 4; ++e) {
+            g[e] = d.y * __expf(acc[i][j][e] - d.x);
+            if (!FULL && col + e >= ncol) g[e] = 0.f;
+          }
+          if ((l & ~3) == col) {   // the label is one of the four
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if ((l & 3) == e) g[e] -= d.z;
+          }
+          return pack_bf16x4(g[0], g[1], g[2], g[3]);
+        },
+        [&](int row) -> uint16_t* {
+          return row < rt.rows ? a.g + static_cast<size_t>(rt.row0 + row) * a.ldg + vt * LT + 64 * wn : nullptr;
+        });
+  };
+  if (ncol == LT)
+    store.template operator()<true>();
+  else
+    store.template operator()<false>();
 }
 
 template <bool GRAD>
