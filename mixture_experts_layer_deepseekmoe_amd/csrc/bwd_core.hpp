@@ -33,12 +33,9 @@ typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
 
 // K-outer stage rows are 512 bytes (256 bf16); the 16-byte chunk of a row is
-// xor-ed with a function of the K-row.  One transpose read takes 32 bytes, an
-// aligned pair of chunks, of each of 16 rows (8 g + j, g, j = 0..3): the xor
-// moves whole pairs, so that the 8 rows of each half of the wave fall on the 8
-// different pairs of the 256 bytes the LDS serves at once.  (Moving single
-// chunks, rows 2 j and 2 j + 1 fell on the same pair.)
-__device__ __forceinline__ int xko(int k) { return ((k & 3) << 1) | (((k >> 3) & 1) << 3); }
+// xor-ed with a function of the K-row that gives the 16 rows one transpose
+// read touches (8 g + j, g, j = 0..3) 16 different chunk positions.
+__device__ __forceinline__ int xko(int k) { return (k & 3) | (((k >> 3) & 3) << 2); }
 
 __device__ __forceinline__ i32x4 frag_kc(const uint8_t* op, int r0) {
   const int lane = threadIdx.x & 63;
