@@ -462,7 +462,7 @@ def _arg(t: Optional[torch.Tensor], name: str, dtype: str, *size: int) -> Option
     """Device pointer of an argument (None stays None) after a check of its type and size."""
     if t is None:
         return None
-    if t.dtype != _ARG_DT[dtype] or t.shape != size:
+    if t.dtype is not _ARG_DT[dtype] or t.shape != size:
         raise ValueError(f"{name}: expected {dtype} {list(size)}, got {t.dtype} {list(t.shape)}")
     return _ptr(t)
 

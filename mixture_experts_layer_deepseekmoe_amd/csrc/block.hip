@@ -370,46 +370,49 @@ __global__ __launch_bounds__(TPB) void block_bwd_kernel(BlockBwdArgs a) {
   }
 }
 
-// Column sums of part[first .. first + n) in a fixed order: 16 threads x 4
-// columns, 64 row lanes (row lane l takes rows l, l + 64, ...), the lanes' sums
-// added in order.  Block (x, g): columns 64 x .., rows g n ...
-//   finish_gates: s_g -> dgate[g] = w s_g, q[g] = gate[g] s_g (dw's summand)
-//   otherwise:    out[g] = s_g
+// Column sums of the blocks' rows in a fixed order: 16 threads x 4 columns, 64 row
+// lanes (row lane l takes rows l, l + 64, ...), the lanes' sums added in order.
+// Block (x, y): columns 64 x .., gates y n_gates .. of n rows each; per gate g
+//   s_g -> dgate[g] = w s_g,  and gate[g] s_g, summed over the block's gates into
+//   out[y]  (dw, or with one gate to a block its summands)
 struct ColSumArgs {
   const float* part;
-  int n, d;
+  int n, d, n_gates;
   const float* w;      // nullable: ones
   const float* gate;   // nullable: ones
   float* dgate;        // nullable
-  float* q;            // nullable
+  float* out;          // nullable
 };
 constexpr int CS_LANES = 64;
+constexpr int CS_GATES = 8;   // up to so many gates are summed by one launch
 __global__ __launch_bounds__(1024) void block_colsum_kernel(ColSumArgs a) {
-  __shared__ float4 s[CS_LANES][16];
+  __shared__ float4 s[2][CS_LANES][16];
   const int tc = threadIdx.x & 15, l = threadIdx.x >> 4;
-  const int c = 64 * blockIdx.x + 4 * tc;
-  const size_t g = blockIdx.y;
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (c < a.d) {
-    const float* p = a.part + g * a.n * a.d + c;
+  const int c = 64 * blockIdx.x + 4 * tc, col = 64 * blockIdx.x + threadIdx.x;
+  float dw = 0.f;
+  for (int k = 0; k < a.n_gates; ++k) {
+    const size_t g = static_cast<size_t>(blockIdx.y) * a.n_gates + k;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < a.d) {
+      const float* p = a.part + g * a.n * a.d + c;
 #pragma unroll 4
-    for (int r = l; r < a.n; r += CS_LANES) {
-      const float4 x = *reinterpret_cast<const float4*>(p + static_cast<size_t>(r) * a.d);
-      v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+      for (int r = l; r < a.n; r += CS_LANES) {
+        const float4 x = *reinterpret_cast<const float4*>(p + static_cast<size_t>(r) * a.d);
+        v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+      }
+    }
+    s[k & 1][l][tc] = v;
+    __syncthreads();
+    if (threadIdx.x < 64 && col < a.d) {   // one column each
+      const float* col_s = reinterpret_cast<const float*>(&s[k & 1][0][0]) + threadIdx.x;
+      float sum = 0.f;
+      const int lanes = min(a.n, CS_LANES);
+      for (int i = 0; i < lanes; ++i) sum += col_s[i * 64];
+      if (a.dgate != nullptr) a.dgate[g * a.d + col] = a.w != nullptr ? a.w[col] * sum : sum;
+      dw = fmaf(a.gate != nullptr ? a.gate[g * a.d + col] : 1.f, sum, dw);
     }
   }
-  s[l][tc] = v;
-  __syncthreads();
-  // 64 threads, one column each
-  if (threadIdx.x >= 64) return;
-  const int col = 64 * blockIdx.x + threadIdx.x;
-  if (col >= a.d) return;
-  const float* col_s = reinterpret_cast<const float*>(&s[0][0]) + threadIdx.x;
-  float sum = 0.f;
-  const int lanes = min(a.n, CS_LANES);
-  for (int i = 0; i < lanes; ++i) sum += col_s[i * 64];
-  if (a.dgate != nullptr) a.dgate[g * a.d + col] = a.w != nullptr ? a.w[col] * sum : sum;
-  if (a.q != nullptr) a.q[g * a.d + col] = a.gate != nullptr ? a.gate[g * a.d + col] * sum : sum;
+  if (threadIdx.x < 64 && col < a.d && a.out != nullptr) a.out[static_cast<size_t>(blockIdx.y) * a.d + col] = dw;
 }
 
 // f.template operator()<NV, TPB>() with TPB threads x NV vectors of 8 columns
@@ -492,14 +495,19 @@ hipError_t launch_block_bwd(BlockBwdArgs a, hipStream_t s) {
   const unsigned cb = static_cast<unsigned>(ceil_div(a.d, 64));
   if (p.whole_gates) {
     if (a.dw == nullptr) return hipSuccess;
-    const ColSumArgs c{a.part, static_cast<int>(p.blocks), a.d, nullptr, nullptr, nullptr, a.dw};
+    const ColSumArgs c{a.part, static_cast<int>(p.blocks), a.d, 1, nullptr, nullptr, nullptr, a.dw};
     hipLaunchKernelGGL(block_colsum_kernel, dim3(cb, 1), dim3(1024), 0, s, c);
     return hipGetLastError();
   }
   if (a.dw == nullptr && a.dgate == nullptr) return hipSuccess;
-  // per gate: dgate and the gate's summand of dw (dw itself where there is one gate)
+  if (p.gates <= CS_GATES) {
+    const ColSumArgs c{a.part, p.runs, a.d, static_cast<int>(p.gates), a.w, a.gate, a.dgate, a.dw};
+    hipLaunchKernelGGL(block_colsum_kernel, dim3(cb, 1), dim3(1024), 0, s, c);
+    return hipGetLastError();
+  }
+  // many gates: a block each, then the sum of their shares of dw
   float* q = a.part + static_cast<size_t>(p.blocks) * a.d;
-  const ColSumArgs c1{a.part, p.runs, a.d, a.w, a.gate, a.dgate, a.dw == nullptr ? nullptr : (p.gates == 1 ? a.dw : q)};
+  const ColSumArgs c1{a.part, p.runs, a.d, 1, a.w, a.gate, a.dgate, a.dw == nullptr ? nullptr : q};
   // the grid's second dimension holds at most 65535 gates
   for (long long g0 = 0; g0 < p.gates; g0 += 32768) {
     ColSumArgs cg = c1;
@@ -508,13 +516,13 @@ hipError_t launch_block_bwd(BlockBwdArgs a, hipStream_t s) {
     cg.part += go * p.runs;
     if (cg.gate != nullptr) cg.gate += go;
     if (cg.dgate != nullptr) cg.dgate += go;
-    if (cg.q != nullptr) cg.q += go;
+    if (cg.out != nullptr) cg.out += go;
     hipLaunchKernelGGL(block_colsum_kernel, dim3(cb, static_cast<unsigned>(n)), dim3(1024), 0, s, cg);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (a.dw != nullptr && p.gates != 1) {
-    const ColSumArgs c2{q, static_cast<int>(p.gates), a.d, nullptr, nullptr, nullptr, a.dw};
+  if (a.dw != nullptr) {
+    const ColSumArgs c2{q, static_cast<int>(p.gates), a.d, 1, nullptr, nullptr, nullptr, a.dw};
     hipLaunchKernelGGL(block_colsum_kernel, dim3(cb, 1), dim3(1024), 0, s, c2);
   }
   return hipGetLastError();
