@@ -9,7 +9,7 @@
 #include <cstdio>
 #endif
 
-#include "kernels.hpp"
+#include "around.hpp"
 
 namespace moe::api {
 

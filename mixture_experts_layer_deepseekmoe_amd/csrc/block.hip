@@ -20,7 +20,7 @@
 // loads of bf16, 16 lanes to a 128-column tile).  Statistics and sums are fp32
 // throughout, in a fixed order; outputs in bf16 are rounded once, at the
 // store.
-#include "kernels.hpp"
+#include "around.hpp"
 
 namespace moe {
 

@@ -25,22 +25,22 @@
 // issue the next tile's first two pairs (buffers 0-3) while the MFMA waves
 // finish the last one (through buffer 4: SPARE).
 //
-// Operands are K-contiguous (KC) or K-outer (KO) as in bwd_core.hpp.
+// Operands are K-contiguous (KC: rows of K) or K-outer (KO: rows along K, the M or N
+// index contiguous): read through the LDS transpose read, which gives a lane four
+// consecutive K values of its own column; two reads make an MFMA operand.
 #pragma once
 
-#include "bwd_core.hpp"
+#include "gemm_core.hpp"
 
 namespace moe {
 
 namespace dense {
 
-using bt::KC;
-using bt::KO;
-using bt::OPB;
-using bt::STB;
-using bt::MI;
-using bt::NJ;
+enum : int { KC = 0, KO = 1 };
 
+constexpr int OPB = 16384;          // bytes of one operand in a stage (256 x 32 bf16)
+constexpr int STB = 2 * OPB;        // stage bytes (A then B)
+constexpr int MI = 8, NJ = 4;       // accumulator subtiles per MFMA wave
 constexpr int NMW = 8;              // MFMA waves
 constexpr int NLW = 4;              // load waves
 constexpr int THREADS = 64 * (NMW + NLW);
@@ -48,6 +48,26 @@ constexpr int NST = 5;
 constexpr int RING_BYTES = NST * STB;
 constexpr int SPARE = 4 * STB;       // LDS offset of the buffer that no tile's first two pairs use
 constexpr int NLI = 4;              // DMA instructions per operand, stage and load wave
+
+// s_waitcnt vmcnt(N), and lgkmcnt(0), each alone
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+__device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (3 << 14)); }
+
+__device__ __forceinline__ uint2 pack4(float a, float b, float c, float d) {
+  return make_uint2(bf16x2(a, b), bf16x2(c, d));
+}
+
+// K-outer stage rows are 512 bytes (256 bf16); the 16-byte chunk of a row is
+// xor-ed with a function of the K-row.  One transpose read takes 32 bytes, an
+// aligned pair of chunks, of each of 16 rows (8 g + j, g, j = 0..3): the xor
+// moves whole pairs, so that the 8 rows of each half of the wave fall on the 8
+// different pairs of the 256 bytes the LDS serves at once (no bank conflicts;
+// moving single chunks there is about one per read, at the same time).
+__device__ __forceinline__ int xko(int k) { return ((k & 3) << 1) | (((k >> 3) & 1) << 3); }
 
 // One operand's loads (load waves only): a buffer resource over its valid bytes
 // (reads past it return zeros), per-lane byte offsets of the lane's NLI 16-byte
@@ -81,7 +101,7 @@ __device__ __forceinline__ Opnd opnd_ko(rsrc_t r, uint32_t ld, int col0) {
 #pragma unroll
   for (int q = 0; q < NLI; ++q) {
     const int k = 2 * (w + NLW * q) + lane / 32;
-    o.off[q] = k * ld + col0 * 2 + (((lane & 31) ^ bt::xko(k)) << 4);
+    o.off[q] = k * ld + col0 * 2 + (((lane & 31) ^ xko(k)) << 4);
   }
   o.kstride = 32 * ld;
   return o;
@@ -135,6 +155,9 @@ __device__ __forceinline__ int fresh_lane() {
 }
 
 typedef __attribute__((address_space(3))) i32x4 lds_i32x4;
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
 struct Lane {
   uint32_t a, b;
 };
@@ -142,8 +165,8 @@ template <int KA, int KB>
 __device__ __forceinline__ Lane make_lane(int wm, int wn) {
   const int lane = fresh_lane(), lr = lane & 15, lg = lane >> 4;
   const uint32_t kc = lr * 64 + ((lg ^ swz<64>(lr)) << 4);
-  // (bt::ko_lane)
-  const int k0 = 8 * lg + (lr >> 2), kbase = k0 * 512 + 8 * (lr & 1), ky = ((lr & 3) >> 1) ^ bt::xko(k0);
+  // KO: lane 16 g + c reads K-rows 8 g + c / 4 and + 4, columns 4 (c % 4) .. + 3 of a subtile
+  const int k0 = 8 * lg + (lr >> 2), kbase = k0 * 512 + 8 * (lr & 1), ky = ((lr & 3) >> 1) ^ xko(k0);
   Lane l;
   l.a = KA == KC ? kc + 1024 * wm : kbase + (((2 * wm) ^ ky) << 4);
   l.b = OPB + (KB == KC ? kc + 4096 * wn : kbase + (((8 * (wn & 1)) ^ ky) << 4) + 256 * (wn >> 1));
@@ -154,9 +177,9 @@ __device__ __forceinline__ i32x4 frag_at(uint32_t addr) {
   if constexpr (KIND == KC) {
     return *reinterpret_cast<const lds_i32x4*>(addr);
   } else {
-    const bt::bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(reinterpret_cast<bt::lds_bf16x4*>(addr));
-    const bt::bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(reinterpret_cast<bt::lds_bf16x4*>(addr + 4 * 512));
-    const bt::i32x2 a = __builtin_bit_cast(bt::i32x2, lo), b = __builtin_bit_cast(bt::i32x2, hi);
+    const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(reinterpret_cast<lds_bf16x4*>(addr));
+    const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(reinterpret_cast<lds_bf16x4*>(addr + 4 * 512));
+    const i32x2 a = __builtin_bit_cast(i32x2, lo), b = __builtin_bit_cast(i32x2, hi);
     return i32x4{a.x, a.y, b.x, b.y};
   }
 }

@@ -85,6 +85,57 @@ __device__ __forceinline__ int k_rotation(int nb, int nk) {
 
 constexpr int MAX_KB = 256;   // FP8: at most 256 scale blocks along K (d, I <= 32768)
 
+// The stage ring: NST stage buffers, one after the other in one LDS array
+// (the bf16 epilogue reuses it whole as its output tile).
+template <int NST>
+struct Ring {
+  uint8_t* s[NST];
+};
+
+template <int NST, int SBY>
+__device__ __forceinline__ Ring<NST> make_ring(uint8_t* base) {
+  Ring<NST> r;
+#pragma unroll
+  for (int i = 0; i < NST; ++i) r.s[i] = base + i * SBY;
+  return r;
+}
+
+// bf16 epilogue, second half: the block's output tile sits in LDS as rows of
+// COLS bf16 (PITCH bytes apart); every wave of the block copies it out in
+// 16-byte pieces, consecutive lanes along a row, so each store instruction
+// writes whole 128-byte lines.  (Written straight from the accumulators,
+// a store put 32 contiguous bytes per row and took ~14% of a down tile.)
+template <int COLS, int PITCH, int THREADS>
+__device__ __forceinline__ void store_tile_from_lds(const uint8_t* lds, int rows, int ncols, uint16_t* dst,
+                                                    size_t stride) {
+  constexpr int CPR = COLS / 8;   // 16-byte pieces per row
+  const int npr = ncols / 8;
+  for (int idx = threadIdx.x; idx < rows * CPR; idx += THREADS) {
+    const int r = idx / CPR, c = idx - r * CPR;
+    if (c < npr)
+      *reinterpret_cast<uint4*>(dst + static_cast<size_t>(r) * stride + c * 8) =
+          *reinterpret_cast<const uint4*>(lds + r * PITCH + c * 16);
+  }
+}
+
+__device__ __forceinline__ uint2 pack_bf16x4(float a, float b, float c, float d) {
+  return make_uint2(bf16x2(a, b), bf16x2(c, d));
+}
+
+// Calls f.template operator()<NSUB>() with NSUB = the number of row subtiles
+// the first of the WM wave rows computes: ceil(rows / (16 WM)), 1 .. MI.
+template <int MI, int WM, int N = 1, class F>
+__device__ __forceinline__ void dispatch_rows(int rows, F&& f) {
+  if constexpr (N >= MI) {
+    f.template operator()<MI>();
+  } else {
+    if (rows <= 16 * WM * N)
+      f.template operator()<N>();
+    else
+      dispatch_rows<MI, WM, N + 1>(rows, f);
+  }
+}
+
 // bf16: wave row wm computes the tile's 16-row subtiles wm, wm + WM, ...; when
 // the last of them is past the tile's rows, its waves compute one fewer than
 // the first wave row instead of a subtile of padding (the loads still cover

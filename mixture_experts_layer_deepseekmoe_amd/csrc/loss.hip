@@ -20,8 +20,8 @@
 // fp32 accumulation; statistics and dh's sums are fp32; G is rounded to bf16
 // once, as the operand of the two products that follow (a relative error of
 // 2^-9 per element, as for the bf16 operands of the layer's backward).
+#include "around.hpp"
 #include "dense_core.hpp"
-#include "kernels.hpp"
 
 namespace moe {
 
@@ -164,7 +164,7 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
 // ------------------------------------------------------------------ logits
 
 constexpr float NEG_INF = -__builtin_inff();
-using Acc = f32x4[bt::MI][bt::NJ];   // a wave's accumulators (dense_core.hpp)
+using Acc = f32x4[dense::MI][dense::NJ];   // a wave's accumulators (dense_core.hpp)
 
 // What the epilogues need of a tile's rows, in SPARE after the waves' staging:
 // one entry per row, written by the load waves.
@@ -187,7 +187,7 @@ __device__ __forceinline__ void stats_epilogue(const LossArgs& a, const Acc& acc
     for (int i = 0; i < NSUB; ++i) {
       float m = NEG_INF;
 #pragma unroll
-      for (int j = 0; j < bt::NJ; ++j)
+      for (int j = 0; j < dense::NJ; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (FULL || 64 * wn + 16 * j + 4 * lg + e < ncol) m = fmaxf(m, acc[i][j][e]);
@@ -196,7 +196,7 @@ __device__ __forceinline__ void stats_epilogue(const LossArgs& a, const Acc& acc
       const float mb = m == NEG_INF ? 0.f : m;   // no column, or all of them -inf: the sum is 0
       float s = 0.f;
 #pragma unroll
-      for (int j = 0; j < bt::NJ; ++j)
+      for (int j = 0; j < dense::NJ; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (FULL || 64 * wn + 16 * j + 4 * lg + e < ncol) s += __expf(acc[i][j][e] - mb);
@@ -231,7 +231,7 @@ __device__ __forceinline__ void stats_epilogue(const LossArgs& a, const Acc& acc
     const int c = lab[row];
     if (c < 0 || c >= ncol || c / 64 != wn || c / 4 % 4 != lg) continue;
 #pragma unroll
-    for (int j = 0; j < bt::NJ; ++j)
+    for (int j = 0; j < dense::NJ; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (c % 64 / 16 == j && c % 4 == e) a.zlab[rt.row0 + row] = acc[i][j][e];
@@ -267,7 +267,7 @@ __device__ __forceinline__ void grad_epilogue(const LossArgs& a, const Acc& acc,
             for (int e = 0; e < 4; ++e)
               if ((l & 3) == e) g[e] -= d.z;
           }
-          return pack_bf16x4(g[0], g[1], g[2], g[3]);
+          return dense::pack4(g[0], g[1], g[2], g[3]);
         },
         [&](int row) -> uint16_t* {
           return row < rt.rows ? a.g + static_cast<size_t>(rt.row0 + row) * a.ldg + vt * LT + 64 * wn : nullptr;
@@ -334,7 +334,7 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_logits_kernel(LossArgs
         reinterpret_cast<float4*>(ring + ROW_DATA)[r] = rd;
       else
         reinterpret_cast<int*>(ring + ROW_DATA)[r] = __float_as_int(rd.w);
-      wait_lgkm0();
+      dense::wait_lgkm0();
       if constexpr (GRAD) block_barrier();
       if (i + 1 < n) head(i + 1);
       if constexpr (!GRAD) block_barrier();
@@ -348,7 +348,7 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_logits_kernel(LossArgs
     const int ncol = min(LT, a.V - a.v_first - vt * LT);
     dense::with_rows(rt.rows, [&]<int NSUB>() {
       Acc acc;
-      dense::mfma_loop<bt::KC, bt::KC, NSUB>(ring, nk, acc);
+      dense::mfma_loop<dense::KC, dense::KC, NSUB>(ring, nk, acc);
       block_barrier();   // the tile's stages are read
       if constexpr (GRAD)
         grad_epilogue<NSUB>(a, acc, ring, vt, rt, ncol);
@@ -553,7 +553,7 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_dh_kernel(LossArgs a) 
     tile(t, rt, run, s, n0);
     dense::with_rows(rt.rows, [&]<int NSUB>() {
       Acc acc;
-      dense::mfma_loop<bt::KC, bt::KO, NSUB>(ring, ceil_div(run.len, 32), acc);
+      dense::mfma_loop<dense::KC, dense::KO, NSUB>(ring, ceil_div(run.len, 32), acc);
       block_barrier();   // the tile's stages are read
       const int lane = dense::fresh_lane();
 #pragma unroll
@@ -562,7 +562,7 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_dh_kernel(LossArgs a) 
         if (row >= rt.rows) continue;
         float* dst = a.acc + (static_cast<size_t>(s) * padded_rows(count) + rt.row0 + row) * a.d;
 #pragma unroll
-        for (int j = 0; j < bt::NJ; ++j) {
+        for (int j = 0; j < dense::NJ; ++j) {
           const int col = n0 + 64 * wn + 16 * j + 4 * (lane >> 4);
           if (col >= a.d) continue;
           f32x4* p = reinterpret_cast<f32x4*>(dst + col);
@@ -587,14 +587,14 @@ __global__ __launch_bounds__(256) void loss_dh_out_kernel(LossArgs a) {
     if (a.dh_fmt == FMT_F32)
       *reinterpret_cast<f32x4*>(static_cast<float*>(a.dh) + t * a.d + c) = v;
     else
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dh) + t * a.d + c) = pack_bf16x4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dh) + t * a.d + c) = dense::pack4(v[0], v[1], v[2], v[3]);
   }
 }
 
 // ------------------------------------------------------------------ dw = G^T h
 
 __global__ __launch_bounds__(dense::THREADS, 1) void loss_dw_kernel(LossArgs a) {
-  using namespace bt;
+  using namespace dense;
   __shared__ __attribute__((aligned(1024))) uint8_t ring[dense::RING_BYTES];
   const int count = a.count[0];
   if (!MOE_CHECK(count >= 0 && count <= a.T, 709)) return;
@@ -629,7 +629,7 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_dw_kernel(LossArgs a) 
     if (a.dw_fmt == FMT_BF16) {
       uint16_t* dst = static_cast<uint16_t*>(a.dw) + static_cast<size_t>(v0) * a.d + n0;
       dense::store_bf16_tile<8>(
-          ring, ncols, [&](int k, int j) { return pack4(acc[k][j]); },
+          ring, ncols, [&](int k, int j) { return pack4(acc[k][j][0], acc[k][j][1], acc[k][j][2], acc[k][j][3]); },
           [&](int row) -> uint16_t* { return row < vrows ? dst + static_cast<size_t>(row) * a.d : nullptr; });
       continue;
     }
