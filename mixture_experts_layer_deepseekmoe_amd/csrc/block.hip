@@ -371,8 +371,9 @@ __global__ __launch_bounds__(TPB) void block_bwd_kernel(BlockBwdArgs a) {
 }
 
 // Column sums of the blocks' rows in a fixed order: 16 threads x 4 columns, 64 row
-// lanes (row lane l takes rows l, l + 64, ...), the lanes' sums added in order.
-// Block (x, y): columns 64 x .., gates y n_gates .. of n rows each; per gate g
+// lanes (row lane l takes rows l, l + 64, ...); a wave's four row lanes are joined
+// by a butterfly, the 16 waves in order.  Block (x, y): columns 64 x .., gates y
+// n_gates .. of n rows each; per gate g
 //   s_g -> dgate[g] = w s_g,  and gate[g] s_g, summed over the block's gates into
 //   out[y]  (dw, or with one gate to a block its summands)
 struct ColSumArgs {
@@ -386,33 +387,44 @@ struct ColSumArgs {
 constexpr int CS_LANES = 64;
 constexpr int CS_GATES = 8;   // up to so many gates are summed by one launch
 __global__ __launch_bounds__(1024) void block_colsum_kernel(ColSumArgs a) {
-  __shared__ float4 s[2][CS_LANES][16];
-  const int tc = threadIdx.x & 15, l = threadIdx.x >> 4;
-  const int c = 64 * blockIdx.x + 4 * tc, col = 64 * blockIdx.x + threadIdx.x;
-  float dw = 0.f;
+  __shared__ float4 s[CS_GATES][16][16];
+  const int tc = threadIdx.x & 15, l = threadIdx.x >> 4, w = threadIdx.x >> 6;
+  const int c = 64 * blockIdx.x + 4 * tc;
+  const size_t g0 = static_cast<size_t>(blockIdx.y) * a.n_gates;
   for (int k = 0; k < a.n_gates; ++k) {
-    const size_t g = static_cast<size_t>(blockIdx.y) * a.n_gates + k;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (c < a.d) {
-      const float* p = a.part + g * a.n * a.d + c;
+      const float* p = a.part + (g0 + k) * a.n * a.d + c;
 #pragma unroll 4
       for (int r = l; r < a.n; r += CS_LANES) {
         const float4 x = *reinterpret_cast<const float4*>(p + static_cast<size_t>(r) * a.d);
         v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
       }
     }
-    s[k & 1][l][tc] = v;
-    __syncthreads();
-    if (threadIdx.x < 64 && col < a.d) {   // one column each
-      const float* col_s = reinterpret_cast<const float*>(&s[k & 1][0][0]) + threadIdx.x;
-      float sum = 0.f;
-      const int lanes = min(a.n, CS_LANES);
-      for (int i = 0; i < lanes; ++i) sum += col_s[i * 64];
-      if (a.dgate != nullptr) a.dgate[g * a.d + col] = a.w != nullptr ? a.w[col] * sum : sum;
-      dw = fmaf(a.gate != nullptr ? a.gate[g * a.d + col] : 1.f, sum, dw);
+#pragma unroll
+    for (int off = 16; off <= 32; off <<= 1) {
+      v.x += __shfl_xor(v.x, off);
+      v.y += __shfl_xor(v.y, off);
+      v.z += __shfl_xor(v.z, off);
+      v.w += __shfl_xor(v.w, off);
     }
+    if ((l & 3) == 0) s[k][w][tc] = v;
   }
-  if (threadIdx.x < 64 && col < a.d && a.out != nullptr) a.out[static_cast<size_t>(blockIdx.y) * a.d + col] = dw;
+  __syncthreads();
+  // one column to a thread
+  const int col = 64 * blockIdx.x + threadIdx.x;
+  if (threadIdx.x >= 64 || col >= a.d) return;
+  float dw = 0.f;
+  for (int k = 0; k < a.n_gates; ++k) {
+    const float* cs = reinterpret_cast<const float*>(&s[k][0][0]) + threadIdx.x;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum += cs[i * 64];
+    const size_t o = (g0 + k) * a.d + col;
+    if (a.dgate != nullptr) a.dgate[o] = a.w != nullptr ? a.w[col] * sum : sum;
+    dw = fmaf(a.gate != nullptr ? a.gate[o] : 1.f, sum, dw);
+  }
+  if (a.out != nullptr) a.out[static_cast<size_t>(blockIdx.y) * a.d + col] = dw;
 }
 
 // f.template operator()<NV, TPB>() with TPB threads x NV vectors of 8 columns

@@ -6,6 +6,8 @@
     python -m mixture_experts_layer_deepseekmoe_amd.profiling peaks
     # the vendor library (hipBLASLt through torch) on GEMMs of the same sizes -> profiles/library_reference.json:
     python -m mixture_experts_layer_deepseekmoe_amd.profiling library --workload bf16_d7168
+    # the operators around the layer (cases of perf/operators.py, by name; default: all of them):
+    python -m mixture_experts_layer_deepseekmoe_amd.profiling operators --case loss_train_d7168 --steps 3
     # turn rocprofv3's CSV output into the summaries kept under profiles/:
     python -m mixture_experts_layer_deepseekmoe_amd.profiling summarize --trace DIR --pmc DIR [DIR...] \
         --workload bf16_d7168 --out profiles
@@ -72,6 +74,31 @@ def _run(args):
         print(f"[profile] step {i} done", flush=True)
 
 
+def _operators(args):
+    """Runs cases of perf/operators.py with the framework's calls, on three sets of inputs in turn."""
+    sys.path.insert(0, ROOT)
+    import importlib.util
+
+    import torch
+
+    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
+    ops = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ops)
+    ops.own = True
+    if args.calibrate:   # the streaming kernel of known size, as in ``run``
+        src = torch.ones(CALIB_BYTES // 8, dtype=torch.float64, device="cuda")
+        torch.mul(src, 2.0, out=torch.empty_like(src))
+        del src
+    for case in ops.listed():
+        if args.case and case["name"] not in args.case:
+            continue
+        states = [ops.prepare(case, 1 + k) for k in range(3)]
+        for k in range(args.steps):
+            ops.run(states[k % 3])
+        torch.cuda.synchronize()
+        print(f"{case['name']}: {args.steps} passes", flush=True)
+
+
 def _short(name: str) -> str:
     for key in ("dgrad_down_kernel", "dgrad_gateup_kernel", "wgrad_down_kernel", "wgrad_gateup_kernel",
                 "wgrad8_down_kernel", "wgrad8_gateup_kernel", "colquant_kernel", "swiglu_bwd_kernel",
@@ -90,6 +117,8 @@ def _short(name: str) -> str:
             return key + fmt
     if name.startswith("void at::native::"):
         return "torch:" + name[len("void at::native::"):].split("<")[0].split("(")[0]
+    if "moe::(anonymous namespace)::" in name:   # the operators around the layer, with their template arguments
+        return name.split("moe::(anonymous namespace)::", 1)[1].split("(")[0]
     return name[:60]
 
 
@@ -295,6 +324,10 @@ def main():
     r.add_argument("--workload", default="bf16_d7168")
     r.add_argument("--steps", type=int, default=3)
     r.add_argument("--train", action="store_true", help="training steps (moe_forward_train + moe_backward)")
+    o = sub.add_parser("operators")
+    o.add_argument("--case", nargs="*")
+    o.add_argument("--steps", type=int, default=3)
+    o.add_argument("--calibrate", action="store_true")
     s = sub.add_parser("summarize")
     s.add_argument("--trace")
     s.add_argument("--pmc", nargs="*")
@@ -308,7 +341,7 @@ def main():
     lb.add_argument("--workload", default="bf16_d7168")
     lb.add_argument("--out", default=os.path.join(ROOT, "profiles"))
     args = ap.parse_args()
-    {"run": _run, "summarize": _summarize, "peaks": _peaks, "library": _library}[args.cmd](args)
+    {"run": _run, "operators": _operators, "summarize": _summarize, "peaks": _peaks, "library": _library}[args.cmd](args)
 
 
 if __name__ == "__main__":
