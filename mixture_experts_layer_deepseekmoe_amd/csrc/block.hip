@@ -101,17 +101,19 @@ __device__ __forceinline__ float rstd_of(float sumsq, int d, float eps) {
 }
 
 // The 1x128 tile that holds this thread's eight values (16 lanes to a tile):
-// scale amax / 448 (1 for an all-zero tile), codes of v * (448 * (1 / amax)).
+// scale amax / 448, codes of v * (448 * (1 / amax)).  A tile below 2^-119, where
+// that factor would overflow, counts as all zero: scale 1, zero codes.
 __device__ __forceinline__ void save_tile(const float (&v)[8], uint8_t* codes, float* scales, size_t row, int d, int c) {
   float m = 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
   m = wave_max_16(m);
-  const float inv = m == 0.f ? 0.f : 448.f * (1.f / m);
+  const bool none = m < 0x1p-119f;
+  const float inv = none ? 0.f : 448.f * (1.f / m);
   *reinterpret_cast<uint2*>(codes + row * d + c) =
       make_uint2(e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
                  e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
-  if ((threadIdx.x & 15) == 0) scales[row * (d / 128) + c / 128] = m == 0.f ? 1.f : m / 448.f;
+  if ((threadIdx.x & 15) == 0) scales[row * (d / 128) + c / 128] = none ? 1.f : m / 448.f;
 }
 
 __device__ __forceinline__ void decode8(const uint2 q, float s, float (&v)[8]) {

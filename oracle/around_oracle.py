@@ -48,14 +48,15 @@ def block_out(x, y, skip, w, gate, gate_rows: int, eps: float, res_scale: float)
 def checkpoint(v: np.ndarray):
     """(codes, scales, the values they stand for) of fp32 rows: per 1x128 tile,
     scale = fl32(amax / 448) and codes E4M3(fl32(v * fl32(448 * fl32(1 / amax))));
-    scale 1 and zero codes for an all-zero tile."""
+    scale 1 and zero codes for a tile of zeros (amax below 2^-119)."""
     v = np.asarray(v, F32)
     T, d = v.shape
     t = v.reshape(T, d // 128, 128)
     amax = np.abs(t).max(axis=2)
-    nz = np.where(amax == 0, F32(1), amax)
-    inv = np.where(amax == 0, F32(0), F32(448) * (F32(1) / nz)).astype(F32)
-    scales = np.where(amax == 0, F32(1), nz / F32(448)).astype(F32)
+    none = amax < F32(2.0 ** -119)
+    nz = np.where(none, F32(1), amax)
+    inv = np.where(none, F32(0), F32(448) * (F32(1) / nz)).astype(F32)
+    scales = np.where(none, F32(1), nz / F32(448)).astype(F32)
     codes = e4m3_encode((t * inv[:, :, None]).astype(F32))
     val = e4m3_decode(codes).astype(F64) * scales.astype(F64)[:, :, None]
     return codes.reshape(T, d), scales, val.reshape(T, d)

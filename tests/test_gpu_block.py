@@ -161,6 +161,10 @@ def test_checkpoints(T, d, y_dtype, skip):
     y[0, :128] = 0
     if skip:
         sk[0, :128] = 0   # an all-zero tile of z
+    if T > 1:   # tiles of tiny and of huge values
+        x[1, :128] = 2.0 ** -122
+        x[1, 1] = 0
+        x[T - 1, -128:] *= 2.0 ** 50
     w, wn, gate = 1 + 0.2 * _make(4, 1, d)[0], 1 + 0.2 * _make(5, 1, d)[0], 0.5 * _make(6, 1, d)
     s0, s1, s2 = (moe.alloc_block_save(shape, e4m3=True) for _ in range(3))
     moe.moe_block_in(shape, _dev(x), _dev(w), save=s0)
