@@ -49,13 +49,14 @@ constexpr int RING_BYTES = NST * STB;
 constexpr int SPARE = 4 * STB;       // LDS offset of the buffer that no tile's first two pairs use
 constexpr int NLI = 4;              // DMA instructions per operand, stage and load wave
 
-// s_waitcnt vmcnt(N), and lgkmcnt(0), each alone
+// s_waitcnt vmcnt(N) alone; and lgkmcnt(0), which LDS writes before it in the
+// program stay in front of (a wave's writes are done before a barrier after it)
 template <int N>
 __device__ __forceinline__ void wait_vm() {
   static_assert(N >= 0 && N < 64, "vmcnt range");
   __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
 }
-__device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (3 << 14)); }
+__device__ __forceinline__ void wait_lgkm0() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 __device__ __forceinline__ uint2 pack4(float a, float b, float c, float d) {
   return make_uint2(bf16x2(a, b), bf16x2(c, d));

@@ -215,7 +215,7 @@ __device__ __forceinline__ void stats_epilogue(const LossArgs& a, const Acc& acc
     stats.template operator()<true>();
   else
     stats.template operator()<false>();
-  wait_vm_lgkm0<0>();
+  dense::wait_lgkm0();
   block_barrier();   // red and the row data are written
   const int r = 64 * w + lane;
   if (r < rt.rows) {
