@@ -104,7 +104,7 @@ struct LossArgs {
   int T, d, V;
   int32_t* rows;          // [T] token of each row
   int32_t* pos;           // [T] row of each token, or -1
-  int32_t* count;         // [2] rows; splits of dh's sum (backward)
+  int32_t* count;         // [3] rows; backward: splits of dh's sum, the gradients' scale (fp32)
   float* loss;            // [T] (forward)
   float* lse;             // [T] (backward: read)
   // forward
@@ -114,8 +114,9 @@ struct LossArgs {
   // backward
   const float* dloss;     // [T]
   const float* dlse;      // [T], or null
-  uint16_t* hc;           // [T][d] the rows' hidden rows, one after the other
-  uint16_t* g;            // [T][ldg] a piece's G = dlogits
+  uint16_t* hc;           // [loss_k_rows(T)][d] the rows' hidden rows, one after the other
+  uint16_t* g;            // [loss_k_rows(T)][ldg] a piece's G = dlogits / scale
+  float* lab_lo;          // [T] by row: the rounding error of G at the label
   float* acc;             // [splits][row tiles of 256][d] dh by row (loss_acc_rows)
   int ldg;                // loss_piece
   int dh_fmt, dw_fmt;
@@ -145,6 +146,14 @@ inline int loss_piece(long long T, long long d, long long V) {
   if (n > nw) n = nw;
   if (n < LOSS_TILE) n = LOSS_TILE;
   return static_cast<int>(n < vt ? n : vt);
+}
+
+// dw = G^T h of up to 64 rows sums over 2 count rows: count .. 2 count - 1 hold
+// what rounding G to bf16 left, and the same hidden rows again.  The product is
+// bound by writing dw; this costs it one or two K-steps.
+constexpr int LOSS_LO_ROWS = 64;
+constexpr int loss_k_rows(int T) {   // the most there can be
+  return T < LOSS_LO_ROWS ? 2 * T : T < 2 * LOSS_LO_ROWS ? 2 * LOSS_LO_ROWS : T;
 }
 
 // dh = G w sums over the whole piece: few rows make few tiles, so the piece is

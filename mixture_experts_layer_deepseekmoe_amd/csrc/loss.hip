@@ -20,12 +20,23 @@
 // holds (1.75-1.95 GHz; 76% of the cycles in the logits' kernel are MFMAs).
 // 3072 rows, d = 7168, V = 65536 (2.89 TFLOP each): logits 2.05 ms (1.41
 // PFLOP/s; with the G epilogue 2.1), dh 2.2-2.3 ms (1.25-1.3), dw 2.4 ms (1.2).
-// hipBLASLt on 4096 rows of the same runs 1.23-1.26, 0.92-0.94 and 0.92-1.06 PFLOP/s on
+// Library products of the same with 4096 rows: 1.23-1.26, 0.92-0.94, 0.92-1.06 on
 // operands laid out as these are.  Few tokens are bound by reading w once.
 //
 // Products are bf16 with fp32 accumulation; statistics and dh's sums are fp32; G
-// is rounded to bf16 once, as the operand of the two products that follow (at
-// most 2^-8 of each element, as for the bf16 operands of the layer's backward).
+// is rounded to bf16 as the operand of the two products that follow (at most
+// 2^-9 of each element).  The label's element outweighs the rest of its row, so
+// its rounding is most of that error and, with few rows, does not average out:
+//   dh   each row's rounding error at its label times the label's row of w is
+//        added in fp32 where dh is written;
+//   dw   up to 64 rows are summed with their rounding errors (LOSS_LO_ROWS);
+//   both G is held over the mantissa of the largest dloss: with the equal
+//        weights of a mean the label's elements are p - 1, near a power of two,
+//        and not all off by the one rounding of the weight.
+// Against 64 bits, with bf16 outputs: 1.7e-3 normwise for dh and few rows (the
+// outputs' own rounding), 2.2e-3 for dw of many; 2.4e-3 without these three, and
+// up to 2.9e-3 for few rows.  They cost 2 us of 67 (207 rows, 10007 entries, d =
+// 512) and 0.5-1% of the large products.
 #include "around.hpp"
 #include "dense_core.hpp"
 
@@ -35,6 +46,7 @@ namespace {
 
 constexpr int LT = LOSS_TILE;
 constexpr int NXCDS = 8;
+constexpr float INF = __builtin_inff(), NEG_INF = -INF;
 
 // The tiles of nm x nn that this block takes.  They are walked in groups of 8
 // m-tiles (m fastest), so that the 32 tiles an XCD's CUs hold at once share 8
@@ -104,18 +116,25 @@ __device__ __forceinline__ RowCut dh_cut(int count, int d, int piece) {
   return RowCut(count, piece <= 16384 ? min(4 * ceil_div(d, LT), NBLOCKS) : NBLOCKS);
 }
 
+// Rows of dw's sum.
+__device__ __forceinline__ int k_rows(int count) { return count <= LOSS_LO_ROWS ? 2 * count : count; }
+
 // ------------------------------------------------------------------ rows
 
 // The tokens with a label in [0, V), in order (one block; 1024 tokens at a
-// time).  Forward: the others' loss and lse are zero.
+// time).  Forward: the others' loss and lse are zero.  Backward: also the splits
+// of dh's sum, and the scale that G is held over: the mantissa, in [1, 2), of
+// the largest finite |dloss| of a row (the range of G stays as it is).
 __global__ __launch_bounds__(1024) void loss_rows_kernel(LossArgs a) {
   __shared__ int wsum[16];
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  int base = 0;
+  int base = 0, top = 0;   // top: bits of the largest |dloss|
   for (int t0 = 0; t0 < a.T; t0 += 1024) {
     const int t = t0 + threadIdx.x;
     const int lab = t < a.T ? a.labels[t] : -1;
+    const int wt = a.acc != nullptr && t < a.T ? __float_as_int(a.dloss[t]) & 0x7fffffff : 0;
     const bool ok = lab >= 0 && lab < a.V;
+    if (ok && wt < 0x7f800000) top = max(top, wt);
     const unsigned long long b = __ballot(ok);
     if (lane == 0) wsum[w] = __popcll(b);
     __syncthreads();
@@ -139,7 +158,14 @@ __global__ __launch_bounds__(1024) void loss_rows_kernel(LossArgs a) {
     __syncthreads();
   }
   if (threadIdx.x == 0) a.count[0] = base;
-  if (a.acc == nullptr || w > 0) return;
+  if (a.acc == nullptr) return;
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) top = max(top, __shfl_xor(top, off));
+  if (lane == 0) wsum[w] = top;
+  __syncthreads();
+  if (w > 0) return;
+#pragma unroll
+  for (int k = 1; k < 16; ++k) top = max(top, wsum[k]);
   // one lane per number of splits
   int best = lane + 1;
   static_assert(LOSS_SPLITS == 64, "one lane each");
@@ -153,14 +179,17 @@ __global__ __launch_bounds__(1024) void loss_rows_kernel(LossArgs a) {
       best = o;
     }
   }
-  if (lane == 0) a.count[1] = best;
+  if (lane == 0) {
+    a.count[1] = best;
+    a.count[2] = (top & 0x007fffff) | 0x3f800000;
+  }
 }
 
-// hc[r] = h[rows[r]]
+// hc[r] = h[rows[r]], and dw's rows of few tokens once more
 __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
-  const int r = blockIdx.x;
-  if (r >= a.count[0]) return;
-  const int t = a.rows[r];
+  const int r = blockIdx.x, count = a.count[0];
+  if (r >= k_rows(count)) return;
+  const int t = a.rows[r < count ? r : r - count];
   if (!MOE_CHECK(t >= 0 && t < a.T, 701)) return;
   const uint4* src = reinterpret_cast<const uint4*>(a.h + static_cast<size_t>(t) * a.d);
   uint4* dst = reinterpret_cast<uint4*>(a.hc + static_cast<size_t>(r) * a.d);
@@ -169,7 +198,6 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
 
 // ------------------------------------------------------------------ logits
 
-constexpr float NEG_INF = -__builtin_inff();
 using Acc = f32x4[dense::MI][dense::NJ];   // a wave's accumulators (dense_core.hpp)
 
 // What the epilogues need of a tile's rows, in SPARE after the waves' staging:
@@ -244,15 +272,23 @@ __device__ __forceinline__ void stats_epilogue(const LossArgs& a, const Acc& acc
   }
 }
 
-// Backward epilogue: the tile of G.  One barrier.
+// What rounding x to bf16 leaves, nothing of what is not finite.
+__device__ __forceinline__ float rounding_error(float x) {
+  const float e = x - __uint_as_float(bf16x2(x, 0.f) << 16);
+  return fabsf(e) < INF ? e : 0.f;
+}
+
+// Backward epilogue: the tile of G, its rows' errors at the label, and of few
+// rows (one tile of 64) the errors of all.  One barrier.
 template <int NSUB>
 __device__ __forceinline__ void grad_epilogue(const LossArgs& a, const Acc& acc, uint8_t* ring, int vt, RowTile rt,
-                                              int ncol) {
+                                              int ncol, int count) {
   const float4* rd = reinterpret_cast<const float4*>(ring + ROW_DATA);
   const int w = wave_id(), lane = dense::fresh_lane(), lr = lane & 15, lg = lane >> 4, wm = w % 2, wn = w / 2;
   block_barrier();   // the row data are written
   auto store = [&]<bool FULL>() {   // FULL: all 256 columns are there
     float4 d;
+    float gl = 0.f;   // G at the label, on the lane that has it
     int l = 0;
     dense::store_bf16_tile<NSUB>(
         ring, 64,
@@ -268,10 +304,21 @@ __device__ __forceinline__ void grad_epilogue(const LossArgs& a, const Acc& acc,
             g[e] = d.y * __expf(acc[i][j][e] - d.x);
             if (!FULL && col + e >= ncol) g[e] = 0.f;
           }
+          const int row = 16 * (2 * i + wm) + lr;
           if ((l & ~3) == col) {   // the label is one of the four
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if ((l & 3) == e) g[e] -= d.z;
+              if ((l & 3) == e) {
+                g[e] -= d.z;
+                gl = g[e];
+              }
+          }
+          if (j == dense::NJ - 1 && l >> 6 == wn && (l >> 2 & 3) == lg)
+            a.lab_lo[rt.row0 + row] = rounding_error(gl);
+          if constexpr (NSUB == 2) {
+            if (count <= LOSS_LO_ROWS && row < rt.rows)
+              *reinterpret_cast<uint2*>(a.g + static_cast<size_t>(count + row) * a.ldg + vt * LT + col) =
+                  dense::pack4(rounding_error(g[0]), rounding_error(g[1]), rounding_error(g[2]), rounding_error(g[3]));
           }
           return dense::pack4(g[0], g[1], g[2], g[3]);
         },
@@ -300,6 +347,8 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_logits_kernel(LossArgs
     dense::Opnd oa, ob;
     float4 rd;
     RowTile rt;
+    float inv = 1.f;
+    if constexpr (GRAD) inv = 1.f / __int_as_float(a.count[2]);
     auto head = [&](int i) {
       int mt, vt;
       walk.tile(i, mt, vt);
@@ -326,8 +375,8 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_logits_kernel(LossArgs
           rd.w = __int_as_float(a.labels[t] - v0);
           if constexpr (GRAD) {
             rd.x = a.lse[t];
-            rd.z = a.dloss[t];
-            rd.y = a.dlse != nullptr ? rd.z + a.dlse[t] : rd.z;
+            rd.z = a.dloss[t] * inv;
+            rd.y = a.dlse != nullptr ? rd.z + a.dlse[t] * inv : rd.z;
           }
         }
       }
@@ -357,7 +406,7 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_logits_kernel(LossArgs
       dense::mfma_loop<dense::KC, dense::KC, NSUB>(ring, nk, acc);
       block_barrier();   // the tile's stages are read
       if constexpr (GRAD)
-        grad_epilogue<NSUB>(a, acc, ring, vt, rt, ncol);
+        grad_epilogue<NSUB>(a, acc, ring, vt, rt, ncol, count);
       else
         stats_epilogue<NSUB>(a, acc, ring, vt, rt, ncol);
     });
@@ -579,17 +628,29 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_dh_kernel(LossArgs a) 
   }
 }
 
-// dh[t] = the sum of its row's splits, in order; zero for a token that is no row.
+// dh[t] = the sum of its row's splits, in order, and G's rounding error at the
+// label; zero for a token that is no row.
 __global__ __launch_bounds__(256) void loss_dh_out_kernel(LossArgs a) {
   const size_t t = blockIdx.x;
-  const int r = a.pos[t], rows = padded_rows(a.count[0]), splits = a.count[1];
+  const int r = a.pos[t], label = a.labels[t], rows = padded_rows(a.count[0]), splits = a.count[1];
   if (!MOE_CHECK(r >= -1 && r < a.T && splits <= LOSS_SPLITS, 708)) return;
+  const float scale = __int_as_float(a.count[2]), lo = r >= 0 ? a.lab_lo[r] : 0.f;
+  const uint16_t* wl = a.w + static_cast<size_t>(r >= 0 ? label : 0) * a.d;
   for (int c = 4 * threadIdx.x; c < a.d; c += 1024) {
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    if (r >= 0)
+    if (r >= 0) {
+      const uint2 q = *reinterpret_cast<const uint2*>(wl + c);
 #pragma unroll 8
       for (int s = 0; s < splits; ++s)
         v += *reinterpret_cast<const f32x4*>(a.acc + (static_cast<size_t>(s) * rows + r) * a.d + c);
+      const f32x4 we = {__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xffff0000u), __uint_as_float(q.y << 16),
+                        __uint_as_float(q.y & 0xffff0000u)};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = lo * we[e];
+        v[e] = scale * (fabsf(x) < INF ? v[e] + x : v[e]);   // an infinite w is in v already
+      }
+    }
     if (a.dh_fmt == FMT_F32)
       *reinterpret_cast<f32x4*>(static_cast<float*>(a.dh) + t * a.d + c) = v;
     else
@@ -605,15 +666,15 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_dw_kernel(LossArgs a) 
   const int count = a.count[0];
   if (!MOE_CHECK(count >= 0 && count <= a.T, 709)) return;
   const TileWalk walk(ceil_div(a.v_len, LT), ceil_div(a.d, LT));
-  const int n = walk.count(), nk = ceil_div(count, 32);
+  const int n = walk.count(), kr = k_rows(count), nk = ceil_div(kr, 32);
   int vt, nt;
   if (wave_id() >= dense::NMW) {
     const uint32_t ldg = a.ldg * 2, ldh = a.d * 2;
     dense::Opnd oa, ob;
     auto head = [&](int i) {
       walk.tile(i, vt, nt);
-      oa = dense::opnd_ko(make_rsrc(a.g, count * ldg), ldg, vt * LT);
-      ob = dense::opnd_ko(make_rsrc(a.hc, count * ldh), ldh, nt * LT);
+      oa = dense::opnd_ko(make_rsrc(a.g, kr * ldg), ldg, vt * LT);
+      ob = dense::opnd_ko(make_rsrc(a.hc, kr * ldh), ldh, nt * LT);
       dense::load_head<4>(ring, oa, ob, nk);
     };
     if (n > 0) head(0);
@@ -625,6 +686,7 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_dw_kernel(LossArgs a) 
     return;
   }
   const int w = wave_id(), wm = w % 2, wn = w / 2;
+  const float scale = __int_as_float(a.count[2]);
   for (int i = 0; i < n; ++i) {
     walk.tile(i, vt, nt);
     const int v0 = a.v_first + vt * LT, vrows = min(LT, a.V - v0), n0 = nt * LT + 64 * wn, ncols = min(64, a.d - n0);
@@ -632,6 +694,10 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_dw_kernel(LossArgs a) 
     dense::mfma_loop<KO, KO, 8>(ring, nk, acc);
     block_barrier();   // the tile's stages are read
     if (ncols <= 0) continue;
+#pragma unroll
+    for (int k = 0; k < MI; ++k)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[k][j] *= scale;
     if (a.dw_fmt == FMT_BF16) {
       uint16_t* dst = static_cast<uint16_t*>(a.dw) + static_cast<size_t>(v0) * a.d + n0;
       dense::store_bf16_tile<8>(
@@ -696,7 +762,7 @@ hipError_t launch_loss_forward(const LossArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_loss_gather(const LossArgs& a, hipStream_t s) {
-  if (a.T > 0) hipLaunchKernelGGL(loss_gather_kernel, dim3(a.T), dim3(256), 0, s, a);
+  if (a.T > 0) hipLaunchKernelGGL(loss_gather_kernel, dim3(loss_k_rows(a.T)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -24,7 +24,7 @@ int validate_shape(const moe_loss_shape* s) {
 // Workspace map (byte offsets, each 256-byte aligned).
 struct Layout {
   size_t rows, pos, count, part, zlab, forward_total;
-  size_t hc, g, acc, backward_total;
+  size_t lab_lo, hc, g, acc, backward_total;
   int piece;
 };
 
@@ -33,7 +33,7 @@ Layout make_layout(const moe_loss_shape& s) {
   const size_t T = static_cast<size_t>(s.T), nv = static_cast<size_t>(moe::loss_tiles(s.T, s.V));
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o += align_up(bytes); return at; };
-  L.count = take(8);
+  L.count = take(12);
   L.rows = take(T * 4);
   L.pos = take(T * 4);
   const size_t shared = o;
@@ -42,8 +42,10 @@ Layout make_layout(const moe_loss_shape& s) {
   L.forward_total = o;
   o = shared;
   L.piece = moe::loss_piece(s.T, s.d, s.V);
-  L.hc = take(T * s.d * 2);
-  L.g = take(T * L.piece * 2);
+  const size_t kr = static_cast<size_t>(moe::loss_k_rows(s.T));
+  L.lab_lo = take(T * 4);
+  L.hc = take(kr * s.d * 2);
+  L.g = take(kr * L.piece * 2);
   L.acc = take(static_cast<size_t>(moe::loss_acc_rows(s.T, s.d, L.piece)) * s.d * 4);
   L.backward_total = o;
   return L;
@@ -115,6 +117,7 @@ int moe_vocab_loss_backward(const moe_loss_shape* shape, const void* h, const vo
   a.lse = const_cast<float*>(lse);
   a.dloss = dloss;
   a.dlse = dlse;
+  a.lab_lo = at<float>(workspace, L.lab_lo);
   a.hc = at<uint16_t>(workspace, L.hc);
   a.g = at<uint16_t>(workspace, L.g);
   a.acc = at<float>(workspace, L.acc);

@@ -183,6 +183,66 @@ def test_pieces_of_the_vocabulary(T, d, V):
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("T,d,V,masked", [(1, 256, 4099, 0.0), (2, 64, 1000, 0.0), (5, 128, 700, 0.5), (17, 320, 2000, 0.0),
+                                          (64, 64, 4099, 0.0), (65, 128, 520, 0.2), (300, 64, 2000, 0.85)])
+def test_gradients_of_few_rows(T, d, V, masked):
+    """Up to 64 rows: dw carries G's rounding errors too, which are themselves
+    rounded (2^-9 of 2^-9 of an element); dh that of the label's element."""
+    say(f"case: vocab_loss, few rows T={T} d={d} V={V} masked={masked}")
+    h, w, labels, dloss, dlse = _make(T, T, d, V, masked)
+    _, _, dh, dw = _run(h, w, labels, dloss, dlse)
+    hn, wn, lab = np.nan_to_num(_np(h)), _np(w), labels.numpy()
+    keep = np.flatnonzero((lab >= 0) & (lab < V))
+    assert len(keep) <= 64
+    rh, rw, G = A.vocab_loss_backward(hn, wn, lab, dloss.numpy(), dlse.numpy())
+    top = (d / 32 + 32) * 2.0 ** -24 * (np.abs(hn) @ np.abs(wn).T)[keep].max(initial=0)
+    rest = G.copy()
+    rest[keep, lab[keep]] = 0
+    tol = 8 * U16 / 3 ** 0.5 * np.sqrt((rest * rest) @ (wn * wn)) + (4 * top + 2e-5) * (np.abs(G) @ np.abs(wn))
+    over = np.abs(_np(dh) - rh) - tol - 2.0 ** -23 * np.abs(rh)
+    assert over.max() <= 1e-30, over.max()
+    over = np.abs(_np(dw) - rw) - (4 * top + 2e-5 + 2.0 ** -17) * (np.abs(G).T @ np.abs(hn)) - 2.0 ** -23 * np.abs(rw)
+    assert over.max() <= 1e-30, over.max()
+
+
+def test_equal_weights_do_not_bias_the_gradient():
+    """dloss = 1 / T, 0.2% from a bf16 value: G is held over its mantissa, so the
+    label's element (p - 1, here p below 1/2) is off by at most p and 2^-9 of the
+    weight, another by 2^-9 of itself."""
+    say("case: vocab_loss, equal weights")
+    T, d, V = 300, 128, 2000
+    g = torch.Generator().manual_seed(5)
+    w = (torch.randn((V, d), generator=g) * (1.0 / d ** 0.5)).bfloat16()
+    h = torch.randn((T, d), generator=g).bfloat16()
+    labels = torch.randint(0, V, (T,), generator=g, dtype=torch.int32)
+    dloss = torch.full((T,), 1 / T)
+    _, _, dh, dw = _run(h, w, labels, dloss, None)
+    hn, wn, lab, t = _np(h), _np(w), labels.numpy(), np.arange(T)
+    rh, rw, G = A.vocab_loss_backward(hn, wn, lab, dloss.numpy())
+    p = G[t, lab] * T + 1
+    assert 0 < p.min() and p.max() < 0.5
+    err = 2.0 ** -9 * np.abs(G)
+    err[t, lab] = np.minimum(p, 2.0 ** -9) / T
+    top = (d / 32 + 32) * 2.0 ** -24 * (np.abs(hn) @ np.abs(wn).T).max()
+    for got, ref, e, a, b in ((_np(dh), rh, err, G, wn), (_np(dw), rw, err.T, G.T, hn)):
+        over = np.abs(got - ref) - e @ np.abs(b) - (4 * top + 2e-5) * (np.abs(a) @ np.abs(b)) - 2.0 ** -23 * np.abs(ref)
+        assert over.max() <= 1e-30, over.max()
+
+
+def test_weights_that_are_not_finite():
+    """A row whose dloss is NaN or infinite leaves the other rows' dh as they are."""
+    say("case: vocab_loss, dloss not finite")
+    h, w, labels, dloss, _ = _make(6, 9, 128, 300)
+    clean = _run(h, w, labels, dloss, None)[2]
+    dloss[3], dloss[7] = float("nan"), float("inf")
+    dh = _run(h, w, labels, dloss, None)[2]
+    others = [t for t in range(9) if t not in (3, 7)]
+    # (the scale may be another's mantissa: the rounding of G differs, 2^-8 of a row's sums each)
+    tol = 2 * U16 * (dloss[others].abs()[:, None] * 2 * w.float().abs().max(dim=0).values)
+    assert ((dh - clean)[others].cpu().abs() <= tol).all()
+    assert not torch.isfinite(dh[3]).any() and not torch.isfinite(dh[7]).any()
+
+
 def test_gradient_is_the_difference_quotient():
     """Along random directions of h and w, against central differences of the
     GPU's own loss in steps that bf16 holds exactly.  Errors: the loss's own
