@@ -127,11 +127,14 @@ struct LossArgs {
 };
 
 constexpr int LOSS_TILE = 256;    // rows and columns of a tile
-// The forward of few tokens (loss_stream_kernel, tiles of 64 entries) against
-// the tile pipeline, measured: 1 token, V = 32000, d = 2048: 34 / 47 us; 20,
+// The logits of few tokens (loss_stream_kernel, tiles of 64 entries) against
+// the tile pipeline, measured forward: 1 token, V = 32000, d = 2048: 34 / 47 us; 20,
 // 65536, 2048: 66 / 73; 40, 16000, 2048: 21 / 33; 40, 24000, 2048: 37 / 39; but
 // 64, 32000, 4096: 79 / 73 and 37, 50001, 7168: 192 / 140 (its blocks read the
-// hidden rows again for every 64 entries).
+// hidden rows again for every 64 entries).  Forward and backward, the backward's
+// logits by either: 9 tokens, V = 453, d = 3328: 58 / 81 us; 48, 10000, 7168:
+// 195 / 223; 64, 2000, 7168: 153 / 180; 16, 32000, 2048: 135 / 144; 32, 65536, 1024:
+// 142 / 143.
 constexpr int LOSS_STREAM_TILE = 64;
 inline bool loss_stream(int T, int V) { return T <= 32 || (T <= 64 && V <= 16384); }
 inline int loss_tiles(int T, int V) { return ceil_div(V, loss_stream(T, V) ? LOSS_STREAM_TILE : LOSS_TILE); }

@@ -422,12 +422,18 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_logits_kernel(LossArgs
 // such blocks fit a CU, with a pair of every wave in flight (8 KB); the tile
 // pipeline has one block to a CU and at most 64 KB of w in flight.  (Two pairs
 // in flight per wave cost a block its place on the CU: 20 tokens 66 -> 71 us.)
+//
+// GRAD: the piece's G by the same rule, with its rows' rounding errors below it
+// (there are at most 64 rows).  Every column of the tile is written: G's past V
+// are zero.
 constexpr int SV = LOSS_STREAM_TILE, STHREADS = 512;
 
-template <int NT>
+template <int NT, bool GRAD>
 __global__ __launch_bounds__(STHREADS) void loss_stream_kernel(LossArgs a) {
+  static_assert(16 * NT <= LOSS_LO_ROWS, "all rows have their rounding errors");
   __shared__ float red[8][16 * NT][SV + 4];
   __shared__ int rows[16 * NT], labs[16 * NT];
+  __shared__ float3 rd[GRAD ? 16 * NT : 1];   // lse, (dloss + dlse) / scale, dloss / scale
   const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   // the rows, as loss_rows_kernel lists them (one lane a token)
   const int lab = lane < a.T ? a.labels[lane] : -1;
@@ -437,8 +443,12 @@ __global__ __launch_bounds__(STHREADS) void loss_stream_kernel(LossArgs a) {
   if (w == 0 && ok) {
     rows[at] = lane;
     labs[at] = lab;
+    if constexpr (GRAD) {
+      const float inv = 1.f / __int_as_float(a.count[2]), dl = a.dloss[lane] * inv;
+      rd[at] = make_float3(a.lse[lane], a.dlse != nullptr ? dl + a.dlse[lane] * inv : dl, dl);
+    }
   }
-  if (blockIdx.x == 0 && w == 0) {
+  if (!GRAD && blockIdx.x == 0 && w == 0) {
     if (ok)
       a.rows[at] = lane;
     else if (lane < a.T)
@@ -448,7 +458,7 @@ __global__ __launch_bounds__(STHREADS) void loss_stream_kernel(LossArgs a) {
   __syncthreads();
   if (count == 0) return;
 
-  const int v0 = blockIdx.x * SV, nv = min(SV, a.V - v0);
+  const int v0 = a.v_first + blockIdx.x * SV, nv = max(0, min(SV, a.V - v0));
   const uint32_t ld = a.d * 2;
   const rsrc_t rw = make_rsrc(a.w + static_cast<size_t>(v0) * a.d, nv * ld);   // entries past V: zeros
   const rsrc_t rh = make_rsrc(a.h, a.T * ld);
@@ -495,6 +505,22 @@ __global__ __launch_bounds__(STHREADS) void loss_stream_kernel(LossArgs a) {
     f32x4 l = *reinterpret_cast<const f32x4*>(&red[0][r][c]);
 #pragma unroll
     for (int k = 1; k < 8; ++k) l += *reinterpret_cast<const f32x4*>(&red[k][r][c]);
+    if constexpr (GRAD) {
+      const float3 q = rd[r];
+      const int z = labs[r] - v0 - c;
+      float g[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        g[e] = c + e < nv ? q.y * __expf(l[e] - q.x) : 0.f;
+        if (z == e) g[e] -= q.z;
+        lo[e] = rounding_error(g[e]);
+        if (z == e) a.lab_lo[r] = lo[e];
+      }
+      uint16_t* dst = a.g + static_cast<size_t>(r) * a.ldg + blockIdx.x * SV + c;
+      *reinterpret_cast<uint2*>(dst) = dense::pack4(g[0], g[1], g[2], g[3]);
+      *reinterpret_cast<uint2*>(dst + static_cast<size_t>(count) * a.ldg) = dense::pack4(lo[0], lo[1], lo[2], lo[3]);
+      continue;
+    }
     float m = NEG_INF;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -740,16 +766,21 @@ hipError_t launch_loss_rows(const LossArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <bool GRAD>
+static void launch_stream(const LossArgs& a, int blocks, hipStream_t s) {
+  if (a.T <= 16)
+    hipLaunchKernelGGL((loss_stream_kernel<1, GRAD>), dim3(blocks), dim3(STHREADS), 0, s, a);
+  else if (a.T <= 32)
+    hipLaunchKernelGGL((loss_stream_kernel<2, GRAD>), dim3(blocks), dim3(STHREADS), 0, s, a);
+  else if (a.T <= 48)
+    hipLaunchKernelGGL((loss_stream_kernel<3, GRAD>), dim3(blocks), dim3(STHREADS), 0, s, a);
+  else
+    hipLaunchKernelGGL((loss_stream_kernel<4, GRAD>), dim3(blocks), dim3(STHREADS), 0, s, a);
+}
+
 hipError_t launch_loss_forward(const LossArgs& a, hipStream_t s) {
   if (loss_stream(a.T, a.V)) {
-    if (a.T <= 16)
-      hipLaunchKernelGGL(loss_stream_kernel<1>, dim3(a.tiles), dim3(STHREADS), 0, s, a);
-    else if (a.T <= 32)
-      hipLaunchKernelGGL(loss_stream_kernel<2>, dim3(a.tiles), dim3(STHREADS), 0, s, a);
-    else if (a.T <= 48)
-      hipLaunchKernelGGL(loss_stream_kernel<3>, dim3(a.tiles), dim3(STHREADS), 0, s, a);
-    else
-      hipLaunchKernelGGL(loss_stream_kernel<4>, dim3(a.tiles), dim3(STHREADS), 0, s, a);
+    launch_stream<false>(a, a.tiles, s);
     hipLaunchKernelGGL(loss_finish_kernel<4>, dim3(a.T), dim3(256), 0, s, a);
     return hipGetLastError();
   }
@@ -770,7 +801,10 @@ hipError_t launch_loss_gather(const LossArgs& a, hipStream_t s) {
 hipError_t launch_loss_piece(const LossArgs& a, hipStream_t s) {
   const long long nm = ceil_div(a.T, 64), nv = ceil_div(a.v_len, LT), nn = ceil_div(a.d, LT);
   if (a.T > 0) {
-    hipLaunchKernelGGL(loss_logits_kernel<true>, dim3(loss_grid(nm, nv)), dim3(dense::THREADS), 0, s, a);
+    if (loss_stream(a.T, a.V))
+      launch_stream<true>(a, static_cast<int>(nv) * (LT / SV), s);
+    else
+      hipLaunchKernelGGL(loss_logits_kernel<true>, dim3(loss_grid(nm, nv)), dim3(dense::THREADS), 0, s, a);
     hipLaunchKernelGGL(loss_dh_kernel, dim3(loss_grid(nm, nn * LOSS_SPLITS)), dim3(dense::THREADS), 0, s, a);
   }
   hipLaunchKernelGGL(loss_dw_kernel, dim3(loss_grid(nv, nn)), dim3(dense::THREADS), 0, s, a);
