@@ -347,7 +347,9 @@ int moe_backward(const moe_shape* shape, const void* u, const void* centroids, c
  *   scales     [T][d/128]   codes of v * (448 * (1 / amax)) per 1x128 tile (rounded
  *                           to nearest even) and scale = amax / 448; scale 1 and
  *                           zero codes for a tile of zeros (amax below 2^-119,
- *                           where the factor overflows); d a multiple of 128.
+ *                           where the factor overflows).  A tile that holds a
+ *                           NaN or an infinity reads as NaN throughout (scale NaN
+ *                           or infinity).  d a multiple of 128.
  *                           A backward without the rows themselves reads
  *                           codes * scale in their place: 1.03 bytes per value.
  * save may be null, and save_next (of x_out, for n_next) only with w_next.

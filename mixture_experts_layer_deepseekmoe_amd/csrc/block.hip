@@ -102,17 +102,29 @@ __device__ __forceinline__ float rstd_of(float sumsq, int d, float eps) {
 
 // The 1x128 tile that holds this thread's eight values (16 lanes to a tile):
 // scale amax / 448, codes of v * (448 * (1 / amax)).  A tile below 2^-119, where
-// that factor would overflow, counts as all zero: scale 1, zero codes.
+// that factor would overflow, counts as all zero: scale 1, zero codes.  amax is
+// taken over the bits, where NaN stands above infinity and infinity above the
+// rest (fmaxf would drop a NaN): such a tile has the scale NaN or infinity, and
+// the code NaN wherever v * factor is NaN, so all of it is read as NaN.
 __device__ __forceinline__ void save_tile(const float (&v)[8], uint8_t* codes, float* scales, size_t row, int d, int c) {
-  float m = 0.f;
+  uint32_t top = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
-  m = wave_max_16(m);
+  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+#pragma unroll
+  for (int off = 1; off <= 8; off <<= 1) top = max(top, __shfl_xor(top, off));
+  const float m = __uint_as_float(top);
   const bool none = m < 0x1p-119f;
   const float inv = none ? 0.f : 448.f * (1.f / m);
-  *reinterpret_cast<uint2*>(codes + row * d + c) =
-      make_uint2(e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                 e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+  float t[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) t[e] = v[e] * inv;
+  uint32_t q[2] = {e4m3x4(t[0], t[1], t[2], t[3]), e4m3x4(t[4], t[5], t[6], t[7])};
+  if (top >= 0x7f800000u) {   // e4m3x4 clamps, NaN too
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (t[e] != t[e]) q[e / 4] = (q[e / 4] & ~(0xffu << 8 * (e % 4))) | 0x7fu << 8 * (e % 4);
+  }
+  *reinterpret_cast<uint2*>(codes + row * d + c) = make_uint2(q[0], q[1]);
   if ((threadIdx.x & 15) == 0) scales[row * (d / 128) + c / 128] = none ? 1.f : m / 448.f;
 }
 

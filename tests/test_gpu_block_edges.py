@@ -1,0 +1,124 @@
+"""moe_block_in / moe_block_out and their backward where the rows are not all
+finite, against the definitions in numpy."""
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_layer_deepseekmoe_amd as moe
+from oracle import around_oracle as A
+from tests.parity import say
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+# as in test_gpu_block.py: fp32 arithmetic relative to the terms' sizes, and a bf16 store
+E, U16 = 2e-5, 2.0 ** -8
+
+
+def _np(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def _rows(seed, T, d, dtype=torch.float32):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.exp(0.7 * torch.randn(d, generator=g)) * torch.randn((T, d), generator=g)).to(dtype)
+
+
+def _values(save):
+    """What a checkpoint stands for, decoded by torch."""
+    T, d = save.codes.shape
+    codes = save.codes.view(torch.float8_e4m3fn).float().view(T, d // 128, 128)
+    return (codes * save.scales[:, :, None]).view(T, d)
+
+
+# row, column: the entry that is not finite; entries of one tile, of the first and last tile of a row
+BAD = [(0, 5, float("nan")), (2, 130, float("inf")), (3, 255, -float("inf")), (4, 511, float("nan"))]
+
+
+def _spoil(x):
+    for t, c, v in BAD:
+        x[t, c] = v
+    x[5, 128:256] = float("nan")   # a tile of nothing else
+    bad = torch.zeros(x.shape, dtype=torch.bool)
+    for t, c, _ in BAD:
+        bad[t, c // 128 * 128:c // 128 * 128 + 128] = True
+    bad[5, 128:256] = True
+    return bad
+
+
+def test_checkpoint_keeps_what_is_not_finite():
+    """amax is the tile's largest size in IEEE order (NaN above all), as in the
+    definition amax = max |v|: a tile that holds a NaN or an infinity decodes to
+    NaN throughout (0 x inf, NaN x anything); every other tile to its own bits."""
+    say("case: checkpoints of rows that are not finite")
+    T, d = 7, 512
+    x = _rows(1, T, d, torch.bfloat16)
+    clean = A.checkpoint(x.float().numpy())
+    bad = _spoil(x)
+    y = _rows(2, T, d)
+    ybad = _spoil(y)
+    w = torch.ones(d)
+    shape = moe.BlockShape(T, d)
+    s_in, s_out, s_next = (moe.alloc_block_save(shape, e4m3=True) for _ in range(3))
+    moe.moe_block_in(shape, x.to(DEV), w.to(DEV), save=s_in)
+    finite = _rows(3, T, d, torch.bfloat16)
+    xo, _ = moe.moe_block_out(shape, finite.to(DEV), y.to(DEV), w_next=w.to(DEV), save=s_out, save_next=s_next)
+    for save, b in ((s_in, bad), (s_out, ybad), (s_next, ybad)):
+        v = _values(save).cpu()
+        assert torch.isnan(v[b]).all() and torch.isfinite(v[~b]).all()
+    ok = ~bad.numpy()
+    assert (s_in.codes.cpu().numpy() == clean[0])[ok].all()
+    assert (s_in.scales.cpu().numpy() == clean[1])[ok[:, ::128]].all()
+    # the entries themselves, where the tile's other entries are finite: x_out = x + y
+    for t, c, val in BAD:
+        assert float(xo[t, c]) == val or (np.isnan(val) and torch.isnan(xo[t, c]))
+
+
+def test_gradients_show_what_is_not_finite():
+    """Without a norm nothing but the checkpoint carries a NaN of the rows to the
+    backward: dgate is NaN in the tile's columns and right in the others.  With a
+    norm the whole row's dy is NaN and no other row's is."""
+    say("case: backward from checkpoints of rows that are not finite")
+    T, d = 7, 512
+    y, do = _rows(2, T, d), _rows(4, T, d)
+    bad = _spoil(y)
+    gate = 0.5 * _rows(5, 1, d)
+    shape = moe.BlockShape(T, d)
+    x = _rows(3, T, d, torch.bfloat16)
+    cols = bad.any(dim=0).numpy()
+    z = np.where(np.isfinite(_np(y)), _np(y), 0)   # the columns compared hold no entry that is replaced
+    for w in (None, 1 + 0.2 * _rows(6, 1, d)[0]):
+        dv = None if w is None else w.to(DEV)
+        for rows in (False, True):
+            save = moe.alloc_block_save(shape, e4m3=True)
+            moe.moe_block_out(shape, x.to(DEV), y.to(DEV), w=dv, gate=gate.to(DEV), save=save)
+            dy, dw, dgate = moe.moe_block_out_backward(shape, do.to(DEV), save, w=dv, gate=gate.to(DEV),
+                                                       y=y.to(DEV) if rows else None)
+            if w is None:
+                v = z if rows else np.where(cols, 0, _np(_values(save)))
+                ref = (_np(do) * v).sum(axis=0)
+                got = _np(dgate)[0]
+                assert (~np.isfinite(got[cols if not rows else (~np.isfinite(_np(y))).any(axis=0)])).all()
+                assert (np.abs(got - ref) <= E * np.abs(_np(do) * v).sum(axis=0))[~cols].all()
+                assert torch.equal(dy.cpu(), do * gate)
+            else:
+                hit = bad.any(dim=1)
+                assert not torch.isfinite(dy.cpu()[hit]).all(dim=1).any()
+                assert torch.isfinite(dy.cpu()[~hit]).all()
+                assert torch.isnan(dgate.cpu()[0, torch.from_numpy(cols)]).all()
+
+
+def test_rows_that_are_not_finite_stay_alone():
+    """NaN and infinities in a row reach that row's outputs only."""
+    say("case: rows that are not finite beside rows that are")
+    T, d = 7, 512
+    x, y = _rows(1, T, d, torch.bfloat16), _rows(2, T, d)
+    w = 1 + 0.2 * _rows(6, 1, d)[0]
+    shape = moe.BlockShape(T, d)
+    run = lambda a, b: (moe.moe_block_in(shape, a.to(DEV), w.to(DEV)),) + \
+        moe.moe_block_out(shape, a.to(DEV), b.to(DEV), w=w.to(DEV), w_next=w.to(DEV))  # noqa: E731
+    want = run(x, y)
+    hit = _spoil(x).any(dim=1) | _spoil(y).any(dim=1)
+    for a, b in zip(run(x, y), want):
+        assert torch.equal(a[~hit.to(DEV)], b[~hit.to(DEV)])
+        assert not torch.isfinite(a[hit.to(DEV)]).all(dim=1).any()
