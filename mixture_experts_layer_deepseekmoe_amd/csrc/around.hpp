@@ -115,11 +115,11 @@ struct LossArgs {
   const float* dloss;     // [T]
   const float* dlse;      // [T], or null
   uint16_t* hc;           // [loss_k_rows(T)][d] the rows' hidden rows, one after the other
-  uint16_t* g;            // [loss_k_rows(T)][ldg] a piece's G = dlogits / scale
+  uint16_t* g;            // [loss_g_rows(T, pairs)][ldg] a piece's G = dlogits / scale
   float* lab_lo;          // [T] by row: the rounding error of G at the label
   float* acc;             // [splits][row tiles of 256][d] dh by row (loss_acc_rows)
   int ldg;                // loss_piece
-  int dh_fmt, dw_fmt;
+  int dh_fmt, dw_fmt;     // fp32: from pairs of bf16 values of G
   void* dh;               // [T][d]
   void* dw;               // [V][d]
   // the piece of the vocabulary: columns v_first .. v_first + v_len - 1
@@ -139,24 +139,32 @@ constexpr int LOSS_STREAM_TILE = 64;
 inline bool loss_stream(int T, int V) { return T <= 32 || (T <= 64 && V <= 16384); }
 inline int loss_tiles(int T, int V) { return ceil_div(V, loss_stream(T, V) ? LOSS_STREAM_TILE : LOSS_TILE); }
 
+// A gradient in fp32 is summed from G held as pairs of bf16 values, what bf16
+// rounds off of G below it (2^-16 of an element is left, where one bf16 value
+// leaves 2^-8): one of its two products more.
+inline bool loss_pairs(int dh_fmt, int dw_fmt) { return dh_fmt == FMT_F32 || dw_fmt == FMT_F32; }
+
 // The backward's pieces of the vocabulary: as many whole tiles of columns as
 // keep G within LOSS_G_BYTES (and a piece of w within 2^31 bytes).
 constexpr long long LOSS_G_BYTES = 512LL << 20;
-inline int loss_piece(long long T, long long d, long long V) {
-  const long long vt = (V + LOSS_TILE - 1) / LOSS_TILE * LOSS_TILE;
-  long long n = LOSS_G_BYTES / (2 * (T > LOSS_TILE ? T : LOSS_TILE)) / LOSS_TILE * LOSS_TILE;
+inline int loss_piece(long long T, long long d, long long V, bool pairs) {
+  const long long vt = (V + LOSS_TILE - 1) / LOSS_TILE * LOSS_TILE, rows = pairs ? 2 * T : T;
+  long long n = LOSS_G_BYTES / (2 * (rows > LOSS_TILE ? rows : LOSS_TILE)) / LOSS_TILE * LOSS_TILE;
   const long long nw = (1LL << 30) / d / LOSS_TILE * LOSS_TILE;
   if (n > nw) n = nw;
   if (n < LOSS_TILE) n = LOSS_TILE;
   return static_cast<int>(n < vt ? n : vt);
 }
 
-// dw = G^T h of up to 64 rows sums over 2 count rows: count .. 2 count - 1 hold
-// what rounding G to bf16 left, and the same hidden rows again.  The product is
-// bound by writing dw; this costs it one or two K-steps.
+// dw = G^T h of up to 64 rows sums over 2 count rows in any case: count .. 2 count
+// - 1 hold what rounding G to bf16 left, and the same hidden rows again.  The product
+// is bound by writing dw; this costs it one or two K-steps.
 constexpr int LOSS_LO_ROWS = 64;
 constexpr int loss_k_rows(int T) {   // the most there can be
   return T < LOSS_LO_ROWS ? 2 * T : T < 2 * LOSS_LO_ROWS ? 2 * LOSS_LO_ROWS : T;
+}
+constexpr long long loss_g_rows(long long T, bool pairs) {
+  return pairs ? 2 * T : loss_k_rows(static_cast<int>(T));
 }
 
 // dh = G w sums over the whole piece: few rows make few tiles, so the piece is

@@ -23,10 +23,16 @@
 // Library products of the same with 4096 rows: 1.23-1.26, 0.92-0.94, 0.92-1.06 on
 // operands laid out as these are.  Few tokens are bound by reading w once.
 //
-// Products are bf16 with fp32 accumulation; statistics and dh's sums are fp32; G
-// is rounded to bf16 as the operand of the two products that follow (at most
-// 2^-9 of each element).  The label's element outweighs the rest of its row, so
-// its rounding is most of that error and, with few rows, does not average out:
+// Products are bf16 with fp32 accumulation; statistics and dh's sums are fp32.  G
+// is the operand of the two products that follow, in bf16.  For a gradient in fp32
+// it is a pair of bf16 values, what the first rounds off in the second (2^-16 of
+// an element is left): the product runs once for each, the second's sums added
+// to the first's (4096 tokens, a quarter ignored, d = 7168, V = 65536, both gradients: 15.4
+// ms against 9.3 in bf16; d = 2048, none ignored: 6.0 against 3.7).
+// For a gradient in bf16, G is rounded to bf16 once (at most 2^-8 of an element), an
+// error of the size of the output's own rounding.  The label's element outweighs
+// the rest of its row, so its rounding is most of that error and, with few rows,
+// does not average out:
 //   dh   each row's rounding error at its label times the label's row of w is
 //        added in fp32 where dh is written;
 //   dw   up to 64 rows are summed with their rounding errors (LOSS_LO_ROWS);
@@ -56,15 +62,15 @@ struct TileWalk {
   int nm, nn;
   long long j0, n;   // the XCD's first tile and its number of them
   int l, P;
-  __device__ TileWalk(int nm_, int nn_) : nm(nm_), nn(nn_) {
+  __device__ __forceinline__ TileWalk(int nm_, int nn_) : nm(nm_), nn(nn_) {
     const long long total = static_cast<long long>(nm) * nn, chunk = (total + NXCDS - 1) / NXCDS;
     j0 = blockIdx.x % NXCDS * chunk;
     n = max(0LL, min(chunk, total - j0));
     l = blockIdx.x / NXCDS;
     P = gridDim.x / NXCDS;
   }
-  __device__ int count() const { return l < n ? static_cast<int>((n - l + P - 1) / P) : 0; }
-  __device__ void tile(int i, int& m, int& k) const {
+  __device__ __forceinline__ int count() const { return l < n ? static_cast<int>((n - l + P - 1) / P) : 0; }
+  __device__ __forceinline__ void tile(int i, int& m, int& k) const {
     constexpr int GM = 8;
     const long long j = j0 + l + static_cast<long long>(i) * P;
     const int per = GM * nn, g = static_cast<int>(j / per), rem = static_cast<int>(j - static_cast<long long>(g) * per);
@@ -89,13 +95,13 @@ struct RowTile {
 };
 struct RowCut {
   int n, per, count;
-  __device__ RowCut(int count_, int nn) : count(count_) {
+  __device__ __forceinline__ RowCut(int count_, int nn) : count(count_) {
     const int least = (count + LT - 1) / LT, most = (count + 63) / 64;
     const int want = max(least, min(most, NBLOCKS / nn));
     per = want > 0 ? ((count + want - 1) / want + 15) / 16 * 16 : LT;
     n = (count + per - 1) / per;
   }
-  __device__ RowTile tile(int m) const { return {m * per, min(per, count - m * per)}; }
+  __device__ __forceinline__ RowTile tile(int m) const { return {m * per, min(per, count - m * per)}; }
 };
 __device__ __forceinline__ int padded_rows(int count) { return (count + LT - 1) / LT * LT; }
 
@@ -103,7 +109,7 @@ __device__ __forceinline__ int padded_rows(int count) { return (count + LT - 1) 
 // 0.75 us per 32-column step, and the splits' fp32 tiles written and read at
 // about 4 TB/s.  The least cost (the fewest splits of equal ones) is taken; the
 // limits are those of loss_acc_rows.
-__device__ inline float split_cost(int s, int nm, int nn, int piece) {
+__device__ __forceinline__ float split_cost(int s, int nm, int nn, int piece) {
   const int tiles = nm * nn;   // below 2^17
   if (s > 1 && (s * LT > piece || s * tiles > LOSS_SPLIT_TILES)) return 1e30f;
   const float rounds = static_cast<float>((tiles * s + NBLOCKS - 1) / NBLOCKS);
@@ -278,9 +284,9 @@ __device__ __forceinline__ float rounding_error(float x) {
   return fabsf(e) < INF ? e : 0.f;
 }
 
-// Backward epilogue: the tile of G, its rows' errors at the label, and of few
-// rows (one tile of 64) the errors of all.  One barrier.
-template <int NSUB>
+// Backward epilogue: the tile of G, its rows' errors at the label, and with
+// PAIRS, or of few rows (one tile of 64), the errors of all.  One barrier.
+template <int NSUB, bool PAIRS>
 __device__ __forceinline__ void grad_epilogue(const LossArgs& a, const Acc& acc, uint8_t* ring, int vt, RowTile rt,
                                               int ncol, int count) {
   const float4* rd = reinterpret_cast<const float4*>(ring + ROW_DATA);
@@ -315,9 +321,9 @@ __device__ __forceinline__ void grad_epilogue(const LossArgs& a, const Acc& acc,
           }
           if (j == dense::NJ - 1 && l >> 6 == wn && (l >> 2 & 3) == lg)
             a.lab_lo[rt.row0 + row] = rounding_error(gl);
-          if constexpr (NSUB == 2) {
-            if (count <= LOSS_LO_ROWS && row < rt.rows)
-              *reinterpret_cast<uint2*>(a.g + static_cast<size_t>(count + row) * a.ldg + vt * LT + col) =
+          if constexpr (PAIRS || NSUB == 2) {
+            if ((PAIRS || count <= LOSS_LO_ROWS) && row < rt.rows)
+              *reinterpret_cast<uint2*>(a.g + static_cast<size_t>(count + rt.row0 + row) * a.ldg + vt * LT + col) =
                   dense::pack4(rounding_error(g[0]), rounding_error(g[1]), rounding_error(g[2]), rounding_error(g[3]));
           }
           return dense::pack4(g[0], g[1], g[2], g[3]);
@@ -332,7 +338,7 @@ __device__ __forceinline__ void grad_epilogue(const LossArgs& a, const Acc& acc,
     store.template operator()<false>();
 }
 
-template <bool GRAD>
+template <bool GRAD, bool PAIRS>
 __global__ __launch_bounds__(dense::THREADS, 1) void loss_logits_kernel(LossArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t ring[dense::RING_BYTES];
   const int count = a.count[0];
@@ -406,7 +412,7 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_logits_kernel(LossArgs
       dense::mfma_loop<dense::KC, dense::KC, NSUB>(ring, nk, acc);
       block_barrier();   // the tile's stages are read
       if constexpr (GRAD)
-        grad_epilogue<NSUB>(a, acc, ring, vt, rt, ncol, count);
+        grad_epilogue<NSUB, PAIRS>(a, acc, ring, vt, rt, ncol, count);
       else
         stats_epilogue<NSUB>(a, acc, ring, vt, rt, ncol);
     });
@@ -578,6 +584,12 @@ __global__ __launch_bounds__(256) void loss_finish_kernel(LossArgs a) {
 
 // ------------------------------------------------------------------ dh = G w
 
+// Offset of the pairs' second values in G.
+template <bool SECOND>
+__device__ __forceinline__ size_t second_at(int count, int ldg) {
+  return SECOND ? static_cast<size_t>(count) * ldg : 0;
+}
+
 // Split s of the piece: its columns k0 .. k0 + len - 1 (a multiple of 64 but
 // for the last).
 struct Run {
@@ -588,6 +600,8 @@ __device__ __forceinline__ Run split_run(int n, int splits, int s) {
   return {s * per, max(0, min(per, n - s * per))};
 }
 
+// SECOND: of the pairs' second values, added to the sums of the first.
+template <bool SECOND>
 __global__ __launch_bounds__(dense::THREADS, 1) void loss_dh_kernel(LossArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t ring[dense::RING_BYTES];
   const int count = a.count[0], splits = a.count[1];
@@ -609,11 +623,12 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_dh_kernel(LossArgs a) 
   int s, n0;
   if (wave_id() >= dense::NMW) {
     const uint32_t ldg = a.ldg * 2, ldw = a.d * 2;
+    const uint16_t* g = a.g + second_at<SECOND>(count, a.ldg);
     dense::Opnd oa, ob;
     auto head = [&](int i) {
       tile(i, rt, run, s, n0);
       // G's columns past V are zero, w's rows past V lie past the resource
-      oa = dense::opnd_kc(make_rsrc(a.g + static_cast<size_t>(rt.row0) * a.ldg + run.k0, rt.rows * ldg - run.k0 * 2),
+      oa = dense::opnd_kc(make_rsrc(g + static_cast<size_t>(rt.row0) * a.ldg + run.k0, rt.rows * ldg - run.k0 * 2),
                           [&](int m) { return static_cast<uint32_t>((m < rt.rows ? m : rt.rows) * ldg); });
       ob = dense::opnd_ko(make_rsrc(a.w + static_cast<size_t>(a.v_first + run.k0) * a.d, run.len * ldw), ldw, n0);
       dense::with_rows(rt.rows,
@@ -629,7 +644,7 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_dh_kernel(LossArgs a) 
     return;
   }
   const int w = wave_id(), wm = w % 2, wn = w / 2;
-  const bool first = a.v_first == 0;
+  const bool first = a.v_first == 0 && !SECOND;
   for (int t = 0; t < n; ++t) {
     tile(t, rt, run, s, n0);
     dense::with_rows(rt.rows, [&]<int NSUB>() {
@@ -654,13 +669,13 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_dh_kernel(LossArgs a) 
   }
 }
 
-// dh[t] = the sum of its row's splits, in order, and G's rounding error at the
-// label; zero for a token that is no row.
+// dh[t] = the sum of its row's splits, in order, and without pairs G's rounding
+// error at the label; zero for a token that is no row.
 __global__ __launch_bounds__(256) void loss_dh_out_kernel(LossArgs a) {
   const size_t t = blockIdx.x;
   const int r = a.pos[t], label = a.labels[t], rows = padded_rows(a.count[0]), splits = a.count[1];
   if (!MOE_CHECK(r >= -1 && r < a.T && splits <= LOSS_SPLITS, 708)) return;
-  const float scale = __int_as_float(a.count[2]), lo = r >= 0 ? a.lab_lo[r] : 0.f;
+  const float scale = __int_as_float(a.count[2]), lo = r >= 0 && a.dh_fmt == FMT_BF16 ? a.lab_lo[r] : 0.f;
   const uint16_t* wl = a.w + static_cast<size_t>(r >= 0 ? label : 0) * a.d;
   for (int c = 4 * threadIdx.x; c < a.d; c += 1024) {
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
@@ -686,20 +701,23 @@ __global__ __launch_bounds__(256) void loss_dh_out_kernel(LossArgs a) {
 
 // ------------------------------------------------------------------ dw = G^T h
 
+// SECOND: as for dh; fp32 only.
+template <bool SECOND>
 __global__ __launch_bounds__(dense::THREADS, 1) void loss_dw_kernel(LossArgs a) {
   using namespace dense;
   __shared__ __attribute__((aligned(1024))) uint8_t ring[dense::RING_BYTES];
   const int count = a.count[0];
   if (!MOE_CHECK(count >= 0 && count <= a.T, 709)) return;
+  if (SECOND && count <= LOSS_LO_ROWS) return;   // the first product took both values
   const TileWalk walk(ceil_div(a.v_len, LT), ceil_div(a.d, LT));
-  const int n = walk.count(), kr = k_rows(count), nk = ceil_div(kr, 32);
+  const int n = walk.count(), kr = SECOND ? count : k_rows(count), nk = ceil_div(kr, 32);
   int vt, nt;
   if (wave_id() >= dense::NMW) {
     const uint32_t ldg = a.ldg * 2, ldh = a.d * 2;
     dense::Opnd oa, ob;
     auto head = [&](int i) {
       walk.tile(i, vt, nt);
-      oa = dense::opnd_ko(make_rsrc(a.g, kr * ldg), ldg, vt * LT);
+      oa = dense::opnd_ko(make_rsrc(a.g + second_at<SECOND>(count, a.ldg), kr * ldg), ldg, vt * LT);
       ob = dense::opnd_ko(make_rsrc(a.hc, kr * ldh), ldh, nt * LT);
       dense::load_head<4>(ring, oa, ob, nk);
     };
@@ -724,7 +742,7 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_dw_kernel(LossArgs a) 
     for (int k = 0; k < MI; ++k)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[k][j] *= scale;
-    if (a.dw_fmt == FMT_BF16) {
+    if (!SECOND && a.dw_fmt == FMT_BF16) {
       uint16_t* dst = static_cast<uint16_t*>(a.dw) + static_cast<size_t>(v0) * a.d + n0;
       dense::store_bf16_tile<8>(
           ring, ncols, [&](int k, int j) { return pack4(acc[k][j][0], acc[k][j][1], acc[k][j][2], acc[k][j][3]); },
@@ -747,8 +765,10 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_dw_kernel(LossArgs a) 
       for (int q = 0; q < 4; ++q) {
         const int rr = 4 * q + (lane >> 4), c = lane & 15, row = 16 * (2 * k + wm) + rr;
         const f32x4 v = *reinterpret_cast<const f32x4*>(sg + rr * 256 + ((c ^ rr) << 4));
-        if (row < vrows && 4 * c < ncols)
-          *reinterpret_cast<f32x4*>(dst + static_cast<size_t>(row) * a.d + 4 * c) = v;
+        if (row < vrows && 4 * c < ncols) {
+          f32x4* p = reinterpret_cast<f32x4*>(dst + static_cast<size_t>(row) * a.d + 4 * c);
+          *p = SECOND ? *p + v : v;
+        }
       }
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
@@ -786,8 +806,8 @@ hipError_t launch_loss_forward(const LossArgs& a, hipStream_t s) {
   }
   const hipError_t e = launch_loss_rows(a, s);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(loss_logits_kernel<false>, dim3(loss_grid(ceil_div(a.T, 64), a.tiles)), dim3(dense::THREADS), 0, s,
-                     a);
+  hipLaunchKernelGGL((loss_logits_kernel<false, false>), dim3(loss_grid(ceil_div(a.T, 64), a.tiles)),
+                     dim3(dense::THREADS), 0, s, a);
   hipLaunchKernelGGL(loss_finish_kernel<1>, dim3(ceil_div(a.T, 4)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
@@ -800,14 +820,21 @@ hipError_t launch_loss_gather(const LossArgs& a, hipStream_t s) {
 // One piece: G, its part of dh, its rows of dw.
 hipError_t launch_loss_piece(const LossArgs& a, hipStream_t s) {
   const long long nm = ceil_div(a.T, 64), nv = ceil_div(a.v_len, LT), nn = ceil_div(a.d, LT);
+  const dim3 grid(loss_grid(nm, nv)), block(dense::THREADS);
   if (a.T > 0) {
     if (loss_stream(a.T, a.V))
       launch_stream<true>(a, static_cast<int>(nv) * (LT / SV), s);
+    else if (loss_pairs(a.dh_fmt, a.dw_fmt))
+      hipLaunchKernelGGL((loss_logits_kernel<true, true>), grid, block, 0, s, a);
     else
-      hipLaunchKernelGGL(loss_logits_kernel<true>, dim3(loss_grid(nm, nv)), dim3(dense::THREADS), 0, s, a);
-    hipLaunchKernelGGL(loss_dh_kernel, dim3(loss_grid(nm, nn * LOSS_SPLITS)), dim3(dense::THREADS), 0, s, a);
+      hipLaunchKernelGGL((loss_logits_kernel<true, false>), grid, block, 0, s, a);
+    const dim3 dh_grid(loss_grid(nm, nn * LOSS_SPLITS));
+    hipLaunchKernelGGL(loss_dh_kernel<false>, dh_grid, block, 0, s, a);
+    if (a.dh_fmt == FMT_F32) hipLaunchKernelGGL(loss_dh_kernel<true>, dh_grid, block, 0, s, a);
   }
-  hipLaunchKernelGGL(loss_dw_kernel, dim3(loss_grid(nv, nn)), dim3(dense::THREADS), 0, s, a);
+  const dim3 dw_grid(loss_grid(nv, nn));
+  hipLaunchKernelGGL(loss_dw_kernel<false>, dw_grid, block, 0, s, a);
+  if (a.dw_fmt == FMT_F32 && a.T > LOSS_LO_ROWS) hipLaunchKernelGGL(loss_dw_kernel<true>, dw_grid, block, 0, s, a);
   return hipGetLastError();
 }
 

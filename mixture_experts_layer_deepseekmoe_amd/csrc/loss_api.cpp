@@ -41,11 +41,11 @@ Layout make_layout(const moe_loss_shape& s) {
   L.zlab = take(T * 4);
   L.forward_total = o;
   o = shared;
-  L.piece = moe::loss_piece(s.T, s.d, s.V);
-  const size_t kr = static_cast<size_t>(moe::loss_k_rows(s.T));
+  const bool pairs = moe::loss_pairs(fmt_of(s.dh_dtype), fmt_of(s.dw_dtype));
+  L.piece = moe::loss_piece(s.T, s.d, s.V, pairs);
   L.lab_lo = take(T * 4);
-  L.hc = take(kr * s.d * 2);
-  L.g = take(kr * L.piece * 2);
+  L.hc = take(static_cast<size_t>(moe::loss_k_rows(s.T)) * s.d * 2);
+  L.g = take(static_cast<size_t>(moe::loss_g_rows(s.T, pairs)) * L.piece * 2);
   L.acc = take(static_cast<size_t>(moe::loss_acc_rows(s.T, s.d, L.piece)) * s.d * 4);
   L.backward_total = o;
   return L;

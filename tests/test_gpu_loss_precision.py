@@ -1,0 +1,97 @@
+"""The gradients of moe_vocab_loss held to the bounds of tests/loss_bounds.py:
+batches of more than 64 labelled rows, every height of a row tile, several row
+tiles, and several pieces of the vocabulary."""
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_layer_deepseekmoe_amd as moe
+from oracle import around_oracle as A
+from tests import loss_bounds as L
+from tests.parity import say
+from tests.test_gpu_loss import _make, _np, _run
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+# Rows are cut into tiles of 64 rows while the tiles fit the card, and with more
+# than 128 column tiles (33100 entries: 130) into tiles of up to 256: here 64;
+# 128; 192; 256 rows, and tiles of 208 and of 256 with a short last one
+SIZES = [(100, 128, 300, 0.0), (770, 192, 65, 0.0), (300, 320, 2000, 0.3), (120, 64, 33100, 0.0), (180, 64, 33100, 0.0),
+         (250, 64, 33100, 0.0), (600, 64, 33100, 0.1), (260, 64, 33100, 0.0), (20, 64, 3000, 0.0), (64, 320, 300, 0.0)]
+
+
+def _check(args, dh_dtype, dw_dtype):
+    h, w, labels, dloss, dlse = args
+    _, _, dh, dw = _run(h, w, labels, dloss, dlse, dh_dtype, dw_dtype)
+    hn, wn, lab = np.nan_to_num(_np(h)), _np(w), labels.numpy()
+    keep = np.flatnonzero((lab >= 0) & (lab < wn.shape[0]))
+    rh, rw, G = A.vocab_loss_backward(hn, wn, lab, dloss.numpy(), dlse.numpy())
+    el = L.logit_error(hn[keep], wn)
+    th, tw = L.bounds(G[keep], hn[keep], wn, np.arange(len(keep)), lab[keep], el, dh_dtype, dw_dtype)
+    assert (np.delete(_np(dh), keep, axis=0) == 0).all()
+    for name, got, ref, tol in (("dh", _np(dh)[keep], rh[keep], th), ("dw", _np(dw), rw, tw)):
+        assert np.isfinite(got).all()
+        over = np.abs(got - ref) - tol
+        assert over.max() <= 0, (name, float(over.max()), np.unravel_index(over.argmax(), over.shape))
+
+
+@pytest.mark.parametrize("T,d,V,masked", SIZES)
+def test_fp32_gradients(T, d, V, masked):
+    """An fp32 gradient is not that of a bf16 operand."""
+    say(f"case: vocab_loss, fp32 gradients T={T} d={d} V={V}")
+    _check(_make(T + 1, T, d, V, masked), "f32", "f32")
+
+
+@pytest.mark.parametrize("dh_dtype,dw_dtype", [("f32", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("T,d,V", [(300, 192, 2000), (40, 64, 1000)])
+def test_mixed_gradients(T, d, V, dh_dtype, dw_dtype):
+    say(f"case: vocab_loss, dh {dh_dtype} dw {dw_dtype} T={T} d={d} V={V}")
+    h, w, labels, dloss, dlse = _make(T, T, d, V, 0.1)
+    _, _, dh, dw = _run(h, w, labels, dloss, dlse, dh_dtype, dw_dtype)
+    # each as with both gradients of its type: bit for bit
+    for k, dt in ((2, dh_dtype), (3, dw_dtype)):
+        assert torch.equal((dh, dw)[k - 2], _run(h, w, labels, dloss, dlse, dt, dt)[k])
+
+
+def _pieces(T, d, V, dtype):
+    """Against float64 on the GPU, by element."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    w = (torch.randn((V, d), generator=g, device=DEV) * (1.5 / d ** 0.5)).bfloat16()
+    h = torch.randn((T, d), generator=g, device=DEV).bfloat16()
+    labels = torch.randint(0, V, (T,), generator=g, device=DEV, dtype=torch.int32)
+    labels[:2] = torch.tensor([0, V - 1])
+    dl = torch.randn(T, generator=g, device=DEV)
+    shape = moe.LossShape(T, d, V, dh_dtype=dtype, dw_dtype=dtype)
+    _, lse = moe.moe_vocab_loss(shape, h, w, labels)
+    dh, dw = moe.moe_vocab_loss_backward(shape, h, w, labels, lse, dl)
+    h, w, lab, rows = h.double(), w.double(), labels.long(), torch.arange(T, device=DEV)
+    G = h @ w.t()
+    el = (d / 32 + 32) * 2.0 ** -24 * float((h.abs() @ w.abs().t()).max())
+    G = torch.softmax(G, 1)
+    G[rows, lab] -= 1
+    G *= dl.double()[:, None]
+    for name, got, g, b in (("dh", dh, G, w), ("dw", dw, G.t(), h)):
+        ref, size = g @ b, g.abs() @ b.abs()
+        tol = (4 * el + 2e-5 + L.U ** 2) * size
+        if dtype == "bf16":
+            r = G.clone()
+            r[rows, lab] = 0
+            r = r * r
+            tol += 8 * L.U / 3 ** 0.5 * ((r if name == "dh" else r.t()) @ (b * b)).sqrt()
+            del r
+            tol += L.U * (ref.abs() + tol)
+        else:
+            tol += 2.0 ** -23 * ref.abs()
+        over = (got.double() - ref).abs() - tol
+        assert over.max() <= 0, (name, float(over.max()), int(over.argmax()) // d)
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T,d,V", [(16384, 64, 16700), (5, 32768, 33000)])
+def test_fp32_gradients_in_pieces(T, d, V):
+    """Three pieces of the vocabulary (a pair of bf16 values takes twice the
+    room), and two of a wide matrix."""
+    say(f"case: vocab_loss in pieces, fp32 gradients T={T} d={d} V={V}")
+    _pieces(T, d, V, "f32")
