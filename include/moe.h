@@ -417,8 +417,8 @@ int moe_block_out_backward(const moe_block_shape* shape, const float* dout, cons
  *   A gradient in F32 is summed from G as pairs of bf16 values (G to 2^-16), a
  *   product more each: about 1.6 times the time of bf16 gradients for both.
  *   A gradient in BF16 is summed from G rounded once to bf16 (2^-8).  What that
- *   takes off at a token's label is added to dh again, and to dw of up to 64
- *   tokens what it takes off anywhere; G is held over the mantissa of the
+ *   takes off at a token's label is added to dh and dw again, and to dw of up to
+ *   64 tokens what it takes off anywhere; G is held over the mantissa of the
  *   largest finite |dloss|, so equal weights are not rounded at all.
  * Products are bf16 with fp32 accumulation; every sum runs in a fixed order
  * (bit-reproducible).  The forward and the backward may use different

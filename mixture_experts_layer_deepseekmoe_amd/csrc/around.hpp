@@ -117,6 +117,8 @@ struct LossArgs {
   uint16_t* hc;           // [loss_k_rows(T)][d] the rows' hidden rows, one after the other
   uint16_t* g;            // [loss_g_rows(T, pairs)][ldg] a piece's G = dlogits / scale
   float* lab_lo;          // [T] by row: the rounding error of G at the label
+  int32_t* lab_first;     // [tiles of V + 1] where loss_labels: a tile's first entry of
+  uint32_t* lab_list;     // [T] rows by their label's tile: row << 8 | label % 256
   float* acc;             // [splits][row tiles of 256][d] dh by row (loss_acc_rows)
   int ldg;                // loss_piece
   int dh_fmt, dw_fmt;     // fp32: from pairs of bf16 values of G
@@ -163,6 +165,9 @@ constexpr int LOSS_LO_ROWS = 64;
 constexpr int loss_k_rows(int T) {   // the most there can be
   return T < LOSS_LO_ROWS ? 2 * T : T < 2 * LOSS_LO_ROWS ? 2 * LOSS_LO_ROWS : T;
 }
+// Of more rows, a bf16 dw takes the rounding errors at the labels alone, tile by
+// tile of the vocabulary, from a list of the rows by their label's tile.
+inline bool loss_labels(int T, int dw_fmt) { return dw_fmt == FMT_BF16 && T > LOSS_LO_ROWS; }
 constexpr long long loss_g_rows(long long T, bool pairs) {
   return pairs ? 2 * T : loss_k_rows(static_cast<int>(T));
 }

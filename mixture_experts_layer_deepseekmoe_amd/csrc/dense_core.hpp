@@ -242,28 +242,46 @@ __device__ __forceinline__ void load_head(uint8_t* ring, const Opnd& a, const Op
   if (nk > 0) issue_pair<NA>(a, b, ring, 0);
   if (nk > 2) issue_pair<NA>(a, b, ring, 2);
 }
-template <int NA>
-__device__ __forceinline__ void load_body(uint8_t* ring, const Opnd& a, const Opnd& b, int nk) {
+//
+// `more` further pairs may follow those of nk, in steps as the rest (at least two
+// pairs are the tile's own then): fetch(k) starts what pair k needs, issue(k, s)
+// then issues it into the stages of steps s, s + 1, with as many DMA instructions
+// as a pair's first half has.
+template <int NA, class F, class I>
+__device__ __forceinline__ void load_body(uint8_t* ring, const Opnd& a, const Opnd& b, int nk, int more, F&& fetch,
+                                          I&& issue) {
   constexpr int H0 = 2 * first_ops<NA>(), N = 2 * (NA + NLI);
-  const int np = (nk + 1) / 2;
+  const int own = (nk + 1) / 2, np = own + more;
   if (np <= 0) return;
   if (np > 1)
     wait_vm<N>();   // pair 0
   else
     wait_vm<0>();
   block_barrier();
-  for (int q = 0; q < np; ++q) {
+  int q = 0;
+  for (; q + 2 < own; ++q) {
     block_barrier();   // A_q
-    const bool more = q + 2 < np;
-    if (more) {
-      issue_half<0, NA>(a, b, ring, 2 * (q + 2));
+    issue_half<0, NA>(a, b, ring, 2 * (q + 2));
+    wait_vm<H0>();     // pair q + 1
+    block_barrier();   // B_q
+    issue_half<1, NA>(a, b, ring, 2 * (q + 2));
+  }
+  if (more > 0) fetch(0);
+  for (; q < np; ++q) {
+    block_barrier();   // A_q
+    if (q + 2 < np) {
+      issue(q + 2 - own, 2 * (q + 2));
       wait_vm<H0>();   // pair q + 1
     } else {
       wait_vm<0>();    // pair q + 1 (if any) is the newest
     }
     block_barrier();   // B_q
-    if (more) issue_half<1, NA>(a, b, ring, 2 * (q + 2));
+    if (q + 3 < np) fetch(q + 3 - own);
   }
+}
+template <int NA>
+__device__ __forceinline__ void load_body(uint8_t* ring, const Opnd& a, const Opnd& b, int nk) {
+  load_body<NA>(ring, a, b, nk, 0, [](int) {}, [](int, int) {});
 }
 
 // f.template operator()<NSUB>() with NSUB the number of 32-row steps (2, 4, 6 or

@@ -18,7 +18,7 @@
 //
 // The large products are bound by the matrix cores at the clock the card's power
 // holds (1.75-1.95 GHz; 76% of the cycles in the logits' kernel are MFMAs).
-// 3072 rows, d = 7168, V = 65536 (2.89 TFLOP each): logits 2.05 ms (1.41
+// 4096 tokens, a quarter ignored, d = 7168, V = 65536 (2.89 TFLOP each): logits 2.05 ms (1.41
 // PFLOP/s; with the G epilogue 2.1), dh 2.2-2.3 ms (1.25-1.3), dw 2.4 ms (1.2).
 // Library products of the same with 4096 rows: 1.23-1.26, 0.92-0.94, 0.92-1.06 on
 // operands laid out as these are.  Few tokens are bound by reading w once.
@@ -35,14 +35,17 @@
 // does not average out:
 //   dh   each row's rounding error at its label times the label's row of w is
 //        added in fp32 where dh is written;
-//   dw   up to 64 rows are summed with their rounding errors (LOSS_LO_ROWS);
+//   dw   up to 64 rows are summed with their rounding errors (LOSS_LO_ROWS); of
+//        more, a tile's K-steps are followed by those of its labels (LabelSteps);
 //   both G is held over the mantissa of the largest dloss: with the equal
 //        weights of a mean the label's elements are p - 1, near a power of two,
 //        and not all off by the one rounding of the weight.
-// Against 64 bits, with bf16 outputs: 1.7e-3 normwise for dh and few rows (the
-// outputs' own rounding), 2.2e-3 for dw of many; 2.4e-3 without these three, and
-// up to 2.9e-3 for few rows.  They cost 2 us of 67 (207 rows, 10007 entries, d =
-// 512) and 0.5-1% of the large products.
+// Against 64 bits, with bf16 outputs: 1.7e-3 normwise, the outputs' own rounding
+// (2.4e-3 without these, up to 2.9e-3 for few rows; 2.2e-3 of dw without its labels'
+// steps).  They cost 4 us of 71 (207 rows, 10007 entries, d = 512) and 1% of the large
+// products.  The labels' steps: a pair to a tile for 4096 tokens, a quarter ignored,
+// 65536 entries, 0.3% (8.80 / 8.77 ms for d = 7168); 16 pairs beside a tile's own 64 for 4096 rows of 1000 entries, 199 /
+// 149 us (d = 256).
 #include "around.hpp"
 #include "dense_core.hpp"
 
@@ -191,9 +194,59 @@ __global__ __launch_bounds__(1024) void loss_rows_kernel(LossArgs a) {
   }
 }
 
-// hc[r] = h[rows[r]], and dw's rows of few tokens once more
+// The rows whose label lies in tile k of the vocabulary, in order (four waves, a
+// quarter of the tokens each: the rows before them are counted, then listed).
+__device__ __forceinline__ void list_labels(const LossArgs& a, int k) {
+  __shared__ int before[4], inside[4];
+  const int w = wave_id(), lane = threadIdx.x & 63;
+  const int per = (a.T + 255) / 256 * 64, t0 = w * per, t1 = min(a.T, t0 + per);
+  auto tile_of = [&](int t) {
+    const int lab = t < t1 ? a.labels[t] : -1;
+    return lab >= 0 && lab < a.V ? lab / LT : -1;
+  };
+  int b = 0, n = 0;
+#pragma unroll 4
+  for (int t = t0 + lane; t < t1; t += 64) {
+    const int x = tile_of(t);
+    b += x >= 0 && x < k;
+    n += x == k;
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) {
+    b += __shfl_xor(b, off);
+    n += __shfl_xor(n, off);
+  }
+  if (lane == 0) {
+    before[w] = b;
+    inside[w] = n;
+  }
+  __syncthreads();
+  const int first = before[0] + before[1] + before[2] + before[3];
+  if (threadIdx.x == 0) a.lab_first[k] = first;
+  if (threadIdx.x == 0 && k == ceil_div(a.V, LT) - 1)
+    a.lab_first[k + 1] = first + inside[0] + inside[1] + inside[2] + inside[3];
+  int at = first;
+  for (int i = 0; i < w; ++i) at += inside[i];
+  for (int t = t0 + lane; t - lane < t1; t += 64) {
+    const bool hit = tile_of(t) == k;
+    const unsigned long long m = __ballot(hit);
+    if (hit) {
+      const int o = at + __popcll(m & ((1ULL << lane) - 1)), r = a.pos[t];
+      if (MOE_CHECK(o < a.T && r >= 0 && r < a.T, 710))
+        a.lab_list[o] = static_cast<uint32_t>(r) << 8 | static_cast<uint32_t>(a.labels[t] % LT);
+    }
+    at += __popcll(m);
+  }
+}
+
+// hc[r] = h[rows[r]], and dw's rows of few tokens once more; the blocks after
+// those list the labels by tile.
 __global__ __launch_bounds__(256) void loss_gather_kernel(LossArgs a) {
-  const int r = blockIdx.x, count = a.count[0];
+  const int r = blockIdx.x, count = a.count[0], lists = loss_k_rows(a.T);
+  if (r >= lists) {
+    if (count > LOSS_LO_ROWS) list_labels(a, r - lists);
+    return;
+  }
   if (r >= k_rows(count)) return;
   const int t = a.rows[r < count ? r : r - count];
   if (!MOE_CHECK(t >= 0 && t < a.T, 701)) return;
@@ -701,6 +754,69 @@ __global__ __launch_bounds__(256) void loss_dh_out_kernel(LossArgs a) {
 
 // ------------------------------------------------------------------ dw = G^T h
 
+// The K-steps that follow a tile's own: what rounding took off G at its labels (in
+// bf16), times those rows of h, 32 rows of the tile's list to a step.  The load
+// waves write A's stage, zero but for each row's label, and gather B's from hc.
+struct LabelSteps {
+  int first, last;   // the tile's entries of the list
+  __device__ __forceinline__ LabelSteps(const LossArgs& a, bool any, int tile, int count) {
+    first = any ? a.lab_first[tile] : 0;
+    last = any ? a.lab_first[tile + 1] : 0;
+    if (!MOE_CHECK(first >= 0 && first <= last && last <= count, 711)) first = last;
+  }
+  __device__ __forceinline__ int pairs() const { return (last - first + 63) / 64; }
+
+  // Load waves: this lane's entries of pair k, ahead of their use, and that pair
+  // into the stages of steps s, s + 1 (hc's resource, columns from col0).
+  static constexpr uint32_t NONE = ~0u;
+  uint32_t e[2][dense::NLI];
+  static __device__ __forceinline__ int k_row(int q) {   // as opnd_ko's
+    return 2 * (wave_id() - dense::NMW + dense::NLW * q) + (threadIdx.x & 63) / 32;
+  }
+  __device__ __forceinline__ void fetch(const LossArgs& a, int k) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int q = 0; q < dense::NLI; ++q) {
+        const int at = first + 64 * k + 32 * h + k_row(q);
+        e[h][q] = at < last ? a.lab_list[at] : NONE;
+      }
+  }
+  __device__ __forceinline__ void issue(const LossArgs& a, rsrc_t rh, uint8_t* ring, int s, int col0, int count) const {
+    const int w = wave_id() - dense::NMW, lane = threadIdx.x & 63;
+    auto chunk = [&](int q) __attribute__((always_inline)) { return (lane & 31) ^ dense::xko(k_row(q)); };
+    auto ok = [&](uint32_t x) __attribute__((always_inline)) {
+      return x != NONE && MOE_CHECK(static_cast<int>(x >> 8) < count, 712);
+    };
+    float lo[2][dense::NLI];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int q = 0; q < dense::NLI; ++q) {
+        const uint32_t x = e[h][q];
+        lo[h][q] = ok(x) && (x & 255) >> 3 == static_cast<uint32_t>(chunk(q)) ? a.lab_lo[x >> 8] : 0.f;
+      }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int q = 0; q < dense::NLI; ++q) {
+        const uint32_t c = e[h][q] & 255, v = bf16x2(lo[h][q], 0.f) << 16 * (c & 1), p = c >> 1 & 3;
+        *reinterpret_cast<uint4*>(dense::stage(ring, s + h) + 1024 * (w + dense::NLW * q) + 16 * lane) =
+            make_uint4(p == 0 ? v : 0, p == 1 ? v : 0, p == 2 ? v : 0, p == 3 ? v : 0);
+      }
+    dense::wait_lgkm0();   // written before a barrier says so
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int q = 0; q < dense::NLI; ++q) {
+        const uint32_t x = e[h][q], r = ok(x) ? x >> 8 : static_cast<uint32_t>(count);   // past the resource: zeros
+        dma16(rh, r * (a.d * 2u) + col0 * 2 + 16 * chunk(q), 0,
+              dense::stage(ring, s + h) + dense::OPB + 1024 * (w + dense::NLW * q));
+      }
+  }
+};
+static_assert(dense::first_ops<4>() == dense::NLI, "as many DMA instructions as a pair's first half: load_body");
+
 // SECOND: as for dh; fp32 only.
 template <bool SECOND>
 __global__ __launch_bounds__(dense::THREADS, 1) void loss_dw_kernel(LossArgs a) {
@@ -711,6 +827,8 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_dw_kernel(LossArgs a) 
   if (SECOND && count <= LOSS_LO_ROWS) return;   // the first product took both values
   const TileWalk walk(ceil_div(a.v_len, LT), ceil_div(a.d, LT));
   const int n = walk.count(), kr = SECOND ? count : k_rows(count), nk = ceil_div(kr, 32);
+  const bool labels = !SECOND && a.dw_fmt == FMT_BF16 && count > LOSS_LO_ROWS;
+  const int tile0 = a.v_first / LT, own = (nk + 1) / 2 * 2;   // the labels' steps start a pair (65 rows: the third)
   int vt, nt;
   if (wave_id() >= dense::NMW) {
     const uint32_t ldg = a.ldg * 2, ldh = a.d * 2;
@@ -723,7 +841,10 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_dw_kernel(LossArgs a) 
     };
     if (n > 0) head(0);
     for (int i = 0; i < n; ++i) {
-      dense::load_body<4>(ring, oa, ob, nk);
+      LabelSteps ls(a, labels, tile0 + vt, count);
+      load_body<4>(
+          ring, oa, ob, nk, ls.pairs(), [&](int k) __attribute__((always_inline)) { ls.fetch(a, k); },
+          [&](int, int st) __attribute__((always_inline)) { ls.issue(a, ob.r, ring, st, nt * LT, count); });
       block_barrier();   // the tile's stages are read
       if (i + 1 < n) head(i + 1);
     }
@@ -734,8 +855,9 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_dw_kernel(LossArgs a) 
   for (int i = 0; i < n; ++i) {
     walk.tile(i, vt, nt);
     const int v0 = a.v_first + vt * LT, vrows = min(LT, a.V - v0), n0 = nt * LT + 64 * wn, ncols = min(64, a.d - n0);
+    const LabelSteps ls(a, labels, tile0 + vt, count);
     Acc acc;
-    dense::mfma_loop<KO, KO, 8>(ring, nk, acc);
+    dense::mfma_loop<KO, KO, 8>(ring, own + 2 * ls.pairs(), acc);
     block_barrier();   // the tile's stages are read
     if (ncols <= 0) continue;
 #pragma unroll
@@ -813,7 +935,8 @@ hipError_t launch_loss_forward(const LossArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_loss_gather(const LossArgs& a, hipStream_t s) {
-  if (a.T > 0) hipLaunchKernelGGL(loss_gather_kernel, dim3(loss_k_rows(a.T)), dim3(256), 0, s, a);
+  const int lists = loss_labels(a.T, a.dw_fmt) ? ceil_div(a.V, LT) : 0;
+  if (a.T > 0) hipLaunchKernelGGL(loss_gather_kernel, dim3(loss_k_rows(a.T) + lists), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -24,7 +24,7 @@ int validate_shape(const moe_loss_shape* s) {
 // Workspace map (byte offsets, each 256-byte aligned).
 struct Layout {
   size_t rows, pos, count, part, zlab, forward_total;
-  size_t lab_lo, hc, g, acc, backward_total;
+  size_t lab_lo, lab_first, lab_list, hc, g, acc, backward_total;
   int piece;
 };
 
@@ -44,6 +44,9 @@ Layout make_layout(const moe_loss_shape& s) {
   const bool pairs = moe::loss_pairs(fmt_of(s.dh_dtype), fmt_of(s.dw_dtype));
   L.piece = moe::loss_piece(s.T, s.d, s.V, pairs);
   L.lab_lo = take(T * 4);
+  const bool labels = moe::loss_labels(s.T, fmt_of(s.dw_dtype));
+  L.lab_first = take(labels ? (static_cast<size_t>((s.V + moe::LOSS_TILE - 1) / moe::LOSS_TILE) + 1) * 4 : 0);
+  L.lab_list = take(labels ? T * 4 : 0);
   L.hc = take(static_cast<size_t>(moe::loss_k_rows(s.T)) * s.d * 2);
   L.g = take(static_cast<size_t>(moe::loss_g_rows(s.T, pairs)) * L.piece * 2);
   L.acc = take(static_cast<size_t>(moe::loss_acc_rows(s.T, s.d, L.piece)) * s.d * 4);
@@ -118,6 +121,8 @@ int moe_vocab_loss_backward(const moe_loss_shape* shape, const void* h, const vo
   a.dloss = dloss;
   a.dlse = dlse;
   a.lab_lo = at<float>(workspace, L.lab_lo);
+  a.lab_first = at<int32_t>(workspace, L.lab_first);
+  a.lab_list = at<uint32_t>(workspace, L.lab_list);
   a.hc = at<uint16_t>(workspace, L.hc);
   a.g = at<uint16_t>(workspace, L.g);
   a.acc = at<float>(workspace, L.acc);

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import mixture_experts_layer_deepseekmoe_amd as moe
+from mixture_experts_layer_deepseekmoe_amd import binding as B
 from oracle import around_oracle as A
 from tests import loss_bounds as L
 from tests.parity import say
@@ -95,3 +96,56 @@ def test_fp32_gradients_in_pieces(T, d, V):
     room), and two of a wide matrix."""
     say(f"case: vocab_loss in pieces, fp32 gradients T={T} d={d} V={V}")
     _pieces(T, d, V, "f32")
+
+
+@pytest.mark.parametrize("T,d,V,masked", SIZES)
+def test_bf16_gradients(T, d, V, masked):
+    """What bf16 takes off G at a label comes back, in dh and in dw, whatever the
+    number of rows."""
+    say(f"case: vocab_loss, bf16 gradients T={T} d={d} V={V}")
+    _check(_make(T + 1, T, d, V, masked), "bf16", "bf16")
+
+
+@pytest.mark.parametrize("labels", [lambda t: 5 + 0 * t, lambda t: 512 + t % 16, lambda t: 33099 - t % 3, lambda t: 256 * (t % 9)],
+                         ids=["one", "one subtile", "the last tile", "a tile's first"])
+def test_bf16_gradients_of_repeated_labels(labels):
+    """Many rows to one tile of the vocabulary, the other tiles none.  Labels
+    repeat, so dloss has random signs and the sums are still of few terms."""
+    say("case: vocab_loss, bf16 gradients of repeated labels")
+    h, w, lab, dloss, dlse = _make(9, 300, 192, 33100)
+    lab = labels(torch.arange(300, dtype=torch.int32)).int()
+    lab[::7] = -100
+    h[::7] = float("nan")
+    _check((h, w, lab, dloss, dlse), "bf16", "bf16")
+
+
+@pytest.mark.parametrize("T,d,V", [(16384, 64, 16700), (5, 32768, 33000)])
+def test_bf16_gradients_in_pieces(T, d, V):
+    """Two pieces of the vocabulary: rows whose label is in either."""
+    say(f"case: vocab_loss in pieces, bf16 gradients T={T} d={d} V={V}")
+    _pieces(T, d, V, "bf16")
+
+
+def test_bf16_gradients_repeat_without_the_ignored():
+    """Bit for bit, with and without the ignored tokens, and again."""
+    say("case: vocab_loss, bf16 gradients without the ignored tokens")
+    h, w, labels, dl, dz = _make(5, 900, 256, 1500, 0.6)
+    keep = (labels >= 0) & (labels < 1500)
+    a = _run(h, w, labels, dl, dz, "bf16", "bf16")
+    b = _run(h[keep], w, labels[keep], dl[keep], dz[keep], "bf16", "bf16")
+    again = _run(h, w, labels, dl, dz, "bf16", "bf16")
+    assert torch.equal(a[2][keep.to(DEV)], b[2]) and torch.equal(a[3], b[3])
+    assert torch.equal(a[2], again[2]) and torch.equal(a[3], again[3])
+
+
+def test_bf16_gradients_debug_build():
+    say("case: debug build, vocab_loss with bf16 gradients")
+    args = _make(3, 700, 192, 20000, 0.3)
+    a = _run(*args, "bf16", "bf16")
+    prev = B.use_library(B.DEBUG_LIB_PATH)
+    try:
+        b = _run(*args, "bf16", "bf16")
+    finally:
+        B.restore_library(prev)
+    for x, y in zip(a, b):
+        assert torch.equal(x, y)
