@@ -424,7 +424,8 @@ int moe_block_out_backward(const moe_block_shape* shape, const float* dout, cons
  * (bit-reproducible).  The forward and the backward may use different
  * workspaces.
  * Limits: d a multiple of 64, at most 32768; V at most 2^24; T below 2^22,
- * (T + 64) * d * 2 below 2^32, ceil(T/256) * ceil(V/256) below about 5.5 million.
+ * (T + 64) * d * 2 below 2^32, ceil(T/256) * ceil(V/256) at most 2^25 (64 GiB of
+ * the forward's workspace).
  */
 typedef struct {
   int32_t T, d, V;

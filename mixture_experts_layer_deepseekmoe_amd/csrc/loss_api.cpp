@@ -6,6 +6,7 @@ namespace {
 
 using namespace moe::api;
 
+constexpr long long kMaxPartials = 64LL << 30;
 constexpr int kMaxTokens = 1 << 22;   // (T + 64) rows of G's smallest piece stay below 2^32 bytes
 
 int validate_shape(const moe_loss_shape* s) {
@@ -15,9 +16,10 @@ int validate_shape(const moe_loss_shape* s) {
   if (s->d % 64 != 0 || s->d > 32768 || s->T >= kMaxTokens || s->V > (1 << 24)) return MOE_ERR_UNSUPPORTED;
   // the hidden rows are addressed with 32-bit byte offsets, a K-step of rows past their end
   if ((static_cast<long long>(s->T) + 64) * s->d * 2 >= (1LL << 32)) return MOE_ERR_UNSUPPORTED;
-  // blocks of one launch
+  // the forward's (max, sum) of every token and tile of 256 entries: 64 GiB of workspace (the kernels
+  // themselves walk any number of tiles)
   const long long tiles = (static_cast<long long>(s->T) + 255) / 256 * ((s->V + 255LL) / 256);
-  if (tiles * 768 >= (1LL << 32) - (1 << 16)) return MOE_ERR_UNSUPPORTED;
+  if (tiles * 256 * static_cast<long long>(sizeof(float2)) > kMaxPartials) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

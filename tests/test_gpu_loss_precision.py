@@ -149,3 +149,48 @@ def test_bf16_gradients_debug_build():
         B.restore_library(prev)
     for x, y in zip(a, b):
         assert torch.equal(x, y)
+
+
+def test_all_of_a_large_vocabulary():
+    """22100 tokens over 2^24 entries (5.7 million tiles of logits), sampled: rows
+    of loss and dh, entries of dw."""
+    say("case: vocab_loss, 22100 tokens over 2^24 entries")
+    T, d, V = 22100, 64, 1 << 24
+    g = torch.Generator(device=DEV).manual_seed(4)
+    w = torch.empty((V, d), dtype=torch.bfloat16, device=DEV)
+    for v in range(0, V, 1 << 22):
+        w[v:v + (1 << 22)] = (torch.randn((1 << 22, d), generator=g, device=DEV) * (1.5 / d ** 0.5)).bfloat16()
+    h = torch.randn((T, d), generator=g, device=DEV).bfloat16()
+    labels = torch.randint(0, V, (T,), generator=g, device=DEV, dtype=torch.int32)
+    labels[7] = V - 1
+    dl = torch.randn(T, generator=g, device=DEV)
+    shape = moe.LossShape(T, d, V, dh_dtype="bf16", dw_dtype="bf16")
+    loss, lse = moe.moe_vocab_loss(shape, h, w, labels)
+    dh, dw = moe.moe_vocab_loss_backward(shape, h, w, labels, lse, dl)
+    # |l| <= 8 d^(1/2) 1.5 or so: products and sums of 64 terms, 2^24 exponentials joined in fp32
+    rows = torch.tensor([0, 7, 8191, 16384, T - 1], device=DEV)
+    hr, lab = h[rows].double(), labels[rows].long()
+    el = (d / 32 + 32) * 2.0 ** -24 * float(hr.abs().sum(1).max() * w.abs().max().double())
+    s, gw = torch.zeros(5, dtype=torch.float64, device=DEV), torch.zeros((5, d), dtype=torch.float64, device=DEV)
+    for v in range(0, V, 1 << 21):
+        p = torch.exp(hr @ w[v:v + (1 << 21)].double().t())
+        s += p.sum(1)
+        gw += p @ w[v:v + (1 << 21)].double()
+    rz = s.log()
+    rl = rz - (hr * w[lab].double()).sum(1)
+    assert (lse[rows].double() - rz).abs().max() <= 2 * el + 2e-6 * (1 + float(rz.max()))
+    assert (loss[rows].double() - rl).abs().max() <= 2 * el + 4e-6 * (1 + float(rz.max()))
+    ref = dl[rows].double()[:, None] * (gw / s[:, None] - w[lab].double())
+    size = dl[rows].abs().double()[:, None] * (float(w.abs().max()) + w[lab].abs().double())
+    assert ((dh[rows].double() - ref).abs() <= L.U * ref.abs() + (4 * el + 2e-5 + 2 * L.U ** 2) * size).all()
+    # dw: a label's row (that of token 7, the last entry) is -dl h but for the others' p <= e^12 / 2^24
+    for t in (7, 0, 16384):
+        v = int(labels[t])
+        G = torch.exp(h.double() @ w[v].double() - lse.double()) * dl.double()
+        G[labels.long() == v] -= dl.double()[labels.long() == v]
+        ref, size = G @ h.double(), G.abs() @ h.double().abs()
+        rest = torch.where(labels.long() == v, torch.zeros_like(G), G)
+        tol = L.U * ref.abs() + (4 * el + 2e-5 + 2 * L.U ** 2) * size + 8 * L.U * ((rest ** 2) @ (h.double() ** 2)).sqrt()
+        assert ((dw[v].double() - ref).abs() <= tol).all()
+    del w, dw
+    torch.cuda.empty_cache()
