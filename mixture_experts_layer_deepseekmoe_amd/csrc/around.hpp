@@ -30,6 +30,7 @@ struct BlockOutArgs {
   const float* gate;      // [ceil(T / gate_rows)][d] (gate_rows 0: one row), or null: ones
   const float* w_next;    // [d], or null: no next norm
   int T, d, x_fmt, n_fmt, y_fmt, gate_rows;
+  long long gates;        // rows of gate
   float eps, res_scale;
   void* x_out;            // [T][d] x_fmt
   void* n_next;           // [T][d] n_fmt (with w_next)
@@ -63,6 +64,7 @@ struct BlockBwdArgs {
   float* part;            // block_bwd_floats(...) of scratch
   // set by the launcher (block_bwd_plan)
   int whole_gates, runs, rows;
+  long long blocks;
 };
 
 // A backward block takes `rows` rows and leaves one row of partial column sums
@@ -105,6 +107,8 @@ struct LossArgs {
   int32_t* rows;          // [T] token of each row
   int32_t* pos;           // [T] row of each token, or -1
   int32_t* count;         // [3] rows; backward: splits of dh's sum, the gradients' scale (fp32)
+  // what the workspace holds, for the checks of the debug build
+  long long g_rows, acc_rows;
   float* loss;            // [T] (forward)
   float* lse;             // [T] (backward: read)
   // forward
@@ -115,7 +119,7 @@ struct LossArgs {
   const float* dloss;     // [T]
   const float* dlse;      // [T], or null
   uint16_t* hc;           // [loss_k_rows(T)][d] the rows' hidden rows, one after the other
-  uint16_t* g;            // [loss_g_rows(T, pairs)][ldg] a piece's G = dlogits / scale
+  uint16_t* g;            // [g_rows = loss_g_rows(T, pairs)][ldg] a piece's G = dlogits / scale
   float* lab_lo;          // [T] by row: the rounding error of G at the label
   int32_t* lab_first;     // [tiles of V + 1] where loss_labels: a tile's first entry of
   uint32_t* lab_list;     // [T] rows by their label's tile: row << 8 | label % 256

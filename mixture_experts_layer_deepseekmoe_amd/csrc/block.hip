@@ -141,6 +141,7 @@ template <int XF, int NF, int NV, int TPB>
 __global__ __launch_bounds__(TPB) void block_in_kernel(BlockInArgs a) {
   __shared__ float red[TPB / 64];
   const size_t row = blockIdx.x;
+  if (!MOE_CHECK(row < static_cast<size_t>(a.T) && a.d <= 8 * TPB * NV, 605)) return;
   float x[NV][8];
   Raw8 raw[NV];
 #pragma unroll
@@ -207,6 +208,7 @@ __global__ __launch_bounds__(TPB) void block_out_kernel(BlockOutArgs a) {
     if (a.rstd != nullptr && threadIdx.x == 0) a.rstd[row] = r;
   }
   const size_t grow = a.gate != nullptr && a.gate_rows > 0 ? row / a.gate_rows : 0;
+  if (!MOE_CHECK(row < static_cast<size_t>(a.T) && (a.gate == nullptr || grow < static_cast<size_t>(a.gates)), 601)) return;
   ss = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -274,6 +276,7 @@ template <int VF, int SF, int NV, int TPB>
 __global__ __launch_bounds__(TPB) void block_bwd_kernel(BlockBwdArgs a) {
   __shared__ float red[2][TPB / 64];
   const BwdRows rows = bwd_rows(a);
+  if (!MOE_CHECK(blockIdx.x < a.blocks && rows.t0 >= 0 && rows.t1 <= a.T, 602)) return;
   float acc[NV][8], gacc[NV][8], gw[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
@@ -283,6 +286,7 @@ __global__ __launch_bounds__(TPB) void block_bwd_kernel(BlockBwdArgs a) {
   for (long long t = rows.t0; t < rows.t1; ++t) {
     const size_t row = static_cast<size_t>(t), ro = row * a.d;
     const size_t gro = a.gate != nullptr ? row / a.gate_len * a.d : 0;
+    if (!MOE_CHECK(a.gate == nullptr || t / a.gate_len < a.gates, 603)) return;
     const bool first = t == rows.t0 || (a.whole_gates && t % a.gate_len == 0);   // of its gate, here
     const float r = a.w != nullptr ? a.rstd[row] : 1.f;
     Raw8 rg[NV], rs[NV], rv[NV], rk[NV], rr[NV];
@@ -399,6 +403,7 @@ struct ColSumArgs {
   const float* gate;   // nullable: ones
   float* dgate;        // nullable
   float* out;          // nullable
+  long long rows, gates;   // rows of part and of gate from here on (the debug build's checks)
 };
 constexpr int CS_LANES = 64;
 constexpr int CS_GATES = 8;   // up to so many gates are summed by one launch
@@ -407,6 +412,10 @@ __global__ __launch_bounds__(1024) void block_colsum_kernel(ColSumArgs a) {
   const int tc = threadIdx.x & 15, l = threadIdx.x >> 4, w = threadIdx.x >> 6;
   const int c = 64 * blockIdx.x + 4 * tc;
   const size_t g0 = static_cast<size_t>(blockIdx.y) * a.n_gates;
+  if (!MOE_CHECK(a.n_gates <= CS_GATES && (g0 + a.n_gates) * a.n <= static_cast<size_t>(a.rows) &&
+                     ((a.gate == nullptr && a.dgate == nullptr) || g0 + a.n_gates <= static_cast<size_t>(a.gates)),
+                 604))
+    return;
   for (int k = 0; k < a.n_gates; ++k) {
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (c < a.d) {
@@ -508,6 +517,7 @@ hipError_t launch_block_bwd(BlockBwdArgs a, hipStream_t s) {
   a.whole_gates = p.whole_gates;
   a.runs = p.runs;
   a.rows = p.rows;
+  a.blocks = p.blocks;
   if (p.blocks > 0) {
     const dim3 grid(static_cast<unsigned>(p.blocks));
     hipError_t e = with_bwd_shape(a.d, [&]<int NV, int TPB>() {
@@ -527,25 +537,28 @@ hipError_t launch_block_bwd(BlockBwdArgs a, hipStream_t s) {
   const unsigned cb = static_cast<unsigned>(ceil_div(a.d, 64));
   if (p.whole_gates) {
     if (a.dw == nullptr) return hipSuccess;
-    const ColSumArgs c{a.part, static_cast<int>(p.blocks), a.d, 1, nullptr, nullptr, nullptr, a.dw};
+    const ColSumArgs c{a.part, static_cast<int>(p.blocks), a.d, 1, nullptr, nullptr, nullptr, a.dw, p.blocks, 1};
     hipLaunchKernelGGL(block_colsum_kernel, dim3(cb, 1), dim3(1024), 0, s, c);
     return hipGetLastError();
   }
   if (a.dw == nullptr && a.dgate == nullptr) return hipSuccess;
   if (p.gates <= CS_GATES) {
-    const ColSumArgs c{a.part, p.runs, a.d, static_cast<int>(p.gates), a.w, a.gate, a.dgate, a.dw};
+    const ColSumArgs c{a.part, p.runs, a.d, static_cast<int>(p.gates), a.w, a.gate, a.dgate, a.dw, p.blocks, p.gates};
     hipLaunchKernelGGL(block_colsum_kernel, dim3(cb, 1), dim3(1024), 0, s, c);
     return hipGetLastError();
   }
   // many gates: a block each, then the sum of their shares of dw
   float* q = a.part + static_cast<size_t>(p.blocks) * a.d;
-  const ColSumArgs c1{a.part, p.runs, a.d, 1, a.w, a.gate, a.dgate, a.dw == nullptr ? nullptr : q};
+  const ColSumArgs c1{a.part, p.runs, a.d, 1, a.w, a.gate, a.dgate, a.dw == nullptr ? nullptr : q,
+                      p.blocks, p.gates};
   // the grid's second dimension holds at most 65535 gates
   for (long long g0 = 0; g0 < p.gates; g0 += 32768) {
     ColSumArgs cg = c1;
     const long long n = p.gates - g0 < 32768 ? p.gates - g0 : 32768;
     const size_t go = static_cast<size_t>(g0) * a.d;
     cg.part += go * p.runs;
+    cg.rows -= g0 * p.runs;
+    cg.gates -= g0;
     if (cg.gate != nullptr) cg.gate += go;
     if (cg.dgate != nullptr) cg.dgate += go;
     if (cg.out != nullptr) cg.out += go;
@@ -554,7 +567,7 @@ hipError_t launch_block_bwd(BlockBwdArgs a, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   if (a.dw != nullptr) {
-    const ColSumArgs c2{q, static_cast<int>(p.gates), a.d, 1, nullptr, nullptr, nullptr, a.dw};
+    const ColSumArgs c2{q, static_cast<int>(p.gates), a.d, 1, nullptr, nullptr, nullptr, a.dw, p.gates, 1};
     hipLaunchKernelGGL(block_colsum_kernel, dim3(cb, 1), dim3(1024), 0, s, c2);
   }
   return hipGetLastError();

@@ -97,6 +97,7 @@ int moe_block_out(const moe_block_shape* shape, const void* x, const void* y, co
   a.n_fmt = fmt_of(s.n_dtype);
   a.y_fmt = fmt_of(s.y_dtype);
   a.gate_rows = s.gate_rows;
+  a.gates = gate_count(s);
   a.eps = s.eps;
   a.res_scale = s.res_scale;
   a.x_out = x_out;

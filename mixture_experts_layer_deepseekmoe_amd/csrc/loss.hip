@@ -315,7 +315,8 @@ __device__ __forceinline__ void stats_epilogue(const LossArgs& a, const Acc& acc
       const float2 p = red[k][r];
       s += p.x == NEG_INF ? p.y : p.y * __expf(p.x - m);
     }
-    a.part[static_cast<size_t>(rt.row0 + r) * a.tiles + vt] = make_float2(m, s);
+    if (MOE_CHECK(rt.row0 + r < a.T && vt < a.tiles, 713))
+      a.part[static_cast<size_t>(rt.row0 + r) * a.tiles + vt] = make_float2(m, s);
   }
 #pragma unroll
   for (int i = 0; i < NSUB; ++i) {
@@ -375,14 +376,15 @@ __device__ __forceinline__ void grad_epilogue(const LossArgs& a, const Acc& acc,
           if (j == dense::NJ - 1 && l >> 6 == wn && (l >> 2 & 3) == lg)
             a.lab_lo[rt.row0 + row] = rounding_error(gl);
           if constexpr (PAIRS || NSUB == 2) {
-            if ((PAIRS || count <= LOSS_LO_ROWS) && row < rt.rows)
+            if ((PAIRS || count <= LOSS_LO_ROWS) && row < rt.rows &&
+                MOE_CHECK(count + rt.row0 + row < a.g_rows && vt * LT + col + 4 <= a.ldg, 714))
               *reinterpret_cast<uint2*>(a.g + static_cast<size_t>(count + rt.row0 + row) * a.ldg + vt * LT + col) =
                   dense::pack4(rounding_error(g[0]), rounding_error(g[1]), rounding_error(g[2]), rounding_error(g[3]));
           }
           return dense::pack4(g[0], g[1], g[2], g[3]);
         },
         [&](int row) -> uint16_t* {
-          return row < rt.rows ? a.g + static_cast<size_t>(rt.row0 + row) * a.ldg + vt * LT + 64 * wn : nullptr;
+          return row < rt.rows && MOE_CHECK(rt.row0 + row < a.g_rows && (vt + 1) * LT <= a.ldg, 715) ? a.g + static_cast<size_t>(rt.row0 + row) * a.ldg + vt * LT + 64 * wn : nullptr;
         });
   };
   if (ncol == LT)
@@ -499,6 +501,8 @@ __global__ __launch_bounds__(STHREADS) void loss_stream_kernel(LossArgs a) {
   const bool ok = lab >= 0 && lab < a.V;
   const unsigned long long valid = __ballot(ok);
   const int count = __popcll(valid), at = __popcll(valid & ((1ULL << lane) - 1));
+  if (!MOE_CHECK(a.T <= 16 * NT && count <= a.T && (GRAD ? (blockIdx.x + 1) * SV <= a.ldg : blockIdx.x < a.tiles), 716))
+    return;
   if (w == 0 && ok) {
     rows[at] = lane;
     labs[at] = lab;
@@ -575,6 +579,7 @@ __global__ __launch_bounds__(STHREADS) void loss_stream_kernel(LossArgs a) {
         lo[e] = rounding_error(g[e]);
         if (z == e) a.lab_lo[r] = lo[e];
       }
+      if (!MOE_CHECK(count + r < a.g_rows, 717)) continue;
       uint16_t* dst = a.g + static_cast<size_t>(r) * a.ldg + blockIdx.x * SV + c;
       *reinterpret_cast<uint2*>(dst) = dense::pack4(g[0], g[1], g[2], g[3]);
       *reinterpret_cast<uint2*>(dst + static_cast<size_t>(count) * a.ldg) = dense::pack4(lo[0], lo[1], lo[2], lo[3]);
@@ -709,6 +714,7 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_dh_kernel(LossArgs a) 
       for (int i = 0; i < NSUB; ++i) {
         const int row = 16 * (2 * i + wm) + (lane & 15);
         if (row >= rt.rows) continue;
+        if (!MOE_CHECK(static_cast<long long>(s) * padded_rows(count) + rt.row0 + row < a.acc_rows, 718)) continue;
         float* dst = a.acc + (static_cast<size_t>(s) * padded_rows(count) + rt.row0 + row) * a.d;
 #pragma unroll
         for (int j = 0; j < dense::NJ; ++j) {
@@ -727,7 +733,9 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_dh_kernel(LossArgs a) 
 __global__ __launch_bounds__(256) void loss_dh_out_kernel(LossArgs a) {
   const size_t t = blockIdx.x;
   const int r = a.pos[t], label = a.labels[t], rows = padded_rows(a.count[0]), splits = a.count[1];
-  if (!MOE_CHECK(r >= -1 && r < a.T && splits <= LOSS_SPLITS, 708)) return;
+  if (!MOE_CHECK(r >= -1 && r < a.T && splits <= LOSS_SPLITS &&
+                     (r < 0 || (splits - 1LL) * rows + r < a.acc_rows), 708))
+    return;
   const float scale = __int_as_float(a.count[2]), lo = r >= 0 && a.dh_fmt == FMT_BF16 ? a.lab_lo[r] : 0.f;
   const uint16_t* wl = a.w + static_cast<size_t>(r >= 0 ? label : 0) * a.d;
   for (int c = 4 * threadIdx.x; c < a.d; c += 1024) {

@@ -129,6 +129,8 @@ int moe_vocab_loss_backward(const moe_loss_shape* shape, const void* h, const vo
   a.g = at<uint16_t>(workspace, L.g);
   a.acc = at<float>(workspace, L.acc);
   a.ldg = L.piece;
+  a.g_rows = moe::loss_g_rows(s.T, moe::loss_pairs(fmt_of(s.dh_dtype), fmt_of(s.dw_dtype)));
+  a.acc_rows = moe::loss_acc_rows(s.T, s.d, L.piece);
   a.dh_fmt = fmt_of(s.dh_dtype);
   a.dw_fmt = fmt_of(s.dw_dtype);
   a.dh = dh;

@@ -138,13 +138,18 @@ def test_bf16_gradients_repeat_without_the_ignored():
     assert torch.equal(a[2], again[2]) and torch.equal(a[3], again[3])
 
 
-def test_bf16_gradients_debug_build():
-    say("case: debug build, vocab_loss with bf16 gradients")
-    args = _make(3, 700, 192, 20000, 0.3)
-    a = _run(*args, "bf16", "bf16")
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d,V,masked", [(700, 192, 20000, 0.3), (17, 128, 1000, 0.0), (33, 64, 700, 0.1), (48, 192, 300, 0.0),
+                                          (64, 64, 16384, 0.0), (64, 64, 17000, 0.0), (260, 64, 33100, 0.0)])
+def test_gradients_debug_build(T, d, V, masked, dtype):
+    """The bounds-checked build passes its checks and gives the same bits: either
+    way to the logits of few tokens, and tiles of every kind."""
+    say(f"case: debug build, vocab_loss with {dtype} gradients T={T} d={d} V={V}")
+    args = _make(3, T, d, V, masked)
+    a = _run(*args, dtype, dtype)
     prev = B.use_library(B.DEBUG_LIB_PATH)
     try:
-        b = _run(*args, "bf16", "bf16")
+        b = _run(*args, dtype, dtype)
     finally:
         B.restore_library(prev)
     for x, y in zip(a, b):
