@@ -133,17 +133,31 @@ struct LossArgs {
 };
 
 constexpr int LOSS_TILE = 256;    // rows and columns of a tile
-// The logits of few tokens (loss_stream_kernel, tiles of 64 entries) against
-// the tile pipeline, measured forward: 1 token, V = 32000, d = 2048: 34 / 47 us; 20,
-// 65536, 2048: 66 / 73; 40, 16000, 2048: 21 / 33; 40, 24000, 2048: 37 / 39; but
-// 64, 32000, 4096: 79 / 73 and 37, 50001, 7168: 192 / 140 (its blocks read the
-// hidden rows again for every 64 entries).  Forward and backward, the backward's
-// logits by either: 9 tokens, V = 453, d = 3328: 58 / 81 us; 48, 10000, 7168:
-// 195 / 223; 64, 2000, 7168: 153 / 180; 16, 32000, 2048: 135 / 144; 32, 65536, 1024:
-// 142 / 143.
+// The logits of few tokens (loss_stream_kernel, tiles of 64 entries) against the tile
+// pipeline, by T, d, V (us, forward; stream / tiles):
+//   up to 16 tokens   1, 2048, 32000: 26 / 36; 16, 512, 10007 with backward: 44 / 54;
+//                     16, 4096, 65536: 101 / 130; 16, 2048, 131072: 101 / 131; the tiles
+//                     win by 14% at most (16, 7168, 50001: 157 / 138; 16, 4096, 131072: 201 / 187)
+//   up to 32          two blocks fit a CU: one round of them (32768 entries) wins at any d
+//                     (32, 7168, 32000: 104 / 124; 20, 32768, 8192: 170 / 386); beyond it by
+//                     the last round and the hidden rows that every block reads again: 32, 4096,
+//                     65536: 115 / 131; 32, 2048, 131072: 115 / 132; 20, 2560, 100000: 117 / 122;
+//                     but 28, 5120, 40000: 109 / 103; 32, 7168, 57000: 191 / 151; 32, 4096, 131072:
+//                     221 / 187; 32, 4096, 50001: 109 / 105 and 32, 512, 500000: 142 / 130 are the
+//                     worst within the rule, 32, 7168, 81920: 244 / 266 outside it
+//   up to 64          one block to a CU, one round: 64, 1024, 16000: 18 / 23; 64, 7168, 2000: 57 / 79;
+//                     64, 32768, 16000: 258 / 411; but 40, 2048, 24000: 37 / 39; 64, 4096, 32000: 79 / 73;
+//                     37, 7168, 50001: 192 / 140
+// The backward's logits go the same way (16, 2048, 32000 with backward: 135 / 144; 32, 7168,
+// 50001: 718 / 635).  T counts the ignored tokens too: the host does not know the labels.
 constexpr int LOSS_STREAM_TILE = 64;
-inline bool loss_stream(int T, int V) { return T <= 32 || (T <= 64 && V <= 16384); }
-inline int loss_tiles(int T, int V) { return ceil_div(V, loss_stream(T, V) ? LOSS_STREAM_TILE : LOSS_TILE); }
+inline bool loss_stream(int T, int d, int V) {
+  if (T <= 16 || (T <= 64 && V <= 16384)) return true;
+  return T <= 32 && (V <= 32768 || (d <= 4096 && static_cast<long long>(V) * d <= 1LL << 28));
+}
+inline int loss_tiles(int T, int d, int V) {
+  return ceil_div(V, loss_stream(T, d, V) ? LOSS_STREAM_TILE : LOSS_TILE);
+}
 
 // A gradient in fp32 is summed from G held as pairs of bf16 values, what bf16
 // rounds off of G below it (2^-16 of an element is left, where one bf16 value

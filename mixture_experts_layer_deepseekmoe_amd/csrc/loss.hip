@@ -479,9 +479,10 @@ __global__ __launch_bounds__(dense::THREADS, 1) void loss_logits_kernel(LossArgs
 // Up to 64 tokens (scoring, decoding): the time is that of reading w once.  A
 // block takes 64 entries of the vocabulary; its 8 waves share K, pairs of
 // K-steps (the 128-byte lines of 64 rows) in turn, straight from memory into
-// MFMA fragments, and add their partial logits through LDS in order.  Several
-// such blocks fit a CU, with a pair of every wave in flight (8 KB); the tile
-// pipeline has one block to a CU and at most 64 KB of w in flight.  (Two pairs
+// MFMA fragments, and add their partial logits through LDS in order.  Of up to 16
+// tokens four such blocks fit a CU, of up to 32 two, else one (LDS), with a pair of
+// every wave in flight (8 KB); the tile pipeline has one block to a CU and at most 64
+// KB of w in flight, but its blocks share the hidden rows among 256 entries.  (Two pairs
 // in flight per wave cost a block its place on the CU: 20 tokens 66 -> 71 us.)
 //
 // GRAD: the piece's G by the same rule, with its rows' rounding errors below it
@@ -929,7 +930,7 @@ static void launch_stream(const LossArgs& a, int blocks, hipStream_t s) {
 }
 
 hipError_t launch_loss_forward(const LossArgs& a, hipStream_t s) {
-  if (loss_stream(a.T, a.V)) {
+  if (loss_stream(a.T, a.d, a.V)) {
     launch_stream<false>(a, a.tiles, s);
     hipLaunchKernelGGL(loss_finish_kernel<4>, dim3(a.T), dim3(256), 0, s, a);
     return hipGetLastError();
@@ -953,7 +954,7 @@ hipError_t launch_loss_piece(const LossArgs& a, hipStream_t s) {
   const long long nm = ceil_div(a.T, 64), nv = ceil_div(a.v_len, LT), nn = ceil_div(a.d, LT);
   const dim3 grid(loss_grid(nm, nv)), block(dense::THREADS);
   if (a.T > 0) {
-    if (loss_stream(a.T, a.V))
+    if (loss_stream(a.T, a.d, a.V))
       launch_stream<true>(a, static_cast<int>(nv) * (LT / SV), s);
     else if (loss_pairs(a.dh_fmt, a.dw_fmt))
       hipLaunchKernelGGL((loss_logits_kernel<true, true>), grid, block, 0, s, a);

@@ -32,7 +32,7 @@ struct Layout {
 
 Layout make_layout(const moe_loss_shape& s) {
   Layout L{};
-  const size_t T = static_cast<size_t>(s.T), nv = static_cast<size_t>(moe::loss_tiles(s.T, s.V));
+  const size_t T = static_cast<size_t>(s.T), nv = static_cast<size_t>(moe::loss_tiles(s.T, s.d, s.V));
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o += align_up(bytes); return at; };
   L.count = take(12);
@@ -101,7 +101,7 @@ int moe_vocab_loss(const moe_loss_shape* shape, const void* h, const void* w, co
   a.lse = lse;
   a.part = at<float2>(workspace, L.part);
   a.zlab = at<float>(workspace, L.zlab);
-  a.tiles = moe::loss_tiles(s.T, s.V);
+  a.tiles = moe::loss_tiles(s.T, s.d, s.V);
   a.v_len = s.V;
   return debug_status(check_launch(moe::launch_loss_forward(a, stream)), stream, "moe_vocab_loss");
 }
