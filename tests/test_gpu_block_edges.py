@@ -155,3 +155,61 @@ def test_debug_build(T, d, gate_rows, norm, ckpt):
         B.restore_library(prev)
     for p, q in zip(a, b):
         assert torch.equal(p, q)
+
+
+def _near(got, ref, size, tol=E):
+    got = _np(got)
+    assert got.shape == ref.shape and np.isfinite(got).all()
+    over = np.abs(got - ref) - (tol * size + 2.0 ** -24 * np.abs(ref) + 1e-30)
+    assert over.max(initial=-1.0) <= 0, float(over.max())
+
+
+@pytest.mark.parametrize("T,d,gate_rows,norm", [
+    (40, 256, None, True), (40, 256, None, False),    # no gate; neither
+    (160, 256, 1, True), (1100, 128, 1, True), (1100, 128, 2, False), (1100, 128, 3, True),    # whole gates
+    (33, 384, 5, True), (300, 128, 40, False), (8200, 128, 700, True), (700, 256, 30, True)])    # cut; up to 8, and more
+def test_backward_from_checkpoints(T, d, gate_rows, norm):
+    """Every gating, with and without a norm, from the 8-bit checkpoint."""
+    say(f"case: backward from checkpoints T={T} d={d} gate_rows={gate_rows} norm={norm}")
+    shape = moe.BlockShape(T, d, gate_rows=gate_rows or 0, eps=1e-5)
+    x, y, do = _rows(1, T, d, torch.bfloat16), _rows(2, T, d), _rows(3, T, d)
+    w = 1 + 0.2 * _rows(4, 1, d)[0] if norm else None
+    gate = 0.5 * _rows(5, shape.gates, d) if gate_rows else None
+    dv = lambda t: None if t is None else t.to(DEV)  # noqa: E731
+    save = moe.alloc_block_save(shape, e4m3=True)
+    moe.moe_block_out(shape, dv(x), dv(y), w=dv(w), gate=dv(gate), save=save)
+    dy, dw, dgate = moe.moe_block_out_backward(shape, dv(do), save, w=dv(w), gate=dv(gate))
+    codes, scales, v = A.checkpoint(y.numpy())
+    assert (save.codes.cpu().numpy() == codes).all() and (save.scales.cpu().numpy() == scales).all()
+    r = A.rstd(_np(y), 1e-5)
+    opt = lambda t: None if t is None else _np(t)  # noqa: E731
+    ry, rw, rg, sy, sw, sg = A.block_out_backward(_np(do), v, opt(w), opt(gate), gate_rows or 0, r)
+    _near(dy, ry, sy)
+    if norm:
+        _near(dw, rw, sw)
+    if gate is not None:
+        _near(dgate, rg, sg)
+    assert (dw is None) == (w is None) and (dgate is None) == (gate is None)
+
+
+def test_more_than_32768_gates():
+    """32769 gates of 17 rows and one of 5, two runs of rows each: their sums take
+    two launches.  dw joins 32770 partial sums: at most 16 rows, 2 runs, 513 + 18
+    partial sums and the products on a path, 566 x 2^-24 = 3.4e-5 of the terms."""
+    say("case: block_out backward, 32770 gates")
+    T, d, L = 32769 * 17 + 5, 8, 17
+    shape = moe.BlockShape(T, d, x_dtype="f32", gate_rows=L, eps=1e-5)
+    x, y, do = (_rows(k, T, d) for k in (1, 2, 3))
+    w, gate = 1 + 0.2 * _rows(4, 1, d)[0], 0.5 * _rows(5, shape.gates, d)
+    assert shape.gates == 32770
+    save = moe.alloc_block_save(shape)
+    dev = [t.to(DEV) for t in (x, y, do, w, gate)]
+    xo, _ = moe.moe_block_out(shape, dev[0], dev[1], w=dev[3], gate=dev[4], save=save)
+    dy, dw, dgate = moe.moe_block_out_backward(shape, dev[2], save, w=dev[3], gate=dev[4], y=dev[1])
+    ref, zn = A.block_out(_np(x), _np(y), None, _np(w), _np(gate), L, 1e-5, 1.0)
+    _near(xo, ref, np.abs(_np(x)) + np.abs(ref - _np(x)))
+    r = A.rstd(_np(y), 1e-5)
+    ry, rw, rg, sy, sw, sg = A.block_out_backward(_np(do), _np(y), _np(w), _np(gate), L, r)
+    _near(dy, ry, sy)
+    _near(dgate, rg, sg)
+    _near(dw, rw, sw, 5e-5)

@@ -209,3 +209,25 @@ def test_all_of_a_large_vocabulary():
         assert ((dw[v].double() - ref).abs() <= tol).all()
     del w, dw
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T,d,V", [(9, 128, 300), (40, 64, 20000), (300, 192, 2000)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_hidden_rows_that_are_not_finite(T, d, V, dtype):
+    """A NaN or an infinity in a labelled hidden row: its loss, lse and dh are NaN,
+    and by the formula all of dw; every other token's results keep their bits."""
+    say(f"case: vocab_loss, hidden rows not finite T={T} d={d} V={V} {dtype}")
+    h, w, labels, dloss, dlse = _make(6, T, d, V)
+    clean = _run(h, w, labels, dloss, dlse, dtype, dtype)
+    h[3, 5], h[7, 0] = float("nan"), -float("inf")
+    got = _run(h, w, labels, dloss, dlse, dtype, dtype)
+    bad = torch.zeros(T, dtype=torch.bool, device=DEV)
+    bad[[3, 7]] = True
+    for a, b in zip(got[:3], clean[:3]):
+        assert torch.equal(a[~bad], b[~bad]) and torch.isfinite(a[~bad]).all()
+        assert torch.isnan(a[bad]).all()
+    assert torch.isnan(got[3]).all()
+    # ignored, the same rows matter to nobody
+    labels[[3, 7]] = -100
+    got = _run(h, w, labels, dloss, dlse, dtype, dtype)
+    assert all(torch.isfinite(t).all() for t in got) and (got[2][bad] == 0).all()
