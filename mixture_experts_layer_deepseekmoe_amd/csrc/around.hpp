@@ -68,10 +68,11 @@ struct BlockBwdArgs {
 };
 
 // A backward block takes `rows` rows and leaves one row of partial column sums
-// (d floats): 512 blocks (two to a CU) for short batches, and at most 16 rows,
-// which keep the partial sums' traffic below a tenth of the rows' own.  Measured:
-// 517 x 1992 with 16 rows to a block 27 us, with 2 rows 7; 8192 x 7168 with 8 rows
-// to a block 3% slower than with 16.
+// (d floats, written and read again: 8 bytes a column beside the 9 to 20 of each of its
+// rows).  Long batches take 16 rows to a block, where that is 3 to 6% of the rows'
+// traffic; short ones trade it for parallelism, down to one row to a block (as much
+// as 90%): 512 blocks, two to a CU.  Measured: 517 x 1992 with 16 rows to a block 27 us,
+// with 2 rows 7; 8192 x 7168 with 8 rows to a block 3% slower than with 16.
 struct BlockBwdPlan {
   int rows;
   int whole_gates;        // gates of at most `rows` rows, whole ones to a block

@@ -16,7 +16,10 @@
 //
 // All of it is bound by HBM: each value is loaded once into registers, where
 // its row stays between the row's sum and its use, and each result is stored
-// once.  Measured at 8192 x 7168 (a 1 GiB copy runs at 5.1 TB/s): block_in with
+// once.  (But for the backward above 8192 columns: its values, gate w and sums of
+// 32 columns to a thread do not fit the 128 registers that 1024 threads leave it,
+// and about 1 KB a thread goes through scratch for each row.  2048 rows of 8192
+// columns: 46 us; of 8200: 303, of 16384: 408.)  Measured at 8192 x 7168 (a 1 GiB copy runs at 5.1 TB/s): block_in with
 // a checkpoint 56 us (5.2 TB/s), block_out with one and the next norm 156 us (4.9
 // TB/s), their backward 214 us (4.7) and 110 us (4.9).  A block takes whole rows, 8 consecutive columns to a thread (16-byte
 // loads of bf16, 16 lanes to a 128-column tile).  Statistics and sums are fp32
@@ -101,7 +104,10 @@ __device__ __forceinline__ float rstd_of(float sumsq, int d, float eps) {
 }
 
 // The 1x128 tile that holds this thread's eight values (16 lanes to a tile):
-// scale amax / 448, codes of v * (448 * (1 / amax)).  A tile below 2^-119, where
+// scale amax / 448, codes of v * (448 * (1 / amax)): the factor as 32-bit torch
+// forms 448 / amax, rounded twice (the layer's own quantisers divide once: codes
+// may differ by one there where v falls between two; either way scale * code is
+// within the format's half step).  A tile below 2^-119, where
 // that factor would overflow, counts as all zero: scale 1, zero codes.  amax is
 // taken over the bits, where NaN stands above infinity and infinity above the
 // rest (fmaxf would drop a NaN): such a tile has the scale NaN or infinity, and
@@ -454,8 +460,12 @@ __global__ __launch_bounds__(1024) void block_colsum_kernel(ColSumArgs a) {
 
 // f.template operator()<NV, TPB>() with TPB threads x NV vectors of 8 columns
 // for rows of d columns.  Few rows (up to 512, two to a CU) are spread over
-// as many threads as they fill: a call's time is then its chain of loads (1 row
-// of 7168 columns: 5.4 us with 256 threads, 3.8 with 1024; 256 rows: 9.9, 7.7).
+// as many threads as they fill: a call's time is then its chain of loads.  The
+// kernel's time with 1024 threads and with 256, block_out with the next norm / block_in, us:
+//   7168 columns    16 rows 4.5, 6.0 / 3.0, 3.6     256 rows 5.7, 6.9 / 3.6, 3.9
+//                  512 rows 8.5, 8.9 / 4.6, 4.5     768 rows 13.1, 12.0 / 6.2, 5.3
+//   4096 columns   256 rows 4.6, 5.0 / 3.2, 3.3     512 rows 6.1, 6.0 / 4.0, 3.6
+//                 1024 rows 10.6, 8.9 / 5.9, 4.4
 template <class F>
 hipError_t with_row_shape(int T, int d, F&& f) {
   if (d <= 2048) f.template operator()<1, 256>();

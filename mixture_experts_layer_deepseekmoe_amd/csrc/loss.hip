@@ -27,8 +27,8 @@
 // is the operand of the two products that follow, in bf16.  For a gradient in fp32
 // it is a pair of bf16 values, what the first rounds off in the second (2^-16 of
 // an element is left): the product runs once for each, the second's sums added
-// to the first's (4096 tokens, a quarter ignored, d = 7168, V = 65536, both gradients: 15.4
-// ms against 9.3 in bf16; d = 2048, none ignored: 6.0 against 3.7).
+// to the first's (4096 tokens, a quarter ignored, d = 7168, V = 65536, both gradients: 14.6
+// ms against 8.85 in bf16; d = 2048, none ignored: 5.6 against 3.5).
 // For a gradient in bf16, G is rounded to bf16 once (at most 2^-8 of an element), an
 // error of the size of the output's own rounding.  The label's element outweighs
 // the rest of its row, so its rounding is most of that error and, with few rows,
@@ -111,7 +111,10 @@ __device__ __forceinline__ int padded_rows(int count) { return (count + LT - 1) 
 // Cost of s splits of dh's sum for nm x nn tiles: rounds of 256 tiles at about
 // 0.75 us per 32-column step, and the splits' fp32 tiles written and read at
 // about 4 TB/s.  The least cost (the fewest splits of equal ones) is taken; the
-// limits are those of loss_acc_rows.
+// limits are those of loss_acc_rows.  A step's time is that of 256 rows, and taken for
+// fewer as well: with 0.3 us instead, forward + backward of 256 x 8000 x 1024 takes 87
+// us instead of 82, of 207 x 10007 x 512 75 instead of 71; with 1.5 us 82 and 72, of 128
+// x 16000 x 2048 115 instead of 118.
 __device__ __forceinline__ float split_cost(int s, int nm, int nn, int piece) {
   const int tiles = nm * nn;   // below 2^17
   if (s > 1 && (s * LT > piece || s * tiles > LOSS_SPLIT_TILES)) return 1e30f;
@@ -120,7 +123,11 @@ __device__ __forceinline__ float split_cost(int s, int nm, int nn, int piece) {
 }
 
 // dh's row tiles: fine ones would read w's piece again for every 64 rows, which
-// pays only where a piece is short.
+// pays only where a piece is short.  Forward + backward with fine and with 256-row
+// tiles, us: 207 x 10007 x 512 71, 78; 256 x 8000 x 1024 82, 91; 256 x 16000 x 1024 90, 98;
+// 256 x 16000 x 4096 240, 239; beyond: 256 x 20000 x 4096 271, 265; 256 x 32000 x 4096 397,
+// 373; 512 x 24000 x 2048 260, 251 (but 256 x 32000 x 1024 119, 125; and within,
+// 128 x 8000 x 7168 282, 274).
 __device__ __forceinline__ RowCut dh_cut(int count, int d, int piece) {
   return RowCut(count, piece <= 16384 ? min(4 * ceil_div(d, LT), NBLOCKS) : NBLOCKS);
 }
