@@ -567,7 +567,9 @@ def moe_block_out_backward(shape: BlockShape, do: torch.Tensor, save: Optional[B
 @dataclass
 class LossShape:
     """Cross entropy of T hidden rows of d columns over V entries
-    (moe_loss_shape); dh_dtype and dw_dtype: "f32" or "bf16"."""
+    (moe_loss_shape).  dh_dtype and dw_dtype: "f32", from the gradient of the
+    logits to 16 bits, or "bf16", from its bf16 rounding (about 1.6 times as fast
+    for both)."""
     T: int
     d: int
     V: int

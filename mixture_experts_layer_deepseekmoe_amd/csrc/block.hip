@@ -19,12 +19,12 @@
 // once.  (But for the backward above 8192 columns: its values, gate w and sums of
 // 32 columns to a thread do not fit the 128 registers that 1024 threads leave it,
 // and about 1 KB a thread goes through scratch for each row.  2048 rows of 8192
-// columns: 46 us; of 8200: 303, of 16384: 408.)  Measured at 8192 x 7168 (a 1 GiB copy runs at 5.1 TB/s): block_in with
-// a checkpoint 56 us (5.2 TB/s), block_out with one and the next norm 156 us (4.9
-// TB/s), their backward 214 us (4.7) and 110 us (4.9).  A block takes whole rows, 8 consecutive columns to a thread (16-byte
+// columns: 46 us; of 8200: 303, of 16384: 408.)  Measured at 8192 x 7168 (a 1 GiB
+// copy runs at 5.1 TB/s): block_in with a checkpoint 56 us (5.2 TB/s), block_out
+// with one and the next norm 156 us (4.9 TB/s), their backward 214 us (4.7) and 110
+// us (4.9).  A block takes whole rows, 8 consecutive columns to a thread (16-byte
 // loads of bf16, 16 lanes to a 128-column tile).  Statistics and sums are fp32
-// throughout, in a fixed order; outputs in bf16 are rounded once, at the
-// store.
+// throughout, in a fixed order; outputs in bf16 are rounded once, at the store.
 #include "around.hpp"
 
 namespace moe {

@@ -18,8 +18,8 @@
 //
 // The large products are bound by the matrix cores at the clock the card's power
 // holds (1.75-1.95 GHz; 76% of the cycles in the logits' kernel are MFMAs).
-// 4096 tokens, a quarter ignored, d = 7168, V = 65536 (2.89 TFLOP each): logits 2.05 ms (1.41
-// PFLOP/s; with the G epilogue 2.1), dh 2.2-2.3 ms (1.25-1.3), dw 2.4 ms (1.2).
+// 4096 tokens, a quarter ignored, d = 7168, V = 65536 (2.89 TFLOP each): logits 2.05
+// ms (1.41 PFLOP/s; with the G epilogue 2.1), dh 2.25-2.4 ms (1.2-1.3), dw 2.5 (1.15).
 // Library products of the same with 4096 rows: 1.23-1.26, 0.92-0.94, 0.92-1.06 on
 // operands laid out as these are.  Few tokens are bound by reading w once.
 //
@@ -40,12 +40,12 @@
 //   both G is held over the mantissa of the largest dloss: with the equal
 //        weights of a mean the label's elements are p - 1, near a power of two,
 //        and not all off by the one rounding of the weight.
-// Against 64 bits, with bf16 outputs: 1.7e-3 normwise, the outputs' own rounding
-// (2.4e-3 without these, up to 2.9e-3 for few rows; 2.2e-3 of dw without its labels'
-// steps).  They cost 4 us of 71 (207 rows, 10007 entries, d = 512) and 1% of the large
-// products.  The labels' steps: a pair to a tile for 4096 tokens, a quarter ignored,
-// 65536 entries, 0.3% (8.80 / 8.77 ms for d = 7168); 16 pairs beside a tile's own 64 for 4096 rows of 1000 entries, 199 /
-// 149 us (d = 256).
+// Against 64 bits, normwise: 2e-6 in fp32; 1.65e-3 in bf16, the outputs' own
+// rounding (2.4e-3 without these, up to 2.9e-3 for few rows; 2.2e-3 of dw without its
+// labels' steps).  They cost 4 us of 71 (207 rows, 10007 entries, d = 512) and 1% of the
+// large products.  The labels' steps: a pair to a tile for 4096 tokens, a quarter
+// ignored, 65536 entries, 0.3% (8.80 / 8.77 ms for d = 7168); 16 pairs beside a tile's
+// own 64 for 4096 rows of 1000 entries, 199 / 149 us (d = 256).
 #include "around.hpp"
 #include "dense_core.hpp"
 

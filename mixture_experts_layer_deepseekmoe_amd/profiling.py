@@ -6,8 +6,9 @@
     python -m mixture_experts_layer_deepseekmoe_amd.profiling peaks
     # the vendor library (hipBLASLt through torch) on GEMMs of the same sizes -> profiles/library_reference.json:
     python -m mixture_experts_layer_deepseekmoe_amd.profiling library --workload bf16_d7168
-    # the operators around the layer (cases of perf/operators.py, by name; default: all of them):
-    python -m mixture_experts_layer_deepseekmoe_amd.profiling operators --case loss_train_d7168 --steps 3
+    # the operators around the layer (cases of perf/operators.py, by name, and training passes of the loss of any
+    # size and gradient type; default: all the cases):
+    python -m mixture_experts_layer_deepseekmoe_amd.profiling operators --case loss_train_d7168 --loss 48,7168,10000,f32 --steps 3
     # turn rocprofv3's CSV output into the summaries kept under profiles/:
     python -m mixture_experts_layer_deepseekmoe_amd.profiling summarize --trace DIR --pmc DIR [DIR...] \
         --workload bf16_d7168 --out profiles
@@ -75,11 +76,14 @@ def _run(args):
 
 
 def _operators(args):
-    """Runs cases of perf/operators.py with the framework's calls, on three sets of inputs in turn."""
+    """Runs cases of perf/operators.py with the framework's calls, and losses of other sizes, on three sets of inputs
+    in turn."""
     sys.path.insert(0, ROOT)
     import importlib.util
 
     import torch
+
+    import mixture_experts_layer_deepseekmoe_amd as moe
 
     spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
     ops = importlib.util.module_from_spec(spec)
@@ -90,13 +94,25 @@ def _operators(args):
         torch.mul(src, 2.0, out=torch.empty_like(src))
         del src
     for case in ops.listed():
-        if args.case and case["name"] not in args.case:
+        if (args.case or args.loss) and case["name"] not in (args.case or ()):
             continue
         states = [ops.prepare(case, 1 + k) for k in range(3)]
         for k in range(args.steps):
             ops.run(states[k % 3])
         torch.cuda.synchronize()
         print(f"{case['name']}: {args.steps} passes", flush=True)
+    for size in args.loss or ():
+        T, d, V = (int(v) for v in size.split(",")[:3])
+        dtype = size.split(",")[3]
+        case = dict(op="vocab_loss", T=T, d=d, V=V, masked=0.0, train=True)
+        states = [ops.prepare(case, 1 + k) for k in range(3)]
+        shape = moe.LossShape(T, d, V, dh_dtype=dtype, dw_dtype=dtype)
+        for k in range(args.steps):
+            q = states[k % 3]
+            _, lse = moe.moe_vocab_loss(shape, q["h"], q["w"], q["labels"])
+            moe.moe_vocab_loss_backward(shape, q["h"], q["w"], q["labels"], lse, q["dloss"])
+        torch.cuda.synchronize()
+        print(f"loss {size}: {args.steps} passes", flush=True)
 
 
 def _short(name: str) -> str:
@@ -326,6 +342,7 @@ def main():
     r.add_argument("--train", action="store_true", help="training steps (moe_forward_train + moe_backward)")
     o = sub.add_parser("operators")
     o.add_argument("--case", nargs="*")
+    o.add_argument("--loss", nargs="*", metavar="T,d,V,DTYPE")
     o.add_argument("--steps", type=int, default=3)
     o.add_argument("--calibrate", action="store_true")
     s = sub.add_parser("summarize")
