@@ -265,6 +265,27 @@ int moe_forward_static(const moe_shape* shape, const void* u, const void* centro
                        hipStream_t stream);
 
 /*
+ * moe_forward for up to MOE_FEW_TOKENS tokens (single tokens, a decode batch, the
+ * drafted tokens of a request): the same layer, arguments and routing, in three
+ * launches (E4M3: four), each chosen expert's weights read once.  All dtype
+ * combinations, shared experts and group-limited routing as moe_forward has
+ * them.  The expert outputs are not rounded between the kernels (BF16 weights:
+ * H enters the down product as a pair of bf16 values), so y may differ from
+ * moe_forward's by the roundings that it makes: 2^-9 of H and of Y (E4M3: of Y).
+ * A token's y is the same whatever other tokens stand in the batch, but for
+ * the order in which its logits and its experts' sums are formed.
+ * MOE_STAGE_ROUTE, MOE_STAGE_GATE_UP (with the selection), MOE_STAGE_QUANT (E4M3:
+ * of h; u is quantised by the first launch) and MOE_STAGE_DOWN (with gates and
+ * residual) are traced.
+ * Limits beside the layer's: T at most MOE_FEW_TOKENS, d and inter at most 32768.
+ */
+#define MOE_FEW_TOKENS 64
+int moe_few_workspace_size(const moe_shape* shape, size_t* bytes);
+int moe_forward_few(const moe_shape* shape, const void* u, const void* centroids, const float* bias,
+                    const moe_weights* weights, void* y, const moe_routing* routing, void* workspace,
+                    size_t workspace_bytes, const moe_trace* trace, hipStream_t stream);
+
+/*
  * Training: the layer backward (x_dtype = BF16 with w_dtype = BF16 or E4M3;
  * other dtypes return MOE_ERR_UNSUPPORTED).  The report's FP8 training
  * section (as paraphrased on why-be.co.kr, its Figure 6 passage) runs the
@@ -437,6 +458,60 @@ int moe_vocab_loss(const moe_loss_shape* shape, const void* h, const void* w, co
 int moe_vocab_loss_backward(const moe_loss_shape* shape, const void* h, const void* w, const int32_t* labels,
                             const float* lse, const float* dloss, const float* dlse, void* dh, void* dw,
                             void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The embedding, where the residual stream begins:
+ *   x_t = scale table[token_t]        rows [T][d] from table [V][d]
+ *   with w_next: n_next = moe_block_in of x as stored, under w_next -- the first
+ *   block's n in the same pass (save_next: as moe_block_in's save)
+ * A token outside [0, V) (-1, say: padding) is a row of zeros; its n_next is zero.
+ *
+ * moe_embed_backward: for dx [T][d] fp32 (moe_block_in_backward's),
+ *   dtable_v = scale sum_{t: token_t = v} dx_t      [V][d] in grad_dtype
+ * accumulate 0: overwritten, rows of no token with zeros.  Not 0: added to, and
+ * rows of no token are left as they are (a table that is also the vocabulary
+ * matrix: moe_vocab_loss_backward's dw first).  Tokens outside [0, V) add nothing,
+ * and their rows of dx are not read.  Sums are fp32, in a fixed order
+ * (bit-reproducible); a bf16 dtable is rounded once.
+ *
+ * table_dtype, x_dtype, n_dtype, grad_dtype: F32 or BF16.  Limits: d a multiple of
+ * 8, at most 32768; T below 2^22; V at most 2^24.
+ */
+typedef struct {
+  int32_t T, d, V;
+  int32_t table_dtype, x_dtype, n_dtype, grad_dtype;
+  float scale, eps;
+} moe_embed_shape;
+int moe_embed(const moe_embed_shape* shape, const int32_t* tokens, const void* table, const float* w_next, void* x,
+              void* n_next, const moe_block_save* save_next, hipStream_t stream);
+int moe_embed_workspace_size(const moe_embed_shape* shape, size_t* bytes);
+int moe_embed_backward(const moe_embed_shape* shape, const int32_t* tokens, const float* dx, void* dtable,
+                       int32_t accumulate, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The gradients of a step, together, whatever tensors they lie in:
+ *   moe_grad_sumsq   sumsq = the sum of all elements' squares (64 bits, a fixed
+ *                    order).  Sums of several calls, or ranks, add up.
+ *   moe_grad_clip    norm = sqrt(sumsq) (nullable; fp32, infinite above its range),
+ *                    and every element times min(1, max_norm / norm): in place (out
+ *                    null), or to out[i] for tensors[i], which may differ in dtype.
+ *                    A sumsq that is NaN or infinite clips nothing: the caller
+ *                    sees it in `norm`.
+ * moe_tensor: `numel` consecutive elements, F32 or BF16, at any address of an
+ * element (16-byte alignment is not needed here); numel may be 0.  The structs
+ * are host memory, read before the call returns.  No two tensors may share memory, but out[i] may be tensors[i].
+ * max_norm > 0 (infinity: never clips).
+ */
+typedef struct {
+  void* data;
+  int64_t numel;
+  int32_t dtype;
+} moe_tensor;
+int moe_grad_workspace_size(int32_t n, size_t* bytes);
+int moe_grad_sumsq(const moe_tensor* tensors, int32_t n, double* sumsq, void* workspace, size_t workspace_bytes,
+                   hipStream_t stream);
+int moe_grad_clip(const moe_tensor* tensors, const moe_tensor* out, int32_t n, const double* sumsq, double max_norm,
+                  float* norm, hipStream_t stream);
 
 /*
  * Aux-loss-free bias update (xyznot summary, section 2: b_i is lowered by

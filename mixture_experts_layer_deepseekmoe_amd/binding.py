@@ -31,9 +31,12 @@ EXPORTED = ("moe_status_str", "moe_version", "moe_workspace_size", "moe_workspac
             "moe_forward", "moe_forward_static", "moe_train_workspace_size", "moe_forward_train", "moe_backward",
             "moe_update_bias", "moe_quantize_weight_e4m3", "moe_quantize_act_e4m3",
             "moe_block_in", "moe_block_out", "moe_block_workspace_size", "moe_block_in_backward",
-            "moe_block_out_backward", "moe_vocab_loss_workspace_size", "moe_vocab_loss", "moe_vocab_loss_backward")
+            "moe_block_out_backward", "moe_vocab_loss_workspace_size", "moe_vocab_loss", "moe_vocab_loss_backward",
+            "moe_few_workspace_size", "moe_forward_few", "moe_embed", "moe_embed_workspace_size", "moe_embed_backward",
+            "moe_grad_workspace_size", "moe_grad_sumsq", "moe_grad_clip")
 
 STATIC_SCRATCH_BYTES = 64 << 20   # MOE_STATIC_SCRATCH_BYTES
+FEW_TOKENS = 64                   # MOE_FEW_TOKENS
 
 
 class MoEError(RuntimeError):
@@ -89,6 +92,15 @@ class CBlockShape(ctypes.Structure):
 
 class CLossShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "d", "V", "dh_dtype", "dw_dtype")]
+
+
+class CEmbedShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "d", "V", "table_dtype", "x_dtype", "n_dtype", "grad_dtype")] + \
+               [(n, ctypes.c_float) for n in ("scale", "eps")]
+
+
+class CTensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32)]
 
 
 class CBlockSave(ctypes.Structure):
@@ -176,6 +188,23 @@ def _open(path: str) -> ctypes.CDLL:
     lib.moe_vocab_loss.argtypes = [ls, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.moe_vocab_loss_backward.restype = ctypes.c_int
     lib.moe_vocab_loss_backward.argtypes = [ls, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_few_workspace_size.restype = ctypes.c_int
+    lib.moe_few_workspace_size.argtypes = [ctypes.POINTER(Shape), szp]
+    lib.moe_forward_few.restype = ctypes.c_int
+    lib.moe_forward_few.argtypes = lib.moe_forward.argtypes
+    es, tn = ctypes.POINTER(CEmbedShape), ctypes.c_void_p   # tensors: a ctypes array of CTensor or its address
+    lib.moe_embed.restype = ctypes.c_int
+    lib.moe_embed.argtypes = [es, vp, vp, vp, vp, vp, bk, vp]
+    lib.moe_embed_workspace_size.restype = ctypes.c_int
+    lib.moe_embed_workspace_size.argtypes = [es, szp]
+    lib.moe_embed_backward.restype = ctypes.c_int
+    lib.moe_embed_backward.argtypes = [es, vp, vp, vp, i32, vp, sz, vp]
+    lib.moe_grad_workspace_size.restype = ctypes.c_int
+    lib.moe_grad_workspace_size.argtypes = [i32, szp]
+    lib.moe_grad_sumsq.restype = ctypes.c_int
+    lib.moe_grad_sumsq.argtypes = [tn, i32, vp, vp, sz, vp]
+    lib.moe_grad_clip.restype = ctypes.c_int
+    lib.moe_grad_clip.argtypes = [tn, tn, i32, vp, ctypes.c_double, vp, vp]
     return lib
 
 
@@ -343,6 +372,50 @@ def moe_forward_static(shape: LayerShape, u: torch.Tensor, centroids: torch.Tens
     return y
 
 
+def few_workspace_size(shape: LayerShape) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_few_workspace_size(ctypes.byref(shape.c()), ctypes.byref(n)), "moe_few_workspace_size")
+    return n.value
+
+
+def alloc_few_workspace(shape: LayerShape, device="cuda") -> torch.Tensor:
+    return torch.empty(max(few_workspace_size(shape), 1), dtype=torch.uint8, device=device)
+
+
+def _few_weights(shape: LayerShape, w: ExpertWeights) -> Weights:
+    N, S, d, I2, I = shape.n_routed, shape.n_shared, shape.d, 2 * shape.inter, shape.inter
+    wd = "u8" if shape.w_dtype == "e4m3" else shape.w_dtype
+    b = [_arg(w.w_gate_up, "w_gate_up", wd, N, I2, d), _arg(w.w_down, "w_down", wd, N, d, I)]
+    b += [_arg(w.ws_gate_up, "ws_gate_up", wd, S, I2, d), _arg(w.ws_down, "ws_down", wd, S, d, I)] if S else [None, None]
+    if wd == "u8":
+        b += [_arg(w.s_gate_up, "s_gate_up", "f32", N, I2 // 128, d // 128), _arg(w.s_down, "s_down", "f32", N, d // 128, I // 128)]
+        if S:
+            b += [_arg(w.ss_gate_up, "ss_gate_up", "f32", S, I2 // 128, d // 128),
+                  _arg(w.ss_down, "ss_down", "f32", S, d // 128, I // 128)]
+    return Weights(*b)
+
+
+def moe_forward_few(shape: LayerShape, u: torch.Tensor, centroids: torch.Tensor, bias: torch.Tensor,
+                    weights: ExpertWeights, y: Optional[torch.Tensor] = None,
+                    routing: Optional[Dict[str, torch.Tensor]] = None, workspace: Optional[torch.Tensor] = None,
+                    trace: Optional[Trace] = None) -> torch.Tensor:
+    """moe_forward for up to FEW_TOKENS tokens, in three launches (e4m3: four): the
+    weights of each chosen expert are read once, and its outputs are not rounded
+    between the kernels.  The workspace is few_workspace_size(shape) bytes."""
+    T, d, N, x = shape.T, shape.d, shape.n_routed, shape.x_dtype
+    if y is None:
+        y = torch.empty((T, d), dtype=_TORCH_DT[DTYPE_CODE[shape.out_dtype]], device=u.device)
+    ws = alloc_few_workspace(shape, u.device) if workspace is None else workspace
+    _same_device(u, centroids, bias, weights.w_gate_up, weights.w_down, weights.ws_gate_up, weights.ws_down, y, ws)
+    rs = _routing_struct(routing)
+    rc = load_library().moe_forward_few(
+        ctypes.byref(shape.c()), _arg(u, "u", x, T, d), _arg(centroids, "centroids", x, N, d), _arg(bias, "bias", "f32", N),
+        ctypes.byref(_few_weights(shape, weights)), _arg(y, "y", shape.out_dtype, T, d), _ref(rs), _ptr(ws), ws.numel(),
+        _ref(trace), _stream())
+    _check(rc, "moe_forward_few")
+    return y
+
+
 def train_workspace_size(shape: LayerShape) -> int:
     n = ctypes.c_size_t(0)
     _check(load_library().moe_train_workspace_size(ctypes.byref(shape.c()), ctypes.byref(n)),
@@ -467,7 +540,20 @@ def _arg(t: Optional[torch.Tensor], name: str, dtype: str, *size: int) -> Option
     return _ptr(t)
 
 
-_ARG_DT = {"f32": torch.float32, "bf16": torch.bfloat16, "u8": torch.uint8, "i32": torch.int32}
+def _same_device(*tensors: Optional[torch.Tensor]) -> None:
+    """The library launches on the current device: its tensors have to live there."""
+    here = None
+    for t in tensors:
+        if t is None or not t.is_cuda:
+            continue
+        if here is None:
+            here = torch._C._cuda_getDevice()
+        if t.get_device() != here:
+            raise ValueError(f"a tensor lives on cuda:{t.get_device()}, and cuda:{here} is the current device")
+
+
+_ARG_DT = {"f32": torch.float32, "bf16": torch.bfloat16, "u8": torch.uint8, "i32": torch.int32,
+           "f64": torch.float64}
 
 
 def _save_struct(shape: BlockShape, save: Optional[BlockSave]) -> Optional[CBlockSave]:
@@ -628,6 +714,137 @@ def moe_vocab_loss_backward(shape: LossShape, h: torch.Tensor, w: torch.Tensor, 
         _ptr(ws), ws.numel(), _stream())
     _check(rc, "moe_vocab_loss_backward")
     return dh, dw
+
+
+# ---------------------------------------------------------------- a model's two ends
+
+
+@dataclass
+class EmbedShape:
+    """The embedding of T tokens from a table of V rows of d columns
+    (moe_embed_shape): x = scale table[token], in x_dtype; n_next in n_dtype; the
+    table's gradient in grad_dtype."""
+    T: int
+    d: int
+    V: int
+    table_dtype: str = "f32"
+    x_dtype: str = "f32"
+    n_dtype: str = "bf16"
+    grad_dtype: str = "f32"
+    scale: float = 1.0
+    eps: float = 1e-6
+
+    def c(self) -> CEmbedShape:
+        return CEmbedShape(self.T, self.d, self.V, DTYPE_CODE[self.table_dtype], DTYPE_CODE[self.x_dtype],
+                           DTYPE_CODE[self.n_dtype], DTYPE_CODE[self.grad_dtype], self.scale, self.eps)
+
+
+def embed_workspace_size(shape: EmbedShape) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_embed_workspace_size(ctypes.byref(shape.c()), ctypes.byref(n)),
+           "moe_embed_workspace_size")
+    return n.value
+
+
+def moe_embed(shape: EmbedShape, tokens: torch.Tensor, table: torch.Tensor, w_next: Optional[torch.Tensor] = None,
+              save_next: Optional[BlockSave] = None, x: Optional[torch.Tensor] = None,
+              n_next: Optional[torch.Tensor] = None):
+    """The rows of int32 ``tokens`` (outside [0, V): zeros), and with ``w_next`` the
+    first block's n_next = norm(x; w_next).  ``save_next`` receives what
+    moe_block_in_backward needs.  Returns (x, n_next or None)."""
+    T, d, V = shape.T, shape.d, shape.V
+    if x is None:
+        x = torch.empty((T, d), dtype=_ARG_DT[shape.x_dtype], device=tokens.device)
+    if n_next is None and w_next is not None:
+        n_next = torch.empty((T, d), dtype=_ARG_DT[shape.n_dtype], device=tokens.device)
+    _same_device(tokens, table, w_next, x, n_next)
+    rc = load_library().moe_embed(
+        ctypes.byref(shape.c()), _arg(tokens, "tokens", "i32", T), _arg(table, "table", shape.table_dtype, V, d),
+        _arg(w_next, "w_next", "f32", d), _arg(x, "x", shape.x_dtype, T, d), _arg(n_next, "n_next", shape.n_dtype, T, d),
+        _ref(_save_struct(shape, save_next)), _stream())
+    _check(rc, "moe_embed")
+    return x, n_next
+
+
+def moe_embed_backward(shape: EmbedShape, tokens: torch.Tensor, dx: torch.Tensor, dtable: Optional[torch.Tensor] = None,
+                       accumulate: bool = False, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The table's gradient [V, d] for the fp32 gradient ``dx`` of x: overwritten, or
+    with ``accumulate`` added to ``dtable`` (rows of no token stay as they are)."""
+    T, d, V = shape.T, shape.d, shape.V
+    if dtable is None:
+        if accumulate:
+            raise ValueError("accumulate: there is no dtable to add to")
+        dtable = torch.empty((V, d), dtype=_ARG_DT[shape.grad_dtype], device=tokens.device)
+    ws = workspace
+    if ws is None:
+        ws = torch.empty(max(embed_workspace_size(shape), 1), dtype=torch.uint8, device=tokens.device)
+    _same_device(tokens, dx, dtable, ws)
+    rc = load_library().moe_embed_backward(
+        ctypes.byref(shape.c()), _arg(tokens, "tokens", "i32", T), _arg(dx, "dx", "f32", T, d),
+        _arg(dtable, "dtable", shape.grad_dtype, V, d), int(accumulate), _ptr(ws), ws.numel(), _stream())
+    _check(rc, "moe_embed_backward")
+    return dtable
+
+
+class TensorList:
+    """Tensors for moe_grad_sumsq and moe_grad_clip: contiguous fp32 or bf16 tensors
+    on the current device (slices of a larger buffer among them).  It keeps them
+    alive, and may be used for any number of steps."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        _same_device(*self.tensors)
+        code = {torch.float32: F32, torch.bfloat16: BF16}
+        for t in self.tensors:
+            if t.dtype not in code:
+                raise ValueError(f"expected f32 or bf16 tensors, got {t.dtype}")
+        self.c = (CTensor * max(len(self.tensors), 1))(*[(_ptr(t), t.numel(), code[t.dtype]) for t in self.tensors])
+
+    def __len__(self) -> int:
+        return len(self.tensors)
+
+
+def _tensor_list(tensors) -> TensorList:
+    return tensors if isinstance(tensors, TensorList) else TensorList(tensors)
+
+
+def grad_workspace_size(n: int) -> int:
+    b = ctypes.c_size_t(0)
+    _check(load_library().moe_grad_workspace_size(n, ctypes.byref(b)), "moe_grad_workspace_size")
+    return b.value
+
+
+def moe_grad_sumsq(grads, sumsq: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   device="cuda") -> torch.Tensor:
+    """The sum of squares of all elements of ``grads`` (a TensorList, or tensors), an
+    fp64 tensor of one element.  Over ranks or several lists, these add up."""
+    grads = _tensor_list(grads)
+    if sumsq is None:
+        sumsq = torch.empty((1,), dtype=torch.float64, device=device)
+    ws = workspace
+    if ws is None:
+        ws = torch.empty(grad_workspace_size(len(grads)), dtype=torch.uint8, device=device)
+    _same_device(sumsq, ws)
+    rc = load_library().moe_grad_sumsq(grads.c, len(grads), _arg(sumsq, "sumsq", "f64", 1), _ptr(ws), ws.numel(), _stream())
+    _check(rc, "moe_grad_sumsq")
+    return sumsq
+
+
+def moe_grad_clip(grads, sumsq: torch.Tensor, max_norm: float, out=None, norm: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Scales ``grads`` by min(1, max_norm / norm), norm = sqrt(sumsq), in place or
+    into ``out`` (as many tensors of the same sizes).  Returns the norm, an fp32
+    tensor of one element; a NaN or infinite sumsq clips nothing."""
+    grads = _tensor_list(grads)
+    out = None if out is None else _tensor_list(out)
+    if out is not None and len(out) != len(grads):
+        raise ValueError(f"out: expected {len(grads)} tensors, got {len(out)}")
+    if norm is None:
+        norm = torch.empty((1,), dtype=torch.float32, device=sumsq.device)
+    _same_device(sumsq, norm)
+    rc = load_library().moe_grad_clip(grads.c, None if out is None else out.c, len(grads), _arg(sumsq, "sumsq", "f64", 1),
+                                      float(max_norm), _arg(norm, "norm", "f32", 1), _stream())
+    _check(rc, "moe_grad_clip")
+    return norm
 
 
 def moe_update_bias(bias: torch.Tensor, counts: torch.Tensor, total_assignments: int, gamma: float = 0.001):

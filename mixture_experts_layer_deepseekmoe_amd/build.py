@@ -24,8 +24,8 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 # after every call), loaded only where asked for
 DEBUG_LIB_PATH = os.path.join(PKG, "libmoe_mi355x_debug.so")
 
-SOURCES = ["route.hip", "group.hip", "ggemm.hip", "combine.hip", "bwd.hip", "block.hip", "loss.hip",
-           "moe_api.cpp", "block_api.cpp", "loss_api.cpp"]
+SOURCES = ["route.hip", "group.hip", "ggemm.hip", "combine.hip", "bwd.hip", "block.hip", "loss.hip", "few.hip",
+           "embed.hip", "grads.hip", "moe_api.cpp", "block_api.cpp", "loss_api.cpp", "few_api.cpp", "ends_api.cpp"]
 ARCH = "gfx950"
 # measured-ceiling probes (MFMA with random / zero operands, HBM stream), a
 # standalone program run by `profiling.py peaks`

@@ -1,0 +1,685 @@
+// The layer's forward for a few tokens (1 to 64):
+//
+//   s = sigmoid(u E^T), the K largest of s + b, g = s / sum of the K selected s
+//   h = SiLU(W_gate u) * (W_up u) for each selected and shared expert
+//   y = u + sum_shared W_down h + sum_k g_k W_down h_k
+//
+// Each selected expert's matrices are read once and nothing else is large: the
+// whole is bound by HBM.  The weights therefore go from global memory straight
+// into the MFMAs' first operand (16 rows of weights, 16 bytes a lane), no LDS;
+// the tokens are the second operand's 16 columns, read through the caches.  The
+// waves of a block take 128-byte runs of K in turn and their sums meet in LDS.
+//
+//   few_route_kernel   partial logits, 16 experts and a slice of K to a block
+//                      (8-bit weights: also u's 1x128 codes)
+//   few_gateup_kernel  every block first selects the experts of all tokens for
+//                      itself (a launch and a trip through memory less), then
+//                      takes (expert, 16 columns of I) units
+//   few_quant_kernel   8-bit weights: h's 1x128 codes
+//   few_down_kernel    16 columns of y to a block, over all experts in turn: the
+//                      gated sum and the residual stay in registers, in a fixed order
+//
+// Sums are fp32.  With bf16 weights the operand h is a pair of bf16 values, what
+// the first rounds off in the second (2^-16 is left): the MFMAs wait for HBM
+// anyway, so y is as exact as with fp32 products.
+#include "few.hpp"
+#include "gemm_core.hpp"
+
+namespace moe {
+
+namespace {
+
+constexpr int THREADS = 512, WAVES = 8;
+constexpr int MAX_SEL = FEW_TOKENS * MAX_TOPK;
+
+__device__ __forceinline__ i32x4 load16(rsrc_t r, uint32_t off, uint32_t soff) {
+  return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, 0));
+}
+
+// One 128-byte run of K: the products of 16 weight rows with 16 tokens.  A lane holds
+// bytes 16 lg .. +15 of each half of the run, of its weight row and of its token alike.
+template <int FMT>
+__device__ __forceinline__ f32x4 run_product(const i32x4 (&w)[2], const i32x4 (&x)[2], f32x4 c) {
+  if constexpr (FMT == FMT_BF16) {
+    return mfma_bf16(w[1], x[1], mfma_bf16(w[0], x[0], c));
+  } else if constexpr (FMT == FMT_F32) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c = mfma_f32(__int_as_float(w[k][e]), __int_as_float(x[k][e]), c);
+    return c;
+  } else {
+    i32x8 a, b;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      a[e] = w[e / 4][e % 4];
+      b[e] = x[e / 4][e % 4];
+    }
+    return mfma_e4m3(a, b, c);
+  }
+}
+
+// ------------------------------------------------------------------ selection
+
+// Largest value over the wave, in every lane.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+  return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xf, false)));
+}
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  v = dpp_max<0x111, 0xf>(v);   // row_shr 1, 2, 4, 8: lane 15 of each row has the row's
+  v = dpp_max<0x112, 0xf>(v);
+  v = dpp_max<0x114, 0xf>(v);
+  v = dpp_max<0x118, 0xf>(v);
+  v = dpp_max<0x142, 0xa>(v);   // row_bcast 15, 31: lane 63 has the wave's
+  v = dpp_max<0x143, 0xc>(v);
+  return __builtin_amdgcn_readlane(v, 63);
+}
+
+// Order-preserving bits of a key: above 0 for every value, NaN as -inf.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  if (v != v) v = -INFINITY;
+  const uint32_t u = __float_as_uint(v);
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+
+// The top-K of one token by one wave, as the router's (descending s + b, exact
+// ties to the lower expert, NaN below every number); `keys` is the wave's own LDS.
+__device__ __forceinline__ void few_select(const FewArgs& a, int t, float* keys, int32_t* idx_out, float* gate_out) {
+  constexpr int NQ = MAX_ROUTED / 64;
+  const int lane = threadIdx.x & 63, N = a.n_routed;
+  const size_t stride = static_cast<size_t>(a.T) * N;
+  float s[NQ];
+  uint32_t key[NQ];
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) {
+    s[q] = 0.f;
+    key[q] = 0;
+    const int e = lane + 64 * q;
+    if (e >= N) continue;
+    const float* src = a.logits + static_cast<size_t>(t) * N + e;
+    float z = 0.f;
+    for (int k = 0; k < a.slices; ++k) z += src[k * stride];
+    s[q] = sigmoid_f32(z);
+    const float v = s[q] + a.bias[e];
+    key[q] = ordered(v);
+    if (a.topk_groups < a.n_groups) keys[e] = v != v ? -INFINITY : v;
+  }
+  if (a.topk_groups < a.n_groups) {
+    // a group's score: the sum of its qg largest keys, largest first
+    const int size = N / a.n_groups, qg = min((a.top_k + a.topk_groups - 1) / a.topk_groups, size);
+    __builtin_amdgcn_wave_barrier();
+    uint32_t score = 0;
+    if (lane < a.n_groups) {
+      const float* g = keys + lane * size;
+      float sum = 0.f, pv = INFINITY;
+      int pe = -1;
+      for (int j = 0; j < qg; ++j) {
+        float bv = -INFINITY;
+        int be = 0x7fffffff;
+#pragma unroll 4
+        for (int m = 0; m < size; ++m) {
+          const float x = g[m];
+          const bool after = x < pv || (x == pv && m > pe);
+          if (after && (x > bv || (x == bv && m < be))) { bv = x; be = m; }
+        }
+        sum += bv;
+        pv = bv;
+        pe = be;
+      }
+      score = ordered(sum);
+    }
+    unsigned long long kept = 0;
+    for (int j = 0; j < a.topk_groups; ++j) {
+      const uint32_t m = wave_max_u32(score);
+      const int g = __ffsll(__ballot(score == m)) - 1;
+      kept |= 1ULL << g;
+      if (lane == g) score = 0;
+    }
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      const int e = lane + 64 * q;
+      if (e < N && !((kept >> (e / size)) & 1ULL)) key[q] = 0;
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  int chosen = 0;
+  float chosen_s = 0.f, sum = 0.f;
+  for (int k = 0; k < a.top_k; ++k) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) m = max(m, key[q]);
+    m = wave_max_u32(m);
+    int be = -1;
+    float bs = 0.f;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {   // 64 experts at a time: the lowest expert of equal keys
+      if (be >= 0) continue;
+      const unsigned long long b = __ballot(key[q] == m);
+      if (b == 0) continue;
+      const int l = __ffsll(b) - 1;
+      be = 64 * q + l;
+      bs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s[q]), l));
+      if (lane == l) key[q] = 0;
+    }
+    if (!MOE_CHECK(be >= 0 && be < N, 801)) be = 0;
+    sum += bs;
+    if (lane == k) { chosen = be; chosen_s = bs; }
+  }
+  if (lane < a.top_k) {
+    idx_out[lane] = chosen;
+    gate_out[lane] = chosen_s / sum;
+  }
+}
+
+// The experts that have rows, in order, the shared ones last; each one's rows are
+// its tokens in order.
+struct Lists {
+  unsigned long long mask[MAX_ROUTED + MAX_SHARED];   // tokens of entry i (first: of expert i)
+  int32_t expert[MAX_ROUTED + MAX_SHARED];            // of entry i; N_r + s: shared
+  int32_t row0[MAX_ROUTED + MAX_SHARED];              // first row of entry i
+  int32_t at[MAX_ROUTED];                             // first row of expert e
+  int32_t wave_n[WAVES], wave_rows[WAVES];
+  int32_t n;
+};
+
+// From idx [T][K] (LDS); `token` and `gate_row` (nullable) receive each routed row's token and gate.
+__device__ __forceinline__ void make_lists(const FewArgs& a, Lists& L, const int32_t* idx, const float* gate,
+                                           int32_t* token, float* gate_row) {
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), TK = a.T * a.top_k;
+  for (int e = tid; e < MAX_ROUTED; e += THREADS) L.mask[e] = 0;
+  __syncthreads();
+  for (int i = tid; i < TK; i += THREADS) atomicOr(&L.mask[idx[i]], 1ULL << (i / a.top_k));
+  __syncthreads();
+  static_assert(MAX_ROUTED <= THREADS, "a thread an expert");
+  const unsigned long long mine = tid < a.n_routed ? L.mask[tid] : 0;
+  const unsigned long long live = __ballot(mine != 0);
+  const int rows = __popcll(mine);
+  int before = rows;   // inclusive, then exclusive
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int v = __shfl_up(before, off);
+    if (lane >= off) before += v;
+  }
+  if (lane == 63) {
+    L.wave_n[w] = __popcll(live);
+    L.wave_rows[w] = before;
+  }
+  before -= rows;
+  __syncthreads();   // every mask is in a register now
+  int n0 = 0, r0 = 0, n = 0;
+#pragma unroll
+  for (int k = 0; k < WAVES; ++k) {
+    if (k < w) { n0 += L.wave_n[k]; r0 += L.wave_rows[k]; }
+    n += L.wave_n[k];
+  }
+  if (tid < a.n_routed) {
+    L.at[tid] = r0 + before;
+    if (mine != 0) {
+      const int i = n0 + __popcll(live & ((1ULL << lane) - 1));
+      L.mask[i] = mine;
+      L.expert[i] = tid;
+      L.row0[i] = r0 + before;
+      int row = r0 + before;
+      if (token != nullptr)
+        for (unsigned long long m = mine; m != 0; m &= m - 1) token[row++] = __ffsll(m) - 1;
+    }
+  }
+  if (tid < a.n_shared && a.T > 0) {
+    L.mask[n + tid] = a.T < 64 ? (1ULL << a.T) - 1 : ~0ULL;
+    L.expert[n + tid] = a.n_routed + tid;
+    L.row0[n + tid] = TK + tid * a.T;
+  }
+  if (tid == 0) L.n = n + (a.T > 0 ? a.n_shared : 0);
+  __syncthreads();
+}
+
+// ------------------------------------------------------------------ router
+
+template <int FMT, int NT>
+__global__ __launch_bounds__(THREADS) void few_route_kernel(FewArgs a, int blocks) {
+  __shared__ f32x4 red[WAVES][NT][64];
+  const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  if (static_cast<int>(blockIdx.x) >= blocks) {
+    // 8-bit weights: u's 1x128 tiles, 16 lanes each, as moe_quantize_act_e4m3
+    const int tiles = a.d / 128, i = (blockIdx.x - blocks) * (THREADS / 16) + (threadIdx.x >> 4);
+    const bool live = i < a.T * tiles;
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    const size_t off = static_cast<size_t>(i) * 128 + (lane & 15) * 8;
+    if (live) raw = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.u) + off);
+    const uint32_t words[4] = {raw.x, raw.y, raw.z, raw.w};
+    float v[8], m = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[e] = __uint_as_float(e % 2 ? words[e / 2] & 0xffff0000u : words[e / 2] << 16);
+      m = fmaxf(m, fabsf(v[e]));
+    }
+    m = wave_max_16(m);
+    const float inv = m == 0.f ? 0.f : 448.f / m;
+    const uint32_t lo = e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+    const uint32_t hi = e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+    if (live) {
+      *reinterpret_cast<uint2*>(a.uq + off) = make_uint2(lo, hi);
+      if ((lane & 15) == 0) a.us[i] = m == 0.f ? 1.f : m / 448.f;
+    }
+    return;
+  }
+  const int tiles = (a.n_routed + 15) / 16, tile = blockIdx.x % tiles, slice = blockIdx.x / tiles;
+  if (!MOE_CHECK(slice < a.slices, 802)) return;
+  const uint32_t ld = a.d * (FMT == FMT_F32 ? 4 : 2);
+  const int runs = ld / 128, per = (runs + a.slices - 1) / a.slices;
+  const int p1 = min(runs, (slice + 1) * per);
+  const rsrc_t re = make_rsrc(a.centroids, a.n_routed * ld), ru = make_rsrc(a.u, a.T * ld);   // past the end: zeros
+  const uint32_t oe = (16 * tile + lr) * ld + 16 * lg;
+  f32x4 acc[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+  for (int p = slice * per + w; p < p1; p += WAVES) {
+    i32x4 e[2], x[NT][2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) e[k] = load16(re, oe, 128 * p + 64 * k);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) x[t][k] = load16(ru, (16 * t + lr) * ld + 16 * lg, 128 * p + 64 * k);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[t] = run_product<FMT>(e, x[t], acc[t]);
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) red[w][t][lane] = acc[t];
+  __syncthreads();
+  if (w >= NT) return;
+  f32x4 z = red[0][w][lane];
+#pragma unroll
+  for (int k = 1; k < WAVES; ++k) z += red[k][w][lane];
+  // lane: token 16 w + lr, experts 16 tile + 4 lg .. +3
+  const int t = 16 * w + lr;
+  if (t >= a.T) return;
+  float* dst = a.logits + (static_cast<size_t>(slice) * a.T + t) * a.n_routed;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int e = 16 * tile + 4 * lg + r;
+    if (e < a.n_routed) dst[e] = z[r];
+  }
+}
+
+// ------------------------------------------------------------------ gate, up, SwiGLU
+
+// The sums of one unit over this wave's runs: 16 gate rows and the 16 up rows beside them.
+template <int FMT, int NT>
+__device__ __forceinline__ void gateup_sums(rsrc_t rw, rsrc_t rx, const uint32_t (&ow)[2], const uint32_t (&ox)[NT],
+                                            int runs, const float* sg, const float* su, const float* const (&sx)[NT],
+                                            f32x4 (&acc)[2][NT]) {
+  const int w = wave_id();
+#pragma unroll 2
+  for (int p = w; p < runs; p += WAVES) {
+    i32x4 a[2][2], x[NT][2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) a[s][k] = load16(rw, ow[s], 128 * p + 64 * k);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) x[t][k] = load16(rx, ox[t], 128 * p + 64 * k);
+    if constexpr (FMT == FMT_E4M3) {
+      const float g = sg[p], u = su[p];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const float s = sx[t][p];
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+        acc[0][t] += run_product<FMT>(a[0], x[t], zero) * (s * g);
+        acc[1][t] += run_product<FMT>(a[1], x[t], zero) * (s * u);
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) acc[s][t] = run_product<FMT>(a[s], x[t], acc[s][t]);
+    }
+  }
+}
+
+// Two bf16 values whose sum is v to 2^-16: its rounding, and that of what it left
+// (of v itself: not contracted with the product that v is, which only some builds do).
+__device__ __forceinline__ void split4(const float (&v)[4], uint2& hi, uint2& lo) {
+#pragma clang fp contract(off)
+  hi = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+  const uint32_t b[4] = {hi.x << 16, hi.x & 0xffff0000u, hi.y << 16, hi.y & 0xffff0000u};
+  float r[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float f = __uint_as_float(b[e]);
+    r[e] = fabsf(f) < INFINITY ? v[e] - f : 0.f;   // infinities and NaN stay in the first
+  }
+  lo = make_uint2(bf16x2(r[0], r[1]), bf16x2(r[2], r[3]));
+}
+
+template <int FMT, int NT>
+__device__ __forceinline__ void gateup_unit(const FewArgs& a, int e, int row0, int rows, const int32_t* token, int i0,
+                                            f32x4 (*red)[2][64]) {
+  constexpr int ES = FMT == FMT_F32 ? 4 : FMT == FMT_BF16 ? 2 : 1;
+  const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const bool shared = e >= a.n_routed;
+  const int m = shared ? e - a.n_routed : e, TK = a.T * a.top_k;
+  const uint32_t ld = a.d * ES;
+  const uint8_t* base = static_cast<const uint8_t*>(shared ? a.ws_gate_up : a.w_gate_up) +
+                        static_cast<size_t>(m) * 2 * a.inter * ld;
+  const rsrc_t rw = make_rsrc(base, 2u * a.inter * ld);
+  const rsrc_t rx = make_rsrc(FMT == FMT_E4M3 ? static_cast<const void*>(a.uq) : a.u, a.T * ld);
+  const uint32_t ow[2] = {(i0 + lr) * ld + 16 * lg, (a.inter + i0 + lr) * ld + 16 * lg};
+  const int runs = a.d * ES / 128;
+  uint32_t ox[NT];
+  const float* sx[NT];
+  const float *sg = nullptr, *su = nullptr;
+  if constexpr (FMT == FMT_E4M3) {
+    sg = (shared ? a.ss_gate_up : a.s_gate_up) + (static_cast<size_t>(m) * 2 * a.inter + i0) / 128 * runs;
+    su = sg + static_cast<size_t>(a.inter / 128) * runs;
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int r = 16 * t + lr;
+    const int tok = r < rows ? (shared ? r : token[row0 + r]) : a.T;
+    ox[t] = tok * ld + 16 * lg;   // past the last token: zeros
+    sx[t] = nullptr;
+    if constexpr (FMT == FMT_E4M3) sx[t] = a.us + static_cast<size_t>(min(tok, a.T - 1)) * runs;
+  }
+  f32x4 acc[2][NT];
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[s][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  gateup_sums<FMT, NT>(rw, rx, ow, ox, runs, sg, su, sx, acc);
+  __syncthreads();   // the last unit's sums have been read
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int s = 0; s < 2; ++s) red[w * NT + t][s][lane] = acc[s][t];
+  __syncthreads();
+  // wave t: row 16 t + lr, columns i0 + 4 lg .. +3
+  if (w >= NT || 16 * w + lr >= rows) return;
+  f32x4 g = red[w][0][lane], u = red[w][1][lane];
+#pragma unroll
+  for (int k = 1; k < WAVES; ++k) {
+    g += red[k * NT + w][0][lane];
+    u += red[k * NT + w][1][lane];
+  }
+  float h[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) h[r] = silu_f32(g[r]) * u[r];
+  const int row = row0 + 16 * w + lr;
+  if (!MOE_CHECK(row < TK + a.n_shared * a.T, 803)) return;
+  const size_t off = static_cast<size_t>(row) * a.inter + i0 + 4 * lg;
+  if constexpr (FMT == FMT_BF16) {
+    uint2 hi, lo;
+    split4(h, hi, lo);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.h) + off) = hi;
+    *reinterpret_cast<uint2*>(a.h_lo + off) = lo;
+  } else {
+    *reinterpret_cast<float4*>(static_cast<float*>(a.h) + off) = make_float4(h[0], h[1], h[2], h[3]);
+  }
+}
+
+// NT: tiles of 16 tokens that an expert may have.
+template <int FMT, int NT>
+__global__ __launch_bounds__(THREADS, 2) void few_gateup_kernel(FewArgs a) {
+  __shared__ Lists L;
+  __shared__ int32_t idx[16 * NT * MAX_TOPK], token[16 * NT * MAX_TOPK];
+  __shared__ float gate[16 * NT * MAX_TOPK];
+  __shared__ union {
+    float keys[WAVES][MAX_ROUTED];
+    f32x4 red[WAVES * NT][2][64];
+  } s;
+  const int w = wave_id();
+  if (!MOE_CHECK(a.T <= 16 * NT, 804)) return;
+  for (int t = w; t < a.T; t += WAVES) few_select(a, t, s.keys[w], idx + t * a.top_k, gate + t * a.top_k);
+  __syncthreads();
+  make_lists(a, L, idx, gate, token, nullptr);
+  if (blockIdx.x == 0) {
+    const int TK = a.T * a.top_k;
+    for (int i = threadIdx.x; i < TK; i += THREADS) {
+      a.idx[i] = idx[i];
+      a.gate[i] = gate[i];
+      if (a.perm_token != nullptr) a.perm_token[i] = token[i];
+      if (a.pos != nullptr) {
+        int row = L.at[idx[i]];
+        while (token[row] != i / a.top_k) ++row;   // it is among its expert's rows
+        a.pos[i] = row;
+      }
+    }
+    for (int e = threadIdx.x; e < a.n_routed; e += THREADS) {
+      if (a.counts != nullptr) a.counts[e] = (e + 1 < a.n_routed ? L.at[e + 1] : TK) - L.at[e];
+      if (a.offsets != nullptr) a.offsets[e] = L.at[e];
+    }
+    if (a.offsets != nullptr && threadIdx.x == 0) a.offsets[a.n_routed] = TK;
+  }
+  const int cols = a.inter / 16;
+  for (int i = blockIdx.x; i < L.n * cols; i += gridDim.x) {
+    const int k = i / cols, i0 = 16 * (i - k * cols);
+    const int e = __builtin_amdgcn_readfirstlane(L.expert[k]), row0 = __builtin_amdgcn_readfirstlane(L.row0[k]);
+    const int rows = __builtin_amdgcn_readfirstlane(__popcll(L.mask[k]));
+    if constexpr (NT >= 4) {
+      if (rows > 32) {
+        gateup_unit<FMT, 4>(a, e, row0, rows, token, i0, s.red);
+        continue;
+      }
+    }
+    if constexpr (NT >= 2) {
+      if (rows > 16) {
+        gateup_unit<FMT, 2>(a, e, row0, rows, token, i0, s.red);
+        continue;
+      }
+    }
+    gateup_unit<FMT, 1>(a, e, row0, rows, token, i0, s.red);
+  }
+}
+
+// 8-bit weights: h's 1x128 tiles, 32 lanes each (4 columns a lane).
+__global__ __launch_bounds__(256) void few_quant_kernel(FewArgs a) {
+  const long long tiles = static_cast<long long>(a.T) * (a.top_k + a.n_shared) * (a.inter / 128);
+  const long long i = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int l = threadIdx.x & 31;
+  if (i >= tiles) return;
+  const size_t off = static_cast<size_t>(i) * 128 + 4 * l;
+  const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.h) + off);
+  float m = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
+  const float inv = m == 0.f ? 0.f : 448.f / m;
+  *reinterpret_cast<uint32_t*>(a.hq + off) = e4m3x4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+  if (l == 0) a.hs[i] = m == 0.f ? 1.f : m / 448.f;
+}
+
+// ------------------------------------------------------------------ down, gates, residual
+
+template <int FMT, int NT>
+__global__ __launch_bounds__(THREADS, 2) void few_down_kernel(FewArgs a) {
+  constexpr int ES = FMT == FMT_F32 ? 4 : FMT == FMT_BF16 ? 2 : 1;
+  constexpr int CH = 2;   // runs in flight
+  __shared__ Lists L;
+  __shared__ int32_t idx[16 * NT * MAX_TOPK];
+  __shared__ float gate_row[16 * NT * MAX_TOPK];
+  __shared__ f32x4 red[WAVES][NT][64];
+  const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
+  const int TK = a.T * a.top_k, R = TK + a.n_shared * a.T, d0 = 16 * blockIdx.x;
+  if (!MOE_CHECK(a.T <= 16 * NT && d0 + 16 <= a.d, 805)) return;
+  for (int i = threadIdx.x; i < TK; i += THREADS) {
+    int e = a.idx[i];
+    if (!MOE_CHECK(e >= 0 && e < a.n_routed, 806)) e = 0;
+    idx[i] = e;
+  }
+  __syncthreads();
+  make_lists(a, L, idx, nullptr, nullptr, nullptr);
+  // the rows' gates
+  for (int k = threadIdx.x >> 6; k < L.n; k += WAVES) {
+    const unsigned long long m = L.mask[k];
+    const int e = L.expert[k];
+    if (e < a.n_routed && (m >> lane & 1)) {
+      int j = 0;
+      while (j < a.top_k - 1 && idx[lane * a.top_k + j] != e) ++j;
+      gate_row[L.row0[k] + __popcll(m & ((1ULL << lane) - 1))] = a.gate[lane * a.top_k + j];
+    }
+  }
+  __syncthreads();
+
+  const uint32_t ld = a.inter * ES;
+  const int runs = ld / 128;
+  const rsrc_t rh = make_rsrc(FMT == FMT_E4M3 ? static_cast<const void*>(a.hq) : a.h, static_cast<uint32_t>(R) * ld);
+  const rsrc_t rl = make_rsrc(a.h_lo, FMT == FMT_BF16 ? static_cast<uint32_t>(R) * ld : 0);
+  f32x4 acc[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  int first = w;   // of the waves' turns over all experts' runs
+  for (int k = 0; k < L.n; ++k) {
+    const int e = __builtin_amdgcn_readfirstlane(L.expert[k]), row0 = __builtin_amdgcn_readfirstlane(L.row0[k]);
+    const unsigned long long m = L.mask[k];
+    const bool shared = e >= a.n_routed;
+    const int mat = shared ? e - a.n_routed : e;
+    const rsrc_t rw = make_rsrc(static_cast<const uint8_t*>(shared ? a.ws_down : a.w_down) +
+                                (static_cast<size_t>(mat) * a.d + d0) * ld, 16 * ld);
+    const float* sw = nullptr;
+    if constexpr (FMT == FMT_E4M3)
+      sw = (shared ? a.ss_down : a.s_down) + (static_cast<size_t>(mat) * a.d + d0) / 128 * runs;
+    int p = first;
+    for (; p < runs; p += CH * WAVES) {
+      i32x4 wf[CH][2];
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) wf[c][h] = load16(rw, lr * ld + 16 * lg, 128 * (p + WAVES * c) + 64 * h);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const uint32_t part = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(m >> (16 * t)) & 0xffffu);
+        if (part == 0) continue;
+        const int tok = 16 * t + lr;
+        const bool in = m >> tok & 1;
+        const int row = in ? row0 + __popcll(m & ((1ULL << tok) - 1)) : R;   // R: zeros
+        const uint32_t oh = static_cast<uint32_t>(row) * ld + 16 * lg;
+        const float g = in && !shared ? gate_row[row] : 1.f;
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          const int q = p + WAVES * c;
+          if (c > 0 && q >= runs) continue;
+          i32x4 x[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) x[h] = load16(rh, oh, 128 * q + 64 * h);
+          if constexpr (FMT == FMT_E4M3) {
+            const float s = in ? a.hs[static_cast<size_t>(row) * runs + q] : 0.f;
+            sum += run_product<FMT>(wf[c], x, f32x4{0.f, 0.f, 0.f, 0.f}) * (s * sw[q]);
+          } else {
+            sum = run_product<FMT>(wf[c], x, sum);
+            if constexpr (FMT == FMT_BF16) {
+              i32x4 y[2];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) y[h] = load16(rl, oh, 128 * q + 64 * h);
+              sum = run_product<FMT>(wf[c], y, sum);
+            }
+          }
+        }
+        // a token that does not use this expert keeps its sum, whatever the weights hold
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[t][r] = in ? fmaf(g, sum[r], acc[t][r]) : acc[t][r];
+      }
+    }
+    // the first run of the next expert that is this wave's
+    first = (first + WAVES - runs % WAVES) % WAVES;
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) red[w][t][lane] = acc[t];
+  __syncthreads();
+  const int t = 16 * w + lr;
+  if (w >= NT || t >= a.T) return;
+  f32x4 y = red[0][w][lane];
+#pragma unroll
+  for (int k = 1; k < WAVES; ++k) y += red[k][w][lane];
+  const size_t off = static_cast<size_t>(t) * a.d + d0 + 4 * lg;
+  float v[4];
+  if (a.x_fmt == FMT_F32) {
+    const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(a.u) + off);
+    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.u) + off);
+    v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
+    v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) v[r] += y[r];
+  if (a.out_fmt == FMT_F32)
+    *reinterpret_cast<float4*>(static_cast<float*>(a.y) + off) = make_float4(v[0], v[1], v[2], v[3]);
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + off) = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+}
+
+template <int NT>
+struct Launch {
+  static void route(const FewArgs& a, hipStream_t s) {
+    const int blocks = (a.n_routed + 15) / 16 * a.slices;
+    const int quant = a.w_fmt == FMT_E4M3 ? ceil_div(a.T * (a.d / 128), THREADS / 16) : 0;
+    if (a.x_fmt == FMT_F32)
+      hipLaunchKernelGGL((few_route_kernel<FMT_F32, NT>), dim3(blocks), dim3(THREADS), 0, s, a, blocks);
+    else
+      hipLaunchKernelGGL((few_route_kernel<FMT_BF16, NT>), dim3(blocks + quant), dim3(THREADS), 0, s, a, blocks);
+  }
+  template <int FMT>
+  static void gateup(const FewArgs& a, hipStream_t s) {
+    const int tk = a.T * a.top_k;
+    const long long units = static_cast<long long>((tk < a.n_routed ? tk : a.n_routed) + a.n_shared) * (a.inter / 16);
+    hipLaunchKernelGGL((few_gateup_kernel<FMT, NT>), dim3(static_cast<unsigned>(units < 1 ? 1 : units < 2048 ? units : 2048)),
+                       dim3(THREADS), 0, s, a);
+  }
+  template <int FMT>
+  static void down(const FewArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL((few_down_kernel<FMT, NT>), dim3(a.d / 16), dim3(THREADS), 0, s, a);
+  }
+};
+
+template <class F>
+hipError_t by_tokens(int T, F&& f) {
+  if (T <= 16)
+    f(Launch<1>{});
+  else if (T <= 32)
+    f(Launch<2>{});
+  else
+    f(Launch<4>{});
+  return hipGetLastError();
+}
+
+}  // namespace
+
+MOE_DEBUG_FILE(few)
+
+hipError_t launch_few_route(const FewArgs& a, hipStream_t s) {
+  return by_tokens(a.T, [&](auto l) { l.route(a, s); });
+}
+
+hipError_t launch_few_gateup(const FewArgs& a, hipStream_t s) {
+  return by_tokens(a.T, [&](auto l) {
+    if (a.w_fmt == FMT_F32)
+      l.template gateup<FMT_F32>(a, s);
+    else if (a.w_fmt == FMT_BF16)
+      l.template gateup<FMT_BF16>(a, s);
+    else
+      l.template gateup<FMT_E4M3>(a, s);
+  });
+}
+
+hipError_t launch_few_quant(const FewArgs& a, hipStream_t s) {
+  const long long tiles = static_cast<long long>(a.T) * (a.top_k + a.n_shared) * (a.inter / 128);
+  hipLaunchKernelGGL(few_quant_kernel, dim3(static_cast<unsigned>((tiles + 7) / 8)), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_few_down(const FewArgs& a, hipStream_t s) {
+  return by_tokens(a.T, [&](auto l) {
+    if (a.w_fmt == FMT_F32)
+      l.template down<FMT_F32>(a, s);
+    else if (a.w_fmt == FMT_BF16)
+      l.template down<FMT_BF16>(a, s);
+    else
+      l.template down<FMT_E4M3>(a, s);
+  });
+}
+
+}  // namespace moe

@@ -1,0 +1,65 @@
+// Internal launcher interface of the layer's forward for a few tokens (few.hip).
+#pragma once
+
+#include "kernels.hpp"
+
+namespace moe {
+
+constexpr int FEW_TOKENS = 64;   // a token per bit of an expert's 64-bit mask
+
+struct FewArgs {
+  const void* u;            // [T][d] x_fmt
+  const void* centroids;    // [N_r][d] x_fmt
+  const float* bias;        // [N_r]
+  const void* w_gate_up;    // [N_r][2I][d] w_fmt
+  const void* w_down;       // [N_r][d][I]
+  const void* ws_gate_up;   // [N_s][2I][d]
+  const void* ws_down;      // [N_s][d][I]
+  const float* s_gate_up;   // e4m3: the block scales
+  const float* s_down;
+  const float* ss_gate_up;
+  const float* ss_down;
+  int T, d, n_routed, n_shared, inter, top_k, n_groups, topk_groups;
+  int x_fmt, w_fmt, out_fmt;
+  int slices;               // few_slices(...)
+  float* logits;            // [slices][T][N_r] partial logits
+  int32_t* idx;             // [T][K]
+  float* gate;              // [T][K]
+  // the rest of the routing, each null where not wanted
+  int32_t* counts;          // [N_r]
+  int32_t* offsets;         // [N_r + 1]
+  int32_t* perm_token;      // [T*K]
+  int32_t* pos;             // [T][K]
+  // SwiGLU outputs by grouped row (expert-major, tokens ascending; then the shared experts'): fp32 values, or
+  // their bf16 roundings (h) and what those left (h_lo)
+  void* h;                  // [R][I] f32 (f32 and e4m3 weights) or bf16
+  uint16_t* h_lo;           // [R][I] bf16
+  uint8_t* hq;              // e4m3: [R][I] codes and [R][I/128] scales
+  float* hs;
+  uint8_t* uq;              // e4m3: [T][d] codes and [T][d/128] scales
+  float* us;
+  void* y;                  // [T][d] out_fmt
+};
+
+// 128-byte runs of a row of `cols` elements.
+inline int few_runs(int cols, int fmt) { return cols * (fmt == FMT_F32 ? 4 : fmt == FMT_BF16 ? 2 : 1) / 128; }
+
+// The router's K slices: a block takes 16 experts and a slice of K, a run of 128
+// bytes a wave at a time, so one run for each of its 8 waves at least.  Every block of
+// the next kernel reads the slices of all tokens again: 16 of them together at most.
+inline int few_slices(int T, int d, int x_fmt) {
+  const int most = (few_runs(d, x_fmt) + 7) / 8, want = 16 / (T > 0 ? T : 1);
+  const int s = want < most ? want : most;
+  return s > 1 ? s : 1;
+}
+
+hipError_t launch_few_route(const FewArgs& a, hipStream_t s);
+hipError_t launch_few_gateup(const FewArgs& a, hipStream_t s);
+hipError_t launch_few_quant(const FewArgs& a, hipStream_t s);   // e4m3 only
+hipError_t launch_few_down(const FewArgs& a, hipStream_t s);
+
+#ifdef MOE_DEBUG
+int debug_take_few();   // check ids 8xx
+#endif
+
+}  // namespace moe

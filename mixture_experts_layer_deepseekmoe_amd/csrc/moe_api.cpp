@@ -144,18 +144,6 @@ int validate_shape(const moe_shape* s) {
   return MOE_OK;
 }
 
-// Optional per-stage event records on the caller's stream.
-struct Stages {
-  const moe_trace* tr;
-  hipStream_t st;
-  void begin(int i) const {
-    if (tr != nullptr && tr->start[i] != nullptr) (void)hipEventRecord(tr->start[i], st);
-  }
-  void end(int i) const {
-    if (tr != nullptr && tr->stop[i] != nullptr) (void)hipEventRecord(tr->stop[i], st);
-  }
-};
-
 // Route + group.  `mtiles` null: routing only (no GEMM tile list).
 int run_route(const moe_shape& s, const void* u, const void* cen, const float* bias, int32_t* idx, float* gate,
               int32_t* counts, int32_t* offsets, int32_t* perm, int32_t* pos, int32_t* hist, float* scores,
@@ -541,3 +529,17 @@ int moe_quantize_act_e4m3(const void* src, int32_t rows, int32_t cols, uint8_t* 
 }
 
 }  // extern "C"
+
+namespace moe::api {
+
+int layer_shape_status(const moe_shape* shape) { return validate_shape(shape); }
+
+int layer_args_status(const moe_shape* shape, const void* u, const void* centroids, const float* bias,
+                      const moe_weights* wt, const void* y) {
+  return validate_forward(shape, u, centroids, bias, wt, y);
+}
+
+int layer_groups(const moe_shape& s) { return groups_of(s); }
+int layer_topk_groups(const moe_shape& s) { return topk_groups_of(s); }
+
+}  // namespace moe::api

@@ -1,11 +1,14 @@
 """A small language model of MoE blocks, trained and then scored token by token
 with this package's operators only.
 
-    python -m mixture_experts_layer_deepseekmoe_amd.example [--steps 60]
+    python -m mixture_experts_layer_deepseekmoe_amd.example [--steps 60] [--max-norm 1]
 
 Each block is norm -> MoE layer -> norm, gate and residual; the loss is the
 cross entropy over the vocabulary.  The forward keeps 8-bit checkpoints of the
 normed rows, so a block's x, y and its output are not kept for the backward.
+The embedding brings the first block's norm; the gradients are clipped by their
+common norm (--max-norm); up to 64 tokens at a time are scored by the layer's
+forward for a few tokens.
 The task: the next token is a fixed function of the current one.
 """
 
@@ -36,6 +39,9 @@ class ModelShape:
 
     def block(self, T=None) -> moe.BlockShape:
         return moe.BlockShape(self.T if T is None else T, self.d, x_dtype="f32", n_dtype="bf16", y_dtype="f32")
+
+    def embed(self, T=None) -> moe.EmbedShape:
+        return moe.EmbedShape(self.T if T is None else T, self.d, self.vocab)
 
     def loss(self, T=None) -> moe.LossShape:
         return moe.LossShape(self.T if T is None else T, self.d, self.vocab)
@@ -69,11 +75,10 @@ class Model:
         """The final normed rows and, for training, what the backward needs."""
         s, p, T = self.s, self.params, tokens.numel()
         bs, ls = s.block(T), s.layer(T)
-        x = p["embed"][tokens.long()]
         keep: List[dict] = []
         new_save = lambda: moe.alloc_block_save(bs, e4m3=True) if train else None  # noqa: E731
         s_in = new_save()
-        n = moe.moe_block_in(bs, x, p["0.w_in"], save=s_in)
+        x, n = moe.moe_embed(s.embed(T), tokens, p["embed"], w_next=p["0.w_in"], save_next=s_in)
         for k in range(s.layers):
             cen, w = self._weights(k)
             if train:
@@ -81,7 +86,8 @@ class Model:
                 y = moe.moe_forward_train(ls, n, cen, self.bias[k], w, ws)
             else:
                 ws = None
-                y = moe.moe_forward(ls, n, cen, self.bias[k], w)
+                forward = moe.moe_forward_few if T <= moe.FEW_TOKENS else moe.moe_forward
+                y = forward(ls, n, cen, self.bias[k], w)
             s_out, s_next = new_save(), new_save()
             x, n_next = moe.moe_block_out(bs, x, y, w=p[f"{k}.w_out"], gate=p[f"{k}.gate"], skip=n,
                                           w_next=self._norm_after(k), save=s_out, save_next=s_next)
@@ -115,8 +121,14 @@ class Model:
                           f"{k}.ws_gate_up": gw.dws_gate_up, f"{k}.ws_down": gw.dws_down})
             # n feeds the layer (du) and, negated, the skip (dy); x feeds the norm and the residual (dx)
             dx, grads[f"{k}.w_in"] = moe.moe_block_in_backward(bs, du, p[f"{k}.w_in"], f["s_in"], dn_sub=dy, do=dx)
-        grads["embed"] = torch.zeros_like(p["embed"]).index_add_(0, tokens.long(), dx)
+        grads["embed"] = moe.moe_embed_backward(s.embed(), tokens, dx)
         return loss.sum() / count, grads
+
+
+def clip(grads: dict, max_norm: float) -> torch.Tensor:
+    """Scales all gradients, in place, by min(1, max_norm / norm); returns their norm."""
+    tensors = moe.TensorList(grads.values())
+    return moe.moe_grad_clip(tensors, moe.moe_grad_sumsq(tensors), max_norm)
 
 
 def make_batch(s: ModelShape, seed: int, ignored: float = 0.1):
@@ -128,11 +140,13 @@ def make_batch(s: ModelShape, seed: int, ignored: float = 0.1):
     return tokens, labels
 
 
-def train(s: ModelShape, steps: int, lr: float = 0.01, log=lambda *a: None) -> Model:
+def train(s: ModelShape, steps: int, lr: float = 0.01, log=lambda *a: None, max_norm: float = float("inf")) -> Model:
+    """``max_norm``: the gradients are scaled down to this norm (all of them together) where theirs is larger."""
     model = Model(s)
     opt = torch.optim.Adam(list(model.params.values()), lr=lr, betas=(0.9, 0.99))
     for k in range(steps):
         loss, grads = model.step(*make_batch(s, 100 + k))
+        clip(grads, max_norm)
         for name, q in model.params.items():
             q.grad = grads[name]
         opt.step()
@@ -144,9 +158,10 @@ def train(s: ModelShape, steps: int, lr: float = 0.01, log=lambda *a: None) -> M
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--steps", type=int, default=60)
+    ap.add_argument("--max-norm", type=float, default=float("inf"))
     args = ap.parse_args()
     s = ModelShape()
-    model = train(s, args.steps, log=lambda *a: print(*a, flush=True))
+    model = train(s, args.steps, log=lambda *a: print(*a, flush=True), max_norm=args.max_norm)
     # scoring: one new token at a time
     for token in (1, 500, 999):
         t = torch.tensor([token], dtype=torch.int32, device="cuda")
