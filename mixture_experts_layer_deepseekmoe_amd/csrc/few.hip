@@ -12,9 +12,10 @@
 //
 //   few_route_kernel   partial logits, 16 experts and a slice of K to a block
 //                      (8-bit weights: also u's 1x128 codes)
-//   few_gateup_kernel  every block first selects the experts of all tokens for
-//                      itself (a launch and a trip through memory less), then
-//                      takes (expert, 16 columns of I) units
+//   few_select_kernel  the experts of a token, by a wave.  Of up to 8 tokens every
+//                      block of the next kernel selects them for itself instead (a
+//                      launch and a trip through memory less)
+//   few_gateup_kernel  (expert, 16 columns of I) units
 //   few_quant_kernel   8-bit weights: h's 1x128 codes
 //   few_down_kernel    16 columns of y to a block, over all experts in turn: the
 //                      gated sum and the residual stay in registers, in a fixed order
@@ -25,17 +26,18 @@
 #include "few.hpp"
 #include "gemm_core.hpp"
 
+#include <type_traits>
+
 namespace moe {
 
 namespace {
 
 constexpr int THREADS = 512, WAVES = 8;
-constexpr int MAX_SEL = FEW_TOKENS * MAX_TOPK;
+constexpr int GATEUP_BLOCKS = 512;   // two to a CU, each taking units in turn
 
 __device__ __forceinline__ i32x4 load16(rsrc_t r, uint32_t off, uint32_t soff) {
   return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, 0));
 }
-
 // One 128-byte run of K: the products of 16 weight rows with 16 tokens.  A lane holds
 // bytes 16 lg .. +15 of each half of the run, of its weight row and of its token alike.
 template <int FMT>
@@ -83,25 +85,43 @@ __device__ __forceinline__ uint32_t ordered(float v) {
   return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 
-// The top-K of one token by one wave, as the router's (descending s + b, exact
-// ties to the lower expert, NaN below every number); `keys` is the wave's own LDS.
+// The top-K of one token by one wave, as the router's (descending s + b, exact ties
+// to the lower expert, NaN below every number).  A lane holds experts lane + 64 q in
+// descending order, so a round looks at the lanes' first ones alone (without, 2500
+// cycles a round; 250 with).  `keys` is the wave's own LDS, for group-limited routing.
+template <int NQ>
 __device__ __forceinline__ void few_select(const FewArgs& a, int t, float* keys, int32_t* idx_out, float* gate_out) {
-  constexpr int NQ = MAX_ROUTED / 64;
   const int lane = threadIdx.x & 63, N = a.n_routed;
   const size_t stride = static_cast<size_t>(a.T) * N;
-  float s[NQ];
+  const float* src = a.logits + static_cast<size_t>(t) * N + lane;
+  float s[NQ], b[NQ];
   uint32_t key[NQ];
+  int id[NQ];
 #pragma unroll
   for (int q = 0; q < NQ; ++q) {
     s[q] = 0.f;
+    b[q] = lane + 64 * q < N ? a.bias[lane + 64 * q] : 0.f;
+  }
+  constexpr int NS = 16 / NQ;   // slices whose loads go out together
+  for (int k = 0; k < a.slices; k += NS) {
+    float z[NS][NQ];
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) z[j][q] = k + j < a.slices && lane + 64 * q < N ? src[(k + j) * stride + 64 * q] : 0.f;
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) s[q] += z[j][q];
+  }
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) {
     key[q] = 0;
+    id[q] = q;
     const int e = lane + 64 * q;
     if (e >= N) continue;
-    const float* src = a.logits + static_cast<size_t>(t) * N + e;
-    float z = 0.f;
-    for (int k = 0; k < a.slices; ++k) z += src[k * stride];
-    s[q] = sigmoid_f32(z);
-    const float v = s[q] + a.bias[e];
+    s[q] = sigmoid_f32(s[q]);
+    const float v = s[q] + b[q];
     key[q] = ordered(v);
     if (a.topk_groups < a.n_groups) keys[e] = v != v ? -INFINITY : v;
   }
@@ -117,11 +137,16 @@ __device__ __forceinline__ void few_select(const FewArgs& a, int t, float* keys,
       for (int j = 0; j < qg; ++j) {
         float bv = -INFINITY;
         int be = 0x7fffffff;
-#pragma unroll 4
-        for (int m = 0; m < size; ++m) {
-          const float x = g[m];
-          const bool after = x < pv || (x == pv && m > pe);
-          if (after && (x > bv || (x == bv && m < be))) { bv = x; be = m; }
+        for (int m0 = 0; m0 < size; m0 += 8) {
+          float x[8];
+#pragma unroll
+          for (int m = 0; m < 8; ++m) x[m] = g[min(m0 + m, size - 1)];
+#pragma unroll
+          for (int m = 0; m < 8; ++m) {   // after the last taken, and before what the pass has
+            const bool take = (x[m] < pv || (x[m] == pv && m0 + m > pe)) && (x[m] > bv || be == 0x7fffffff) && m0 + m < size;
+            bv = take ? x[m] : bv;
+            be = take ? m0 + m : be;
+          }
         }
         sum += bv;
         pv = bv;
@@ -143,33 +168,50 @@ __device__ __forceinline__ void few_select(const FewArgs& a, int t, float* keys,
     }
     __builtin_amdgcn_wave_barrier();
   }
+  // neighbours change places where the later one is larger: equal keys keep their order
+#pragma unroll
+  for (int n = NQ - 1; n > 0; --n)
+#pragma unroll
+    for (int q = 0; q < n; ++q)
+      if (key[q] < key[q + 1]) {
+        const uint32_t k0 = key[q];
+        const float s0 = s[q];
+        const int i0 = id[q];
+        key[q] = key[q + 1]; s[q] = s[q + 1]; id[q] = id[q + 1];
+        key[q + 1] = k0; s[q + 1] = s0; id[q + 1] = i0;
+      }
   int chosen = 0;
   float chosen_s = 0.f, sum = 0.f;
   for (int k = 0; k < a.top_k; ++k) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) m = max(m, key[q]);
-    m = wave_max_u32(m);
-    int be = -1;
-    float bs = 0.f;
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) {   // 64 experts at a time: the lowest expert of equal keys
-      if (be >= 0) continue;
-      const unsigned long long b = __ballot(key[q] == m);
-      if (b == 0) continue;
-      const int l = __ffsll(b) - 1;
-      be = 64 * q + l;
-      bs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s[q]), l));
-      if (lane == l) key[q] = 0;
+    const uint32_t m = wave_max_u32(key[0]);
+    unsigned long long same = __ballot(key[0] == m);
+    int l = __ffsll(same) - 1, be = 64 * __builtin_amdgcn_readlane(id[0], l) + l;
+    for (same &= same - 1; same != 0; same &= same - 1) {   // equal keys: the lowest expert
+      const int l2 = __ffsll(same) - 1, e2 = 64 * __builtin_amdgcn_readlane(id[0], l2) + l2;
+      if (e2 < be) { be = e2; l = l2; }
     }
     if (!MOE_CHECK(be >= 0 && be < N, 801)) be = 0;
+    const float bs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s[0]), l));
     sum += bs;
     if (lane == k) { chosen = be; chosen_s = bs; }
+    if (lane == l) {
+#pragma unroll
+      for (int q = 0; q + 1 < NQ; ++q) { key[q] = key[q + 1]; s[q] = s[q + 1]; id[q] = id[q + 1]; }
+      key[NQ - 1] = 0;
+    }
   }
   if (lane < a.top_k) {
     idx_out[lane] = chosen;
     gate_out[lane] = chosen_s / sum;
   }
+}
+
+// One wave per token.
+template <int NQ>
+__global__ __launch_bounds__(256) void few_select_kernel(FewArgs a) {
+  __shared__ float keys[4][64 * NQ];
+  const int w = wave_id(), t = blockIdx.x * 4 + w;
+  if (t < a.T) few_select<NQ>(a, t, keys[w], a.idx + t * a.top_k, a.gate + t * a.top_k);
 }
 
 // The experts that have rows, in order, the shared ones last; each one's rows are
@@ -183,9 +225,16 @@ struct Lists {
   int32_t n;
 };
 
-// From idx [T][K] (LDS); `token` and `gate_row` (nullable) receive each routed row's token and gate.
-__device__ __forceinline__ void make_lists(const FewArgs& a, Lists& L, const int32_t* idx, const float* gate,
-                                           int32_t* token, float* gate_row) {
+__device__ __forceinline__ void load_selection(const FewArgs& a, int32_t* idx) {
+  for (int i = threadIdx.x; i < a.T * a.top_k; i += THREADS) {
+    int e = a.idx[i];
+    if (!MOE_CHECK(e >= 0 && e < a.n_routed, 806)) e = 0;
+    idx[i] = e;
+  }
+}
+
+// From idx [T][K] (LDS); `token` receives each routed row's token.
+__device__ __forceinline__ void make_lists(const FewArgs& a, Lists& L, const int32_t* idx, int32_t* token) {
   const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), TK = a.T * a.top_k;
   for (int e = tid; e < MAX_ROUTED; e += THREADS) L.mask[e] = 0;
   __syncthreads();
@@ -221,8 +270,7 @@ __device__ __forceinline__ void make_lists(const FewArgs& a, Lists& L, const int
       L.expert[i] = tid;
       L.row0[i] = r0 + before;
       int row = r0 + before;
-      if (token != nullptr)
-        for (unsigned long long m = mine; m != 0; m &= m - 1) token[row++] = __ffsll(m) - 1;
+      for (unsigned long long m = mine; m != 0; m &= m - 1) token[row++] = __ffsll(m) - 1;
     }
   }
   if (tid < a.n_shared && a.T > 0) {
@@ -306,40 +354,74 @@ __global__ __launch_bounds__(THREADS) void few_route_kernel(FewArgs a, int block
 
 // ------------------------------------------------------------------ gate, up, SwiGLU
 
-// The sums of one unit over this wave's runs: 16 gate rows and the 16 up rows beside them.
+// One unit's sums over this wave's runs: 16 gate rows and the 16 up rows beside them,
+// with NT tiles of 16 tokens.
 template <int FMT, int NT>
-__device__ __forceinline__ void gateup_sums(rsrc_t rw, rsrc_t rx, const uint32_t (&ow)[2], const uint32_t (&ox)[NT],
-                                            int runs, const float* sg, const float* su, const float* const (&sx)[NT],
-                                            f32x4 (&acc)[2][NT]) {
-  const int w = wave_id();
-#pragma unroll 2
-  for (int p = w; p < runs; p += WAVES) {
-    i32x4 a[2][2], x[NT][2];
+struct GateUp {
+  rsrc_t rw, rx;
+  uint32_t ow[2], ox[NT];
+  const float *sg, *su, *sx[NT];   // e4m3: the scales of the unit's blocks, of the tokens' tiles
+  f32x4 acc[2][NT];
+
+  // NB runs from p on: all their loads go out before the first product
+  template <int NB>
+  __device__ __forceinline__ void runs(int p) {
+    i32x4 a[NB][2][2], x[NB][NT][2];
+    float g[NB], u[NB], st[NB][NT];
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int j = 0; j < NB; ++j) {
+      if constexpr (FMT == FMT_E4M3) {
+        g[j] = sg[p + j];
+        u[j] = su[p + j];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) a[s][k] = load16(rw, ow[s], 128 * p + 64 * k);
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) x[t][k] = load16(rx, ox[t], 128 * p + 64 * k);
-    if constexpr (FMT == FMT_E4M3) {
-      const float g = sg[p], u = su[p];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const float s = sx[t][p];
-        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-        acc[0][t] += run_product<FMT>(a[0], x[t], zero) * (s * g);
-        acc[1][t] += run_product<FMT>(a[1], x[t], zero) * (s * u);
+        for (int t = 0; t < NT; ++t) st[j][t] = sx[t][p + j];
       }
-    } else {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) a[j][s][k] = load16(rw, ow[s], 128 * (p + j) + 64 * k);
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) acc[s][t] = run_product<FMT>(a[s], x[t], acc[s][t]);
+        for (int k = 0; k < 2; ++k) x[j][t][k] = load16(rx, ox[t], 128 * (p + j) + 64 * k);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      if constexpr (FMT == FMT_E4M3) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+          acc[0][t] += run_product<FMT>(a[j][0], x[j][t], zero) * (st[j][t] * g[j]);
+          acc[1][t] += run_product<FMT>(a[j][1], x[j][t], zero) * (st[j][t] * u[j]);
+        }
+      } else {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int s = 0; s < 2; ++s) acc[s][t] = run_product<FMT>(a[j][s], x[j][t], acc[s][t]);
+      }
     }
   }
-}
+
+  // Of n runs, an eighth each.  Four runs at a time, as far as the registers go, where a
+  // wave has more than four; the kernels' time, us: 1 token, d = 7168 (14 runs), four
+  // 158, two 162; d = 2048 (4 runs) 43.8, 41.9.  Two of 8-bit runs, which come with
+  // scales: 4 tokens, d = 7168 265, four 300.
+  __device__ __forceinline__ void all(int n) {
+    constexpr int NB = FMT == FMT_E4M3 ? 2 : 4 / NT;
+    const int w = wave_id(), per = (n + WAVES - 1) / WAVES, p1 = min(n, (w + 1) * per);
+    int p = w * per;
+    if (NB <= 2 || per > NB)
+#pragma unroll 1
+      for (; p + NB <= p1; p += NB) runs<NB>(p);
+    if constexpr (NB > 2)
+#pragma unroll 1
+      for (; p + 2 <= p1; p += 2) runs<2>(p);
+    if constexpr (NB > 1)
+      if (p < p1) runs<1>(p);
+  }
+};
 
 // Two bf16 values whose sum is v to 2^-16: its rounding, and that of what it left
 // (of v itself: not contracted with the product that v is, which only some builds do).
@@ -366,36 +448,31 @@ __device__ __forceinline__ void gateup_unit(const FewArgs& a, int e, int row0, i
   const uint32_t ld = a.d * ES;
   const uint8_t* base = static_cast<const uint8_t*>(shared ? a.ws_gate_up : a.w_gate_up) +
                         static_cast<size_t>(m) * 2 * a.inter * ld;
-  const rsrc_t rw = make_rsrc(base, 2u * a.inter * ld);
-  const rsrc_t rx = make_rsrc(FMT == FMT_E4M3 ? static_cast<const void*>(a.uq) : a.u, a.T * ld);
-  const uint32_t ow[2] = {(i0 + lr) * ld + 16 * lg, (a.inter + i0 + lr) * ld + 16 * lg};
+  GateUp<FMT, NT> q;
+  q.rw = make_rsrc(base, 2u * a.inter * ld);
+  q.rx = make_rsrc(FMT == FMT_E4M3 ? static_cast<const void*>(a.uq) : a.u, a.T * ld);
+  q.ow[0] = (i0 + lr) * ld + 16 * lg;
+  q.ow[1] = (a.inter + i0 + lr) * ld + 16 * lg;
   const int runs = a.d * ES / 128;
-  uint32_t ox[NT];
-  const float* sx[NT];
-  const float *sg = nullptr, *su = nullptr;
   if constexpr (FMT == FMT_E4M3) {
-    sg = (shared ? a.ss_gate_up : a.s_gate_up) + (static_cast<size_t>(m) * 2 * a.inter + i0) / 128 * runs;
-    su = sg + static_cast<size_t>(a.inter / 128) * runs;
+    q.sg = (shared ? a.ss_gate_up : a.s_gate_up) + (static_cast<size_t>(m) * 2 * a.inter + i0) / 128 * runs;
+    q.su = q.sg + static_cast<size_t>(a.inter / 128) * runs;
   }
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const int r = 16 * t + lr;
     const int tok = r < rows ? (shared ? r : token[row0 + r]) : a.T;
-    ox[t] = tok * ld + 16 * lg;   // past the last token: zeros
-    sx[t] = nullptr;
-    if constexpr (FMT == FMT_E4M3) sx[t] = a.us + static_cast<size_t>(min(tok, a.T - 1)) * runs;
+    q.ox[t] = tok * ld + 16 * lg;   // past the last token: zeros
+    if constexpr (FMT == FMT_E4M3) q.sx[t] = a.us + static_cast<size_t>(min(tok, a.T - 1)) * runs;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) q.acc[s][t] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  f32x4 acc[2][NT];
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) acc[s][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  gateup_sums<FMT, NT>(rw, rx, ow, ox, runs, sg, su, sx, acc);
+  q.all(runs);
   __syncthreads();   // the last unit's sums have been read
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int s = 0; s < 2; ++s) red[w * NT + t][s][lane] = acc[s][t];
+    for (int s = 0; s < 2; ++s) red[w * NT + t][s][lane] = q.acc[s][t];
   __syncthreads();
   // wave t: row 16 t + lr, columns i0 + 4 lg .. +3
   if (w >= NT || 16 * w + lr >= rows) return;
@@ -421,26 +498,33 @@ __device__ __forceinline__ void gateup_unit(const FewArgs& a, int e, int row0, i
   }
 }
 
-// NT: tiles of 16 tokens that an expert may have.
-template <int FMT, int NT>
-__global__ __launch_bounds__(THREADS, 2) void few_gateup_kernel(FewArgs a) {
+// NT: tiles of 16 tokens that an expert may have.  NQ: the block selects the experts
+// itself, 64 NQ of them at most (0: few_select_kernel has).
+template <int FMT, int NT, int NQ>
+__global__ __launch_bounds__(THREADS, 4) void few_gateup_kernel(FewArgs a) {
   __shared__ Lists L;
   __shared__ int32_t idx[16 * NT * MAX_TOPK], token[16 * NT * MAX_TOPK];
-  __shared__ float gate[16 * NT * MAX_TOPK];
+  __shared__ float gate[NQ > 0 ? WAVES * MAX_TOPK : 1];
   __shared__ union {
-    float keys[WAVES][MAX_ROUTED];
+    float keys[WAVES][64 * NQ + 1];
     f32x4 red[WAVES * NT][2][64];
   } s;
   const int w = wave_id();
-  if (!MOE_CHECK(a.T <= 16 * NT, 804)) return;
-  for (int t = w; t < a.T; t += WAVES) few_select(a, t, s.keys[w], idx + t * a.top_k, gate + t * a.top_k);
+  if (!MOE_CHECK(a.T <= (NQ > 0 ? WAVES : 16 * NT), 804)) return;
+  if constexpr (NQ > 0) {
+    if (w < a.T) few_select<NQ>(a, w, s.keys[w], idx + w * a.top_k, gate + w * a.top_k);
+  } else {
+    load_selection(a, idx);
+  }
   __syncthreads();
-  make_lists(a, L, idx, gate, token, nullptr);
+  make_lists(a, L, idx, token);
   if (blockIdx.x == 0) {
     const int TK = a.T * a.top_k;
     for (int i = threadIdx.x; i < TK; i += THREADS) {
-      a.idx[i] = idx[i];
-      a.gate[i] = gate[i];
+      if constexpr (NQ > 0) {
+        a.idx[i] = idx[i];
+        a.gate[i] = gate[i];
+      }
       if (a.perm_token != nullptr) a.perm_token[i] = token[i];
       if (a.pos != nullptr) {
         int row = L.at[idx[i]];
@@ -493,108 +577,156 @@ __global__ __launch_bounds__(256) void few_quant_kernel(FewArgs a) {
 
 // ------------------------------------------------------------------ down, gates, residual
 
+// A wave's turns over the runs of all experts, one after the other.
+struct Turn {
+  int k, p;   // entry, run
+  __device__ __forceinline__ void advance(int by, int runs, int n) {
+    p += by;
+    while (p >= runs && k < n) {
+      p -= runs;
+      ++k;
+    }
+  }
+};
+
 template <int FMT, int NT>
-__global__ __launch_bounds__(THREADS, 2) void few_down_kernel(FewArgs a) {
+__global__ __launch_bounds__(THREADS, 4) void few_down_kernel(FewArgs a) {
   constexpr int ES = FMT == FMT_F32 ? 4 : FMT == FMT_BF16 ? 2 : 1;
-  constexpr int CH = 2;   // runs in flight
+  constexpr int NB = FMT == FMT_BF16 && NT == 4 ? 3 : 4;   // runs whose loads go out together
+  // Rows of a tile: of bf16 pairs 8, whose columns 0 .. 7 are the first values and 8 ..
+  // 15 the second, so that both take one load and one product.
+  constexpr int TR = FMT == FMT_BF16 ? 8 : 16, TILES = 16 * NT / TR;
   __shared__ Lists L;
-  __shared__ int32_t idx[16 * NT * MAX_TOPK];
+  __shared__ int32_t idx[16 * NT * MAX_TOPK], token[16 * NT * MAX_TOPK];
   __shared__ float gate_row[16 * NT * MAX_TOPK];
-  __shared__ f32x4 red[WAVES][NT][64];
+  __shared__ f32x4 sums[WAVES][16 * NT][5];   // by token, 16 columns (and a gap) each
   const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int TK = a.T * a.top_k, R = TK + a.n_shared * a.T, d0 = 16 * blockIdx.x;
   if (!MOE_CHECK(a.T <= 16 * NT && d0 + 16 <= a.d, 805)) return;
-  for (int i = threadIdx.x; i < TK; i += THREADS) {
-    int e = a.idx[i];
-    if (!MOE_CHECK(e >= 0 && e < a.n_routed, 806)) e = 0;
-    idx[i] = e;
-  }
+  load_selection(a, idx);
+  for (int i = lane; i < 16 * NT * 5; i += 64) (&sums[w][0][0])[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   __syncthreads();
-  make_lists(a, L, idx, nullptr, nullptr, nullptr);
-  // the rows' gates
-  for (int k = threadIdx.x >> 6; k < L.n; k += WAVES) {
-    const unsigned long long m = L.mask[k];
-    const int e = L.expert[k];
-    if (e < a.n_routed && (m >> lane & 1)) {
-      int j = 0;
-      while (j < a.top_k - 1 && idx[lane * a.top_k + j] != e) ++j;
-      gate_row[L.row0[k] + __popcll(m & ((1ULL << lane) - 1))] = a.gate[lane * a.top_k + j];
-    }
+  make_lists(a, L, idx, token);
+  for (int i = threadIdx.x; i < TK; i += THREADS) {
+    int row = L.at[idx[i]];
+    while (token[row] != i / a.top_k) ++row;   // it is among its expert's rows
+    gate_row[row] = a.gate[i];
   }
   __syncthreads();
 
   const uint32_t ld = a.inter * ES;
-  const int runs = ld / 128;
-  const rsrc_t rh = make_rsrc(FMT == FMT_E4M3 ? static_cast<const void*>(a.hq) : a.h, static_cast<uint32_t>(R) * ld);
-  const rsrc_t rl = make_rsrc(a.h_lo, FMT == FMT_BF16 ? static_cast<uint32_t>(R) * ld : 0);
-  f32x4 acc[NT];
+  const int runs = ld / 128, n = L.n;
+  const uint32_t planes = static_cast<uint32_t>(R) * ld, end = FMT == FMT_BF16 ? 2 * planes : planes;
+  const rsrc_t rh = make_rsrc(FMT == FMT_E4M3 ? static_cast<const void*>(a.hq) : a.h, end);
+  const uint32_t ow = lr * ld + 16 * lg;
+  const int tr = lr % TR;                                        // this lane's row of a tile
+  const uint32_t plane = lr >= TR ? planes : 0;                  // and which of its values
+  auto row_at = [&](int row0, int rows, int t) {                 // past the last row: zeros
+    const int r = TR * t + tr;
+    return (r < rows ? static_cast<uint32_t>(row0 + r) * ld + plane : end) + 16 * lg;
+  };
+  f32x4 acc[TILES];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  int first = w;   // of the waves' turns over all experts' runs
-  for (int k = 0; k < L.n; ++k) {
-    const int e = __builtin_amdgcn_readfirstlane(L.expert[k]), row0 = __builtin_amdgcn_readfirstlane(L.row0[k]);
-    const unsigned long long m = L.mask[k];
-    const bool shared = e >= a.n_routed;
-    const int mat = shared ? e - a.n_routed : e;
-    const rsrc_t rw = make_rsrc(static_cast<const uint8_t*>(shared ? a.ws_down : a.w_down) +
-                                (static_cast<size_t>(mat) * a.d + d0) * ld, 16 * ld);
-    const float* sw = nullptr;
-    if constexpr (FMT == FMT_E4M3)
-      sw = (shared ? a.ss_down : a.s_down) + (static_cast<size_t>(mat) * a.d + d0) / 128 * runs;
-    int p = first;
-    for (; p < runs; p += CH * WAVES) {
-      i32x4 wf[CH][2];
+  for (int t = 0; t < TILES; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // adds the products with entry k's rows to their tokens' sums: a row that an expert
+  // does not have takes nothing from its weights, whatever they hold
+  auto flush = [&](int k, int rows) {
+    const int row0 = L.row0[k];
+    const bool shared = L.expert[k] >= a.n_routed;
 #pragma unroll
-      for (int c = 0; c < CH; ++c)
+    for (int t = 0; t < TILES; ++t) {
+      if (TR * t >= rows) continue;
+      f32x4 v = acc[t];
+      acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if constexpr (TR == 8) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) wf[c][h] = load16(rw, lr * ld + 16 * lg, 128 * (p + WAVES * c) + 64 * h);
+        for (int e = 0; e < 4; ++e)   // the second values' column stands 8 lanes on
+          v[e] += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v[e]), 0x128, 0xf, 0xf, false));
+      }
+      const int r = TR * t + lr;
+      if (lr < TR && r < rows) {
+        const float g = shared ? 1.f : gate_row[row0 + r];
+        f32x4& s = sums[w][shared ? r : token[row0 + r]][lg];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const uint32_t part = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(m >> (16 * t)) & 0xffffu);
-        if (part == 0) continue;
-        const int tok = 16 * t + lr;
-        const bool in = m >> tok & 1;
-        const int row = in ? row0 + __popcll(m & ((1ULL << tok) - 1)) : R;   // R: zeros
-        const uint32_t oh = static_cast<uint32_t>(row) * ld + 16 * lg;
-        const float g = in && !shared ? gate_row[row] : 1.f;
-        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const int q = p + WAVES * c;
-          if (c > 0 && q >= runs) continue;
-          i32x4 x[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) x[h] = load16(rh, oh, 128 * q + 64 * h);
-          if constexpr (FMT == FMT_E4M3) {
-            const float s = in ? a.hs[static_cast<size_t>(row) * runs + q] : 0.f;
-            sum += run_product<FMT>(wf[c], x, f32x4{0.f, 0.f, 0.f, 0.f}) * (s * sw[q]);
-          } else {
-            sum = run_product<FMT>(wf[c], x, sum);
-            if constexpr (FMT == FMT_BF16) {
-              i32x4 y[2];
-#pragma unroll
-              for (int h = 0; h < 2; ++h) y[h] = load16(rl, oh, 128 * q + 64 * h);
-              sum = run_product<FMT>(wf[c], y, sum);
-            }
-          }
-        }
-        // a token that does not use this expert keeps its sum, whatever the weights hold
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[t][r] = in ? fmaf(g, sum[r], acc[t][r]) : acc[t][r];
+        for (int e = 0; e < 4; ++e) s[e] = fmaf(g, v[e], s[e]);
       }
     }
-    // the first run of the next expert that is this wave's
-    first = (first + WAVES - runs % WAVES) % WAVES;
+  };
+  Turn turn{0, 0};
+  const int per = (n * runs + WAVES - 1) / WAVES;
+  turn.advance(w * per, runs, n);
+  int cur = -1, cur_rows = 0;
+  for (int left = min(per, n * runs - w * per); left > 0; left -= NB) {
+    Turn at[NB];
+    int e[NB], row0[NB], rows[NB];
+    i32x4 wf[NB][2], x[NB][2];
+    float sw[NB], sh[NB];   // e4m3: the block's scale, this lane's row's
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      at[j] = turn;
+      turn.advance(1, runs, n);
+      if (at[j].k >= n) at[j].p = 0;       // past the end: some run of the last, unused
+      const int k = min(at[j].k, n - 1);
+      e[j] = L.expert[k];
+      row0[j] = L.row0[k];
+      rows[j] = __popcll(L.mask[k]);
+    }
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      e[j] = __builtin_amdgcn_readfirstlane(e[j]);
+      row0[j] = __builtin_amdgcn_readfirstlane(row0[j]);
+      rows[j] = __builtin_amdgcn_readfirstlane(rows[j]);
+      const bool shared = e[j] >= a.n_routed;
+      const size_t mat = shared ? e[j] - a.n_routed : e[j];
+      const rsrc_t rw = make_rsrc(static_cast<const uint8_t*>(shared ? a.ws_down : a.w_down) + (mat * a.d + d0) * ld, 16 * ld);
+      const uint32_t oh = row_at(row0[j], rows[j], 0);
+      if constexpr (FMT == FMT_E4M3) {
+        sw[j] = (shared ? a.ss_down : a.s_down)[(mat * a.d + d0) / 128 * runs + at[j].p];
+        sh[j] = a.hs[static_cast<size_t>(row0[j] + min(lr, rows[j] - 1)) * runs + at[j].p];
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        wf[j][h] = load16(rw, ow, 128 * at[j].p + 64 * h);
+        x[j][h] = load16(rh, oh, 128 * at[j].p + 64 * h);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      if (j >= left) continue;
+      if (at[j].k != cur) {
+        if (cur >= 0) flush(cur, cur_rows);
+        cur = at[j].k;
+        cur_rows = rows[j];
+      }
+      auto product = [&](int t, const i32x4(&v)[2], float s) {
+        if constexpr (FMT == FMT_E4M3)
+          acc[t] += run_product<FMT>(wf[j], v, f32x4{0.f, 0.f, 0.f, 0.f}) * (s * sw[j]);
+        else
+          acc[t] = run_product<FMT>(wf[j], v, acc[t]);
+      };
+      product(0, x[j], sh[j]);
+#pragma unroll
+      for (int t = 1; t < TILES; ++t) {   // more rows than a tile's: few experts have them
+        if (rows[j] <= TR * t) continue;
+        const uint32_t oh = row_at(row0[j], rows[j], t);
+        i32x4 v[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) v[h] = load16(rh, oh, 128 * at[j].p + 64 * h);
+        float s = 0.f;
+        if constexpr (FMT == FMT_E4M3) s = a.hs[static_cast<size_t>(row0[j] + min(TR * t + lr, rows[j] - 1)) * runs + at[j].p];
+        product(t, v, s);
+      }
+    }
   }
-#pragma unroll
-  for (int t = 0; t < NT; ++t) red[w][t][lane] = acc[t];
+  if (cur >= 0) flush(cur, cur_rows);
   __syncthreads();
-  const int t = 16 * w + lr;
-  if (w >= NT || t >= a.T) return;
-  f32x4 y = red[0][w][lane];
+  // 4 lanes to a token, 4 columns each
+  const int t = threadIdx.x >> 2, g = threadIdx.x & 3;
+  if (t >= a.T) return;
+  f32x4 y = sums[0][t][g];
 #pragma unroll
-  for (int k = 1; k < WAVES; ++k) y += red[k][w][lane];
-  const size_t off = static_cast<size_t>(t) * a.d + d0 + 4 * lg;
+  for (int k = 1; k < WAVES; ++k) y += sums[k][t][g];
+  const size_t off = static_cast<size_t>(t) * a.d + d0 + 4 * g;
   float v[4];
   if (a.x_fmt == FMT_F32) {
     const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(a.u) + off);
@@ -612,6 +744,18 @@ __global__ __launch_bounds__(THREADS, 2) void few_down_kernel(FewArgs a) {
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + off) = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
 }
 
+template <class F>
+void by_experts(int n, F&& f) {   // experts in multiples of 64 to a lane
+  if (n <= 64)
+    f(std::integral_constant<int, 1>{});
+  else if (n <= 128)
+    f(std::integral_constant<int, 2>{});
+  else if (n <= 256)
+    f(std::integral_constant<int, 4>{});
+  else
+    f(std::integral_constant<int, 8>{});
+}
+
 template <int NT>
 struct Launch {
   static void route(const FewArgs& a, hipStream_t s) {
@@ -626,8 +770,19 @@ struct Launch {
   static void gateup(const FewArgs& a, hipStream_t s) {
     const int tk = a.T * a.top_k;
     const long long units = static_cast<long long>((tk < a.n_routed ? tk : a.n_routed) + a.n_shared) * (a.inter / 16);
-    hipLaunchKernelGGL((few_gateup_kernel<FMT, NT>), dim3(static_cast<unsigned>(units < 1 ? 1 : units < 2048 ? units : 2048)),
-                       dim3(THREADS), 0, s, a);
+    const dim3 grid(static_cast<unsigned>(units < 1 ? 1 : units < GATEUP_BLOCKS ? units : GATEUP_BLOCKS)), block(THREADS);
+    if constexpr (NT == 1) {
+      if (a.T <= WAVES) {
+        by_experts(a.n_routed, [&](auto nq) {
+          hipLaunchKernelGGL((few_gateup_kernel<FMT, NT, decltype(nq)::value>), grid, block, 0, s, a);
+        });
+        return;
+      }
+    }
+    by_experts(a.n_routed, [&](auto nq) {
+      hipLaunchKernelGGL(few_select_kernel<decltype(nq)::value>, dim3(ceil_div(a.T, 4)), dim3(256), 0, s, a);
+    });
+    hipLaunchKernelGGL((few_gateup_kernel<FMT, NT, 0>), grid, block, 0, s, a);
   }
   template <int FMT>
   static void down(const FewArgs& a, hipStream_t s) {

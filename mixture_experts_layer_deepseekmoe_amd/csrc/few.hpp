@@ -32,7 +32,7 @@ struct FewArgs {
   int32_t* pos;             // [T][K]
   // SwiGLU outputs by grouped row (expert-major, tokens ascending; then the shared experts'): fp32 values, or
   // their bf16 roundings (h) and what those left (h_lo)
-  void* h;                  // [R][I] f32 (f32 and e4m3 weights) or bf16
+  void* h;                  // [R][I] f32 (f32 and e4m3 weights) or bf16, and right behind it
   uint16_t* h_lo;           // [R][I] bf16
   uint8_t* hq;              // e4m3: [R][I] codes and [R][I/128] scales
   float* hs;
@@ -46,9 +46,9 @@ inline int few_runs(int cols, int fmt) { return cols * (fmt == FMT_F32 ? 4 : fmt
 
 // The router's K slices: a block takes 16 experts and a slice of K, a run of 128
 // bytes a wave at a time, so one run for each of its 8 waves at least.  Every block of
-// the next kernel reads the slices of all tokens again: 16 of them together at most.
+// the next kernel reads the slices of all tokens again: 64 of them together at most.
 inline int few_slices(int T, int d, int x_fmt) {
-  const int most = (few_runs(d, x_fmt) + 7) / 8, want = 16 / (T > 0 ? T : 1);
+  const int most = (few_runs(d, x_fmt) + 7) / 8, want = 64 / (T > 0 ? T : 1);
   const int s = want < most ? want : most;
   return s > 1 ? s : 1;
 }

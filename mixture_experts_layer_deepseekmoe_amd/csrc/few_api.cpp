@@ -17,7 +17,7 @@ int validate_few(const moe_shape* s) {
 
 // Workspace map (byte offsets, each 256-byte aligned).
 struct Layout {
-  size_t logits, idx, gate, h, h_lo, hq, hs, uq, us, total;
+  size_t logits, idx, gate, h, hq, hs, uq, us, total;
   int slices;
 };
 
@@ -25,15 +25,14 @@ Layout make_layout(const moe_shape& s) {
   Layout L{};
   const size_t T = static_cast<size_t>(s.T), K = static_cast<size_t>(s.top_k), R = T * (K + s.n_shared);
   const size_t d = static_cast<size_t>(s.d), I = static_cast<size_t>(s.inter);
-  const bool fp8 = s.w_dtype == MOE_DTYPE_E4M3, pairs = s.w_dtype == MOE_DTYPE_BF16;
+  const bool fp8 = s.w_dtype == MOE_DTYPE_E4M3;
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o += align_up(bytes); return at; };
   L.slices = moe::few_slices(s.T, s.d, fmt_of(s.x_dtype));
   L.logits = take(L.slices * T * s.n_routed * 4);
   L.idx = take(T * K * 4);
   L.gate = take(T * K * 4);
-  L.h = take(R * I * (pairs ? 2 : 4));
-  L.h_lo = take(pairs ? R * I * 2 : 0);
+  L.h = take(R * I * 4);   // fp32 values or pairs of bf16 ones
   L.hq = take(fp8 ? R * I : 0);
   L.hs = take(fp8 ? R * (I / 128) * 4 : 0);
   L.uq = take(fp8 ? T * d : 0);
@@ -99,7 +98,7 @@ int moe_forward_few(const moe_shape* shape, const void* u, const void* centroids
     a.idx = r.topk_idx != nullptr ? r.topk_idx : at<int32_t>(workspace, L.idx);
     a.gate = r.topk_gate != nullptr ? r.topk_gate : at<float>(workspace, L.gate);
     a.h = at<void>(workspace, L.h);
-    a.h_lo = at<uint16_t>(workspace, L.h_lo);
+    a.h_lo = at<uint16_t>(workspace, L.h) + static_cast<size_t>(s.T) * (s.top_k + s.n_shared) * s.inter;
     a.hq = at<uint8_t>(workspace, L.hq);
     a.hs = at<float>(workspace, L.hs);
     a.uq = at<uint8_t>(workspace, L.uq);
