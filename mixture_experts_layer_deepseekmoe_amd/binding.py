@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Dict, Optional
 
@@ -786,19 +787,28 @@ def moe_embed_backward(shape: EmbedShape, tokens: torch.Tensor, dx: torch.Tensor
     return dtable
 
 
+_TENSOR_DT = {torch.float32: F32, torch.bfloat16: BF16}
+
+
 class TensorList:
     """Tensors for moe_grad_sumsq and moe_grad_clip: contiguous fp32 or bf16 tensors
     on the current device (slices of a larger buffer among them).  It keeps them
     alive, and may be used for any number of steps."""
 
     def __init__(self, tensors):
-        self.tensors = list(tensors)
-        _same_device(*self.tensors)
-        code = {torch.float32: F32, torch.bfloat16: BF16}
-        for t in self.tensors:
-            if t.dtype not in code:
-                raise ValueError(f"expected f32 or bf16 tensors, got {t.dtype}")
-        self.c = (CTensor * max(len(self.tensors), 1))(*[(_ptr(t), t.numel(), code[t.dtype]) for t in self.tensors])
+        self.tensors = ts = list(tensors)
+        if any(t.dtype not in _TENSOR_DT for t in ts):
+            raise ValueError("expected f32 or bf16 tensors")
+        devices = {t.get_device() for t in ts}
+        if -1 in devices:
+            raise ValueError("tensors passed to the MoE library must live on the GPU")
+        if devices and devices != {torch._C._cuda_getDevice()}:
+            raise ValueError(f"tensors live on devices {sorted(devices)}, not all of them the current one")
+        if not all([t.is_contiguous() for t in ts]):
+            raise ValueError("tensors passed to the MoE library must be contiguous")
+        # packed at once: an array of ctypes structures takes five times as long
+        flat = [v for t in ts for v in (t.data_ptr(), t.numel(), _TENSOR_DT[t.dtype])]
+        self.c = ctypes.create_string_buffer(struct.pack("<" + "Qqi4x" * len(ts), *flat))
 
     def __len__(self) -> int:
         return len(self.tensors)

@@ -7,8 +7,11 @@
 // Both are bound by HBM: the rows once, and of the gradient all V rows written
 // (or, added to, the named rows alone).  For the gradient the rows are sorted by
 // token (stable: rows of a token stay in order), so a wave finds the rows of a
-// token side by side, sums them in registers, in fp32 and in a fixed order, and
-// writes each row of the table once, zeros included: no atomics, no clearing pass.
+// token side by side and sums them in registers, in fp32 and in a fixed order: no
+// atomics.  The table is cleared beside the sorting, which needs few of the CUs; the
+// named rows are then written over.  (One pass that finds each row's run by a search
+// and writes every row once took 417 us for 65536 x 7168 in fp32, where clearing takes
+// 290 and the sums 80: its waves wait for their searches, loads and stores in turn.)
 #include "ends.hpp"
 #include "gemm_core.hpp"
 #include "rows.hpp"
@@ -68,30 +71,58 @@ __device__ __forceinline__ int key_of(const EmbedBwdArgs& a, int t) {
   return tok >= 0 && tok < a.V ? tok : a.V;
 }
 
+// Clears 128 KB of the table, by 1024 threads.
+constexpr int CLEAR_THREADS = 1024;
+constexpr long long CLEAR_BYTES = 128 << 10;
+__host__ __device__ inline long long table_bytes(const EmbedBwdArgs& a) {
+  return static_cast<long long>(a.V) * a.d * (a.grad_fmt == FMT_F32 ? 4 : 2);
+}
+__device__ __forceinline__ void clear_table(const EmbedBwdArgs& a, unsigned block) {
+  const long long n = table_bytes(a);   // a multiple of 16
+#pragma unroll
+  for (int i = 0; i < CLEAR_BYTES / 16 / CLEAR_THREADS; ++i) {
+    const long long at = block * CLEAR_BYTES + 16 * (threadIdx.x + CLEAR_THREADS * i);
+    if (at < n) *reinterpret_cast<i32x4*>(static_cast<uint8_t*>(a.dtable) + at) = i32x4{0, 0, 0, 0};
+  }
+}
+__global__ __launch_bounds__(CLEAR_THREADS) void embed_clear_kernel(EmbedBwdArgs a) {
+  if (!MOE_CHECK(blockIdx.x * CLEAR_BYTES < table_bytes(a), 905)) return;
+  clear_table(a, blockIdx.x);
+}
+
 // A row's place is the number of rows before it: those of a lower token, and earlier
-// ones of its own.  A block ranks 32 rows; its threads hold 8 keys each at a time.
+// ones of its own, both in one comparison of (token, row) as a number of 32 bits where
+// these suffice (U).  A block ranks 32 rows; its threads hold 8 keys each at a time.
 constexpr int RANK_ROWS = 32, RANK_KEYS = 8, RANK_THREADS = 1024;
-__global__ __launch_bounds__(RANK_THREADS) void embed_rank_kernel(EmbedBwdArgs a) {
+template <class U>
+__global__ __launch_bounds__(RANK_THREADS) void embed_rank_kernel(EmbedBwdArgs a, int row_bits, int blocks) {
   __shared__ int cnt[RANK_THREADS / 64][RANK_ROWS];
+  if (static_cast<int>(blockIdx.x) >= blocks) return clear_table(a, blockIdx.x - blocks);
   const int w = wave_id(), lane = threadIdx.x & 63, t0 = blockIdx.x * RANK_ROWS;
   const int rows = min(RANK_ROWS, a.T - t0);
-  const int mine = key_of(a, t0 + min(lane & (RANK_ROWS - 1), rows - 1));   // lane r: row t0 + r
-  int n = 0;                                                              // lane r: rows before it
+  const int row = t0 + min(lane & (RANK_ROWS - 1), rows - 1);   // lane r: row t0 + r
+  const int id = key_of(a, row);
+  const U mine = static_cast<U>(id) << row_bits | static_cast<U>(row);
+  int n = 0;                                                    // lane r: rows before it
   for (int k0 = 0; k0 < a.T; k0 += RANK_KEYS * RANK_THREADS) {
-    int key[RANK_KEYS];
+    U key[RANK_KEYS];
 #pragma unroll
     for (int j = 0; j < RANK_KEYS; ++j) {
       const int p = k0 + j * RANK_THREADS + static_cast<int>(threadIdx.x);
-      key[j] = p < a.T ? key_of(a, p) : 0x7fffffff;
+      key[j] = p < a.T ? static_cast<U>(key_of(a, p)) << row_bits | static_cast<U>(p) : ~U{0};
     }
+    const int held = min(RANK_KEYS, ceil_div(a.T - k0, RANK_THREADS));
     for (int r = 0; r < rows; ++r) {
-      const int k = __builtin_amdgcn_readlane(mine, r), t = t0 + r;
+      U k;
+      if constexpr (sizeof(U) == 4)
+        k = static_cast<U>(__builtin_amdgcn_readlane(mine, r));
+      else
+        k = static_cast<U>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(mine >> 32), r))) << 32 |
+            static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(mine), r));
       int c = 0;
 #pragma unroll
-      for (int j = 0; j < RANK_KEYS; ++j) {
-        const int p = k0 + j * RANK_THREADS + static_cast<int>(threadIdx.x);
-        c += __popcll(__ballot(key[j] < k + (p < t)));
-      }
+      for (int j = 0; j < RANK_KEYS; ++j)
+        if (j < held) c += __popcll(__ballot(key[j] < k));
       if (lane == r) n += c;
     }
   }
@@ -102,8 +133,8 @@ __global__ __launch_bounds__(RANK_THREADS) void embed_rank_kernel(EmbedBwdArgs a
 #pragma unroll
   for (int k = 0; k < RANK_THREADS / 64; ++k) at += cnt[k][threadIdx.x];
   if (!MOE_CHECK(at >= 0 && at < a.T, 902)) return;
-  a.ids[at] = mine;
-  a.order[at] = t0 + threadIdx.x;
+  a.ids[at] = id;
+  a.order[at] = row;
 }
 
 // Radix sort, 8 bits a pass, stable.  A block takes 4096 rows, each of its 4 waves a
@@ -201,60 +232,82 @@ __global__ __launch_bounds__(RADIX_THREADS) void embed_scatter_kernel(RadixArgs 
 
 // ------------------------------------------------------------------ sums
 
-constexpr int SLAB = 1024;   // columns of a wave: 4 times 4 to a lane
-constexpr int SUM_THREADS = 256;
+constexpr int SUM_THREADS = 256, SUM_WAVES = SUM_THREADS / 64;
 
+// A wave's number in a grid of one or (past 2^31 threads) two dimensions.
+__device__ __forceinline__ int sum_wave() {
+  return static_cast<int>((blockIdx.y * gridDim.x + blockIdx.x) * SUM_WAVES + wave_id());
+}
+inline dim3 sum_grid(long long waves) {
+  constexpr long long WIDTH = 1 << 23;
+  const long long blocks = (waves + SUM_WAVES - 1) / SUM_WAVES;
+  if (blocks <= WIDTH) return dim3(static_cast<unsigned>(blocks));
+  return dim3(WIDTH, static_cast<unsigned>((blocks + WIDTH - 1) / WIDTH));
+}
+
+// A wave's sums of 256 V columns, V times four to a lane: pairs of fours side by side
+// for rows of bf16 (16 bytes a store).
+template <int GF, int V>
 struct Slab {
-  float4 v[SLAB / 256];
-};
-__device__ __forceinline__ void zero(Slab& s) {
+  float4 v[V];
+  int c0, d;
+  __device__ __forceinline__ Slab(int c0_, int d_) : c0(c0_), d(d_) {
 #pragma unroll
-  for (int i = 0; i < SLAB / 256; ++i) s.v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-}
-// Adds columns c0 .. of n rows of src, rows at[0], at[1], ... (null: 0, 1, ...), in
-// order; N rows' loads go out together.
-template <int N>
-__device__ __forceinline__ void add_n(Slab& s, const float* src, const int32_t* at, int r0, int d, int c) {
-  float4 v[N][SLAB / 256];
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const size_t row = static_cast<size_t>(at != nullptr ? __builtin_amdgcn_readfirstlane(at[r0 + j]) : r0 + j);
-    const float* p = src + row * d;
-#pragma unroll
-    for (int i = 0; i < SLAB / 256; ++i)
-      if (c + 256 * i < d) v[j][i] = *reinterpret_cast<const float4*>(p + c + 256 * i);
+    for (int i = 0; i < V; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
+  __device__ __forceinline__ int col(int i) const {
+    const int lane = threadIdx.x & 63;
+    return c0 + (GF == FMT_BF16 ? 8 * lane + 512 * (i / 2) + 4 * (i % 2) : 4 * lane + 256 * i);
+  }
+  __device__ __forceinline__ bool in(int i) const { return col(i) < d; }
+  // Adds n rows of src, in order: rows 0, 1, ..., or those that lanes 0, 1, ... of `at`
+  // name.  N rows' loads go out together.
+  template <int N, bool AT>
+  __device__ __forceinline__ void add(const float* src, int at, int n) {
+#pragma unroll 1
+    for (int r = 0; r < n; r += N) {
+      float4 x[N][V];
 #pragma unroll
-  for (int j = 0; j < N; ++j)
+      for (int j = 0; j < N; ++j) {
+        if (r + j >= n) continue;
+        const size_t row = static_cast<size_t>(AT ? __builtin_amdgcn_readlane(at, r + j) : r + j);
 #pragma unroll
-    for (int i = 0; i < SLAB / 256; ++i) {
-      if (c + 256 * i >= d) continue;
-      s.v[i].x += v[j][i].x;
-      s.v[i].y += v[j][i].y;
-      s.v[i].z += v[j][i].z;
-      s.v[i].w += v[j][i].w;
+        for (int i = 0; i < V; ++i)
+          if (in(i)) x[j][i] = *reinterpret_cast<const float4*>(src + row * d + col(i));
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        if (r + j >= n) continue;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          if (!in(i)) continue;
+          v[i].x += x[j][i].x;
+          v[i].y += x[j][i].y;
+          v[i].z += x[j][i].z;
+          v[i].w += x[j][i].w;
+        }
+      }
     }
-}
-__device__ __forceinline__ void add_rows(Slab& s, const float* src, const int32_t* at, int n, int d, int c0) {
-  const int c = c0 + 4 * (threadIdx.x & 63);
-  int r = 0;
-  for (; r + 4 <= n; r += 4) add_n<4>(s, src, at, r, d, c);
-  for (; r < n; ++r) add_n<1>(s, src, at, r, d, c);
-}
+  }
+};
 
-// The sums of chunks that hold one token throughout.
+// The sums of chunks that hold one token throughout (LEVEL 2: of the chunks' chunks), 16
+// rows at once.
+template <int LEVEL>
 __global__ __launch_bounds__(SUM_THREADS) void embed_chunk_kernel(EmbedBwdArgs a) {
-  const int chunk = blockIdx.x * (SUM_THREADS / 64) + wave_id(), c0 = blockIdx.y * SLAB;
-  if (chunk >= a.T / EMBED_CHUNK) return;
-  const int r0 = chunk * EMBED_CHUNK, id = a.ids[r0];
-  if (id >= a.V || a.ids[r0 + EMBED_CHUNK - 1] != id) return;
-  Slab s;
-  zero(s);
-  add_rows(s, a.dx, a.order + r0, EMBED_CHUNK, a.d, c0);
-  const int c = c0 + 4 * (threadIdx.x & 63);
-#pragma unroll
-  for (int i = 0; i < SLAB / 256; ++i)
-    if (c + 256 * i < a.d) *reinterpret_cast<float4*>(a.part + static_cast<size_t>(chunk) * a.d + c + 256 * i) = s.v[i];
+  constexpr int C = LEVEL == 1 ? EMBED_CHUNK : EMBED_CHUNK2, N = LEVEL == 1 ? C : C / EMBED_CHUNK;
+  const int slabs = ceil_div(a.d, 256), wave = sum_wave(), lane = threadIdx.x & 63;
+  const int chunk = wave / slabs;   // waves side by side read a row's columns in order
+  if (chunk >= a.T / C) return;
+  const int r0 = chunk * C, id = a.ids[r0], last = a.ids[r0 + C - 1], at = LEVEL == 1 ? a.order[r0 + lane % C] : 0;
+  if (id >= a.V || last != id || !MOE_CHECK(at >= 0 && at < a.T, 907)) return;
+  Slab<FMT_F32, 1> s(wave % slabs * 256, a.d);
+  if constexpr (LEVEL == 1)
+    s.add<N, true>(a.dx, at, N);
+  else
+    s.add<N, false>(a.part + static_cast<size_t>(chunk) * N * a.d, 0, N);
+  if (s.in(0))
+    *reinterpret_cast<float4*>((LEVEL == 1 ? a.part : a.part2) + static_cast<size_t>(chunk) * a.d + s.col(0)) = s.v[0];
 }
 
 // The first sorted row at or past `lo` whose token is at least v (a wave: 64 probes a
@@ -274,88 +327,88 @@ __device__ __forceinline__ int lower_bound(const int32_t* ids, int lo, int hi, i
   return lo;
 }
 
-// Writes row v of the gradient from sorted rows r0 .. r1 - 1 (none: zeros).
-template <int GF>
-__device__ __forceinline__ void write_row(const EmbedBwdArgs& a, int v, int r0, int r1, int c0) {
-  Slab s;
-  zero(s);
-  if (r0 < r1) {
-    // whole chunks have been summed: the rows before the first, the chunks, the rows behind the last
-    const int k0 = (r0 + EMBED_CHUNK - 1) / EMBED_CHUNK, k1 = r1 / EMBED_CHUNK;
-    if (k0 < k1) {
-      add_rows(s, a.dx, a.order + r0, k0 * EMBED_CHUNK - r0, a.d, c0);
-      add_rows(s, a.part + static_cast<size_t>(k0) * a.d, nullptr, k1 - k0, a.d, c0);
-      add_rows(s, a.dx, a.order + k1 * EMBED_CHUNK, r1 - k1 * EMBED_CHUNK, a.d, c0);
-    } else {
-      add_rows(s, a.dx, a.order + r0, r1 - r0, a.d, c0);
-    }
+// Adds sorted rows r0 .. r1 - 1, all of one token, of which lanes hold the first 64 in
+// `at`: whole chunks by their sums.  A long run is at most five stretches one after the
+// other: rows, chunks, chunks' chunks, chunks, rows.
+constexpr int SUM_ROWS = 4;   // in flight (8: 485 us instead of 474, 65536 x 7168)
+template <class S>
+__device__ __forceinline__ void add_run(S& s, const EmbedBwdArgs& a, int r0, int r1, int at) {
+  if (r1 - r0 < EMBED_CHUNK) {
+    s.template add<SUM_ROWS, true>(a.dx, at, r1 - r0);
+    return;
   }
-  const int c = c0 + 4 * (threadIdx.x & 63);
+  auto up = [](int r, int c) { return (r + c - 1) / c * c; };
+  const int lane = threadIdx.x & 63;
+#pragma unroll 1
+  for (int step = 0; step <= 4 && r0 < r1; ++step) {
+    const int size = step == 2 ? EMBED_CHUNK2 : step % 4 != 0 ? EMBED_CHUNK : 1;
+    if (size == EMBED_CHUNK2 && a.part2 == nullptr) continue;
+    // to where the next stretch's chunks begin, or as far as this one's go
+    const int to = step == 0 ? up(r0, EMBED_CHUNK) : step == 1 && a.part2 != nullptr ? up(r0, EMBED_CHUNK2) : r1;
+    const int n = (min(to, r1) - r0) / size;
+    if (size == 1) {   // fewer than a chunk
+      if (step == 4) at = a.order[min(r0 + lane, a.T - 1)];
+      s.template add<SUM_ROWS, true>(a.dx, at, n);
+    } else {
+      s.template add<SUM_ROWS, false>((size == EMBED_CHUNK ? a.part : a.part2) + static_cast<size_t>(r0 / size) * a.d, 0, n);
+    }
+    r0 += n * size;
+  }
+}
+
+// The named rows of the gradient: the wave of a token's first sorted row sums them.
+constexpr int SUM_COLS = 512;
+template <int GF>
+__global__ __launch_bounds__(SUM_THREADS) void embed_grad_kernel(EmbedBwdArgs a) {
+  const int slabs = ceil_div(a.d, SUM_COLS), wave = sum_wave(), lane = threadIdx.x & 63;
+  const int r = wave / slabs, held = min(r + lane, a.T - 1);
+  if (r >= a.T) return;
+  const int before = r > 0 ? a.ids[r - 1] : -1, at = a.order[held];
+  int id = a.ids[held];
+  if (r + lane >= a.T) id = a.V;
+  const int v = __builtin_amdgcn_readfirstlane(id);
+  if (v >= a.V || __builtin_amdgcn_readfirstlane(before) == v) return;
+  if (!MOE_CHECK(v >= 0 && at >= 0 && at < a.T, 906)) return;
+  int r1 = r + __popcll(__ballot(id == v));
+  if (r1 == r + 64) r1 = lower_bound(a.ids, r1, a.T, v + 1);   // it may go on behind the rows held
+  constexpr int V = SUM_COLS / 256;
+  Slab<GF, V> s(wave % slabs * SUM_COLS, a.d);
+  add_run(s, a, r, r1, at);
+  const size_t off = static_cast<size_t>(v) * a.d;
+  float x[V][4];
 #pragma unroll
-  for (int i = 0; i < SLAB / 256; ++i) {
-    if (c + 256 * i >= a.d) continue;
-    const size_t off = static_cast<size_t>(v) * a.d + c + 256 * i;
-    float4 x = s.v[i];
-    x.x *= a.scale; x.y *= a.scale; x.z *= a.scale; x.w *= a.scale;
-    if constexpr (GF == FMT_F32) {
-      float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.dtable) + off);
+  for (int i = 0; i < V; ++i) {
+    x[i][0] = s.v[i].x * a.scale;
+    x[i][1] = s.v[i].y * a.scale;
+    x[i][2] = s.v[i].z * a.scale;
+    x[i][3] = s.v[i].w * a.scale;
+  }
+  if constexpr (GF == FMT_F32) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (!s.in(i)) continue;
+      float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.dtable) + off + s.col(i));
       if (a.accumulate) {
         const float4 o = *p;
-        x.x += o.x; x.y += o.y; x.z += o.z; x.w += o.w;
+        x[i][0] += o.x; x[i][1] += o.y; x[i][2] += o.z; x[i][3] += o.w;
       }
-      *p = x;
-    } else {
-      uint2* p = reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dtable) + off);
+      *p = make_float4(x[i][0], x[i][1], x[i][2], x[i][3]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      if (!s.in(i)) continue;   // d is a multiple of 8: both or none
+      uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dtable) + off + s.col(i));
       if (a.accumulate) {
-        const uint2 o = *p;
-        x.x += __uint_as_float(o.x << 16); x.y += __uint_as_float(o.x & 0xffff0000u);
-        x.z += __uint_as_float(o.y << 16); x.w += __uint_as_float(o.y & 0xffff0000u);
+        const uint4 o = *p;
+        const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[i + e / 4][e % 4] += __uint_as_float(e % 2 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
       }
-      *p = make_uint2(bf16x2(x.x, x.y), bf16x2(x.z, x.w));
+      *p = make_uint4(bf16x2(x[i][0], x[i][1]), bf16x2(x[i][2], x[i][3]), bf16x2(x[i + 1][0], x[i + 1][1]),
+                      bf16x2(x[i + 1][2], x[i + 1][3]));
     }
   }
-}
-
-// Every row of the table: a wave takes `rows` of them in turn, and the rows of each
-// from the 64 sorted tokens it holds.
-template <int GF>
-__global__ __launch_bounds__(SUM_THREADS) void embed_grad_kernel(EmbedBwdArgs a, int rows) {
-  const long long v0 = (static_cast<long long>(blockIdx.x) * (SUM_THREADS / 64) + wave_id()) * rows;
-  const int v1 = static_cast<int>(min(static_cast<long long>(a.V), v0 + rows)), c0 = blockIdx.y * SLAB;
-  const int lane = threadIdx.x & 63;
-  if (v0 >= a.V || !MOE_CHECK(c0 < a.d, 905)) return;
-  int r = lower_bound(a.ids, 0, a.T, static_cast<int>(v0));
-  int base = r, id = r + lane < a.T ? a.ids[r + lane] : a.V;
-  for (int v = static_cast<int>(v0); v < v1; ++v) {
-    // r is the first row of a token >= v, and base <= r <= base + 64
-    if (r == base + 64) {
-      base = r;
-      id = r + lane < a.T ? a.ids[r + lane] : a.V;
-    }
-    int r1 = r + __popcll(__ballot(id == v));
-    if (r1 == base + 64) {   // it may go on behind the tokens held
-      r1 = lower_bound(a.ids, r1, a.T, v + 1);
-      if (r1 > base + 64) {
-        write_row<GF>(a, v, r, r1, c0);
-        r = base = r1;
-        id = r + lane < a.T ? a.ids[r + lane] : a.V;
-        continue;
-      }
-    }
-    write_row<GF>(a, v, r, r1, c0);
-    r = r1;
-  }
-}
-
-// The named rows alone: the wave of a token's first sorted row takes them.
-template <int GF>
-__global__ __launch_bounds__(SUM_THREADS) void embed_grad_add_kernel(EmbedBwdArgs a) {
-  const int r = blockIdx.x * (SUM_THREADS / 64) + wave_id();
-  if (r >= a.T) return;
-  const int v = __builtin_amdgcn_readfirstlane(a.ids[r]);
-  if (v >= a.V || (r > 0 && __builtin_amdgcn_readfirstlane(a.ids[r - 1]) == v)) return;
-  if (!MOE_CHECK(v >= 0, 906)) return;
-  write_row<GF>(a, v, r, lower_bound(a.ids, r, a.T, v + 1), blockIdx.y * SLAB);
 }
 
 }  // namespace
@@ -377,7 +430,10 @@ hipError_t launch_embed(const EmbedArgs& a, hipStream_t s) {
 
 hipError_t launch_embed_bwd(const EmbedBwdArgs& args, hipStream_t s) {
   EmbedBwdArgs a = args;
-  if (a.T > EMBED_RANK_T) {
+  const int clear = a.accumulate ? 0 : static_cast<int>((table_bytes(a) + CLEAR_BYTES - 1) / CLEAR_BYTES);
+  if (a.T == 0 || a.T > EMBED_RANK_T) {
+    if (clear > 0) hipLaunchKernelGGL(embed_clear_kernel, dim3(clear), dim3(CLEAR_THREADS), 0, s, a);
+    if (a.T == 0) return hipGetLastError();
     RadixArgs r{};
     r.e = a;
     r.blocks = embed_radix_blocks(a.T);
@@ -393,28 +449,31 @@ hipError_t launch_embed_bwd(const EmbedBwdArgs& args, hipStream_t s) {
     }
     a.ids = r.ids_out;
     a.order = r.order_out;
-  } else if (a.T > 0) {
-    hipLaunchKernelGGL(embed_rank_kernel, dim3(ceil_div(a.T, RANK_ROWS)), dim3(RANK_THREADS), 0, s, a);
-  }
-  constexpr int W = SUM_THREADS / 64;
-  const int slabs = ceil_div(a.d, SLAB);
-  if (a.T >= EMBED_CHUNK)
-    hipLaunchKernelGGL(embed_chunk_kernel, dim3(ceil_div(a.T / EMBED_CHUNK, W), slabs), dim3(SUM_THREADS), 0, s, a);
-  if (a.accumulate) {
-    const dim3 grid(ceil_div(a.T, W), slabs);
-    if (a.T == 0) return hipGetLastError();
-    if (a.grad_fmt == FMT_F32)
-      hipLaunchKernelGGL(embed_grad_add_kernel<FMT_F32>, grid, dim3(SUM_THREADS), 0, s, a);
+  } else {
+    int row_bits = 0;
+    while (a.T - 1 >> row_bits) ++row_bits;
+    // (V, T - 1) is the largest, and all ones stand for no row
+    const bool narrow = (static_cast<unsigned long long>(a.V) + 1) << row_bits <= 0xffffffffULL;
+    const int blocks = ceil_div(a.T, RANK_ROWS);
+    const dim3 grid(blocks + clear), block(RANK_THREADS);
+    if (narrow)
+      hipLaunchKernelGGL(embed_rank_kernel<uint32_t>, grid, block, 0, s, a, row_bits, blocks);
     else
-      hipLaunchKernelGGL(embed_grad_add_kernel<FMT_BF16>, grid, dim3(SUM_THREADS), 0, s, a);
-    return hipGetLastError();
+      hipLaunchKernelGGL(embed_rank_kernel<uint64_t>, grid, block, 0, s, a, row_bits, blocks);
   }
-  const int rows = 4;
-  const dim3 grid(ceil_div(ceil_div(a.V, rows), W), slabs);
+  if (a.T < EMBED_PART2_T) a.part2 = nullptr;
+  // rows times slabs: below 2^22 x 64 waves to a launch
+  const dim3 block(SUM_THREADS);
+  const int slabs = ceil_div(a.d, 256);
+  if (a.T >= EMBED_CHUNK)
+    hipLaunchKernelGGL(embed_chunk_kernel<1>, sum_grid(static_cast<long long>(a.T / EMBED_CHUNK) * slabs), block, 0, s, a);
+  if (a.part2 != nullptr)
+    hipLaunchKernelGGL(embed_chunk_kernel<2>, sum_grid(static_cast<long long>(a.T / EMBED_CHUNK2) * slabs), block, 0, s, a);
+  const dim3 grid = sum_grid(static_cast<long long>(a.T) * ceil_div(a.d, SUM_COLS));
   if (a.grad_fmt == FMT_F32)
-    hipLaunchKernelGGL(embed_grad_kernel<FMT_F32>, grid, dim3(SUM_THREADS), 0, s, a, rows);
+    hipLaunchKernelGGL(embed_grad_kernel<FMT_F32>, grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL(embed_grad_kernel<FMT_BF16>, grid, dim3(SUM_THREADS), 0, s, a, rows);
+    hipLaunchKernelGGL(embed_grad_kernel<FMT_BF16>, grid, block, 0, s, a);
   return hipGetLastError();
 }
 

@@ -20,11 +20,10 @@ struct EmbedArgs {
   float* scales;
 };
 
-// Sorted rows are taken in chunks of EMBED_CHUNK; the sum of a chunk that holds one
-// token throughout is formed apart (embed_chunk_kernel), so that a token of many
-// rows is summed by many waves: with chunks of 32 rows the longest sum of one wave is 62
-// rows and a row for every 32 more.
-constexpr int EMBED_CHUNK = 32;
+// A token of many rows is summed by many waves: the sums of 16 sorted rows that are all
+// of one token are formed apart, and of batches of some size those of 256 from them, so
+// that the longest sum of one wave is 30 rows, 30 sums of 16 and one of 256 for every 256.
+constexpr int EMBED_CHUNK = 16, EMBED_CHUNK2 = 256, EMBED_PART2_T = 8192;
 constexpr int EMBED_RADIX_BLOCK = 4096;   // rows of a radix block
 // Rows are ranked by comparing each with all others up to this many (one launch, T^2
 // compares), by a radix sort beyond (three launches for every 8 bits of V).
@@ -41,6 +40,7 @@ struct EmbedBwdArgs {
   int32_t* order2;
   int32_t* hist;          // radix: [256][blocks]
   float* part;            // [T / EMBED_CHUNK][d]
+  float* part2;           // [T / EMBED_CHUNK2][d] (T at least EMBED_PART2_T)
   void* dtable;           // [V][d] grad_fmt
 };
 inline int embed_radix_blocks(int T) { return T > EMBED_RANK_T ? ceil_div(T, EMBED_RADIX_BLOCK) : 0; }
@@ -53,8 +53,8 @@ hipError_t launch_embed_bwd(const EmbedBwdArgs& a, hipStream_t s);
 
 // The gradients' tensors, as many as a launch's arguments hold.
 constexpr int GRAD_TENSORS = 112;
-constexpr int GRAD_CHUNK = 8192;    // elements of a block's turn
-constexpr int GRAD_BLOCKS = 2048;   // blocks of a launch: partial sums each
+constexpr int GRAD_CHUNK = 4096;    // elements of a block's turn
+constexpr int GRAD_BLOCKS = 4096;   // blocks of a sum's launch: a partial sum each
 struct GradArgs {
   const void* data[GRAD_TENSORS];
   void* out[GRAD_TENSORS];          // clipping only

@@ -30,7 +30,7 @@ bool tokens_ok(const moe_embed_shape& s, const int32_t* p) { return s.T == 0 || 
 
 // Workspace map of the backward (byte offsets, each 256-byte aligned).
 struct Layout {
-  size_t ids, order, ids2, order2, hist, part, total;
+  size_t ids, order, ids2, order2, hist, part, part2, total;
 };
 Layout make_layout(const moe_embed_shape& s) {
   Layout L{};
@@ -43,13 +43,14 @@ Layout make_layout(const moe_embed_shape& s) {
   L.order2 = take(blocks > 0 ? T * 4 : 0);
   L.hist = take(blocks * 256 * 4);
   L.part = take(T / moe::EMBED_CHUNK * s.d * 4);
+  L.part2 = take(T >= moe::EMBED_PART2_T ? T / moe::EMBED_CHUNK2 * s.d * 4 : 0);
   L.total = o;
   return L;
 }
 
 // ---- gradient tensors
 
-constexpr long long kMaxElements = 1LL << 44;   // of all tensors: their chunks are counted in 32 bits
+constexpr long long kMaxElements = 1LL << 43;   // of all tensors: their chunks are counted in 32 bits
 
 int tensor_ok(const moe_tensor& t) {
   if (t.numel < 0 || (t.dtype != MOE_DTYPE_F32 && t.dtype != MOE_DTYPE_BF16)) return MOE_ERR_INVALID_ARG;
@@ -174,6 +175,7 @@ int moe_embed_backward(const moe_embed_shape* shape, const int32_t* tokens, cons
     a.order2 = at<int32_t>(workspace, L.order2);
     a.hist = at<int32_t>(workspace, L.hist);
     a.part = at<float>(workspace, L.part);
+    a.part2 = at<float>(workspace, L.part2);
   }
   return debug_status(check_launch(moe::launch_embed_bwd(a, stream)), stream, "moe_embed_backward");
 }
