@@ -102,7 +102,7 @@ __device__ __forceinline__ void few_select(const FewArgs& a, int t, float* keys,
     s[q] = 0.f;
     b[q] = lane + 64 * q < N ? a.bias[lane + 64 * q] : 0.f;
   }
-  constexpr int NS = 16 / NQ;   // slices whose loads go out together
+  constexpr int NS = NQ <= 4 ? 16 : 8;   // slices whose loads go out together
   for (int k = 0; k < a.slices; k += NS) {
     float z[NS][NQ];
 #pragma unroll
@@ -598,19 +598,20 @@ __global__ __launch_bounds__(THREADS, 4) void few_down_kernel(FewArgs a) {
   constexpr int TR = FMT == FMT_BF16 ? 8 : 16, TILES = 16 * NT / TR;
   __shared__ Lists L;
   __shared__ int32_t idx[16 * NT * MAX_TOPK], token[16 * NT * MAX_TOPK];
-  __shared__ float gate_row[16 * NT * MAX_TOPK];
+  __shared__ float gate[16 * NT * MAX_TOPK], gate_row[16 * NT * MAX_TOPK];
   __shared__ f32x4 sums[WAVES][16 * NT][5];   // by token, 16 columns (and a gap) each
   const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int TK = a.T * a.top_k, R = TK + a.n_shared * a.T, d0 = 16 * blockIdx.x;
   if (!MOE_CHECK(a.T <= 16 * NT && d0 + 16 <= a.d, 805)) return;
   load_selection(a, idx);
+  for (int i = threadIdx.x; i < TK; i += THREADS) gate[i] = a.gate[i];
   for (int i = lane; i < 16 * NT * 5; i += 64) (&sums[w][0][0])[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   __syncthreads();
   make_lists(a, L, idx, token);
   for (int i = threadIdx.x; i < TK; i += THREADS) {
     int row = L.at[idx[i]];
     while (token[row] != i / a.top_k) ++row;   // it is among its expert's rows
-    gate_row[row] = a.gate[i];
+    gate_row[row] = gate[i];
   }
   __syncthreads();
 
