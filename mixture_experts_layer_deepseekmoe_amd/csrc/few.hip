@@ -18,7 +18,9 @@
 //   few_gateup_kernel  (expert, 16 columns of I) units
 //   few_quant_kernel   8-bit weights: h's 1x128 codes
 //   few_down_kernel    16 columns of y to a block, over all experts in turn: the
-//                      gated sum and the residual stay in registers, in a fixed order
+//                      gated sum and the residual stay on chip, in a fixed order.  Where
+//                      that leaves CUs idle, blocks share the experts' runs, and
+//   few_sum_kernel     adds their sums
 //
 // Sums are fp32.  With bf16 weights the operand h is a pair of bf16 values, what
 // the first rounds off in the second (2^-16 is left): the MFMAs wait for HBM
@@ -589,10 +591,29 @@ struct Turn {
   }
 };
 
+// y = u + sums, four columns at offset off.
+__device__ __forceinline__ void store_y(const FewArgs& a, size_t off, const f32x4& y) {
+  float v[4];
+  if (a.x_fmt == FMT_F32) {
+    const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(a.u) + off);
+    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.u) + off);
+    v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
+    v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) v[r] += y[r];
+  if (a.out_fmt == FMT_F32)
+    *reinterpret_cast<float4*>(static_cast<float*>(a.y) + off) = make_float4(v[0], v[1], v[2], v[3]);
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + off) = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+}
+
 template <int FMT, int NT>
 __global__ __launch_bounds__(THREADS, 4) void few_down_kernel(FewArgs a) {
   constexpr int ES = FMT == FMT_F32 ? 4 : FMT == FMT_BF16 ? 2 : 1;
-  constexpr int NB = FMT == FMT_BF16 && NT == 4 ? 3 : 4;   // runs whose loads go out together
+  constexpr int NB = NT == 4 ? 2 : 4;   // runs whose loads go out together
   // Rows of a tile: of bf16 pairs 8, whose columns 0 .. 7 are the first values and 8 ..
   // 15 the second, so that both take one load and one product.
   constexpr int TR = FMT == FMT_BF16 ? 8 : 16, TILES = 16 * NT / TR;
@@ -602,7 +623,7 @@ __global__ __launch_bounds__(THREADS, 4) void few_down_kernel(FewArgs a) {
   __shared__ f32x4 sums[WAVES][16 * NT][5];   // by token, 16 columns (and a gap) each
   const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const int TK = a.T * a.top_k, R = TK + a.n_shared * a.T, d0 = 16 * blockIdx.x;
-  if (!MOE_CHECK(a.T <= 16 * NT && d0 + 16 <= a.d, 805)) return;
+  if (!MOE_CHECK(a.T <= 16 * NT && d0 + 16 <= a.d && gridDim.y == static_cast<unsigned>(a.splits), 805)) return;
   load_selection(a, idx);
   for (int i = threadIdx.x; i < TK; i += THREADS) gate[i] = a.gate[i];
   for (int i = lane; i < 16 * NT * 5; i += 64) (&sums[w][0][0])[i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -653,69 +674,80 @@ __global__ __launch_bounds__(THREADS, 4) void few_down_kernel(FewArgs a) {
       }
     }
   };
-  Turn turn{0, 0};
-  const int per = (n * runs + WAVES - 1) / WAVES;
-  turn.advance(w * per, runs, n);
   int cur = -1, cur_rows = 0;
-  for (int left = min(per, n * runs - w * per); left > 0; left -= NB) {
-    Turn at[NB];
-    int e[NB], row0[NB], rows[NB];
-    i32x4 wf[NB][2], x[NB][2];
-    float sw[NB], sh[NB];   // e4m3: the block's scale, this lane's row's
+  // a share of the routed experts' runs, then of the shared ones', whose rows are all tokens
+  const int split = blockIdx.y * WAVES + w, splits = gridDim.y * WAVES, routed = n - (a.T > 0 ? a.n_shared : 0);
+  for (int phase = 0; phase < 2; ++phase) {
+    const int k0 = phase == 0 ? 0 : routed, total = (phase == 0 ? routed : a.n_shared) * runs;
+    const int per = (total + splits - 1) / splits;
+    Turn turn{k0, 0};
+    turn.advance(split * per, runs, n);
+    for (int left = min(per, total - split * per); left > 0; left -= NB) {
+      Turn at[NB];
+      int e[NB], row0[NB], rows[NB];
+      i32x4 wf[NB][2], x[NB][2];
+      float sw[NB], sh[NB];   // e4m3: the block's scale, this lane's row's
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      at[j] = turn;
-      turn.advance(1, runs, n);
-      if (at[j].k >= n) at[j].p = 0;       // past the end: some run of the last, unused
-      const int k = min(at[j].k, n - 1);
-      e[j] = L.expert[k];
-      row0[j] = L.row0[k];
-      rows[j] = __popcll(L.mask[k]);
-    }
-#pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      e[j] = __builtin_amdgcn_readfirstlane(e[j]);
-      row0[j] = __builtin_amdgcn_readfirstlane(row0[j]);
-      rows[j] = __builtin_amdgcn_readfirstlane(rows[j]);
-      const bool shared = e[j] >= a.n_routed;
-      const size_t mat = shared ? e[j] - a.n_routed : e[j];
-      const rsrc_t rw = make_rsrc(static_cast<const uint8_t*>(shared ? a.ws_down : a.w_down) + (mat * a.d + d0) * ld, 16 * ld);
-      const uint32_t oh = row_at(row0[j], rows[j], 0);
-      if constexpr (FMT == FMT_E4M3) {
-        sw[j] = (shared ? a.ss_down : a.s_down)[(mat * a.d + d0) / 128 * runs + at[j].p];
-        sh[j] = a.hs[static_cast<size_t>(row0[j] + min(lr, rows[j] - 1)) * runs + at[j].p];
+      for (int j = 0; j < NB; ++j) {
+        at[j] = turn;
+        turn.advance(1, runs, n);
+        if (at[j].k >= n) at[j].p = 0;       // past the end: some run of the last, unused
+        const int k = min(at[j].k, n - 1);
+        e[j] = L.expert[k];
+        row0[j] = L.row0[k];
+        rows[j] = __popcll(L.mask[k]);
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        wf[j][h] = load16(rw, ow, 128 * at[j].p + 64 * h);
-        x[j][h] = load16(rh, oh, 128 * at[j].p + 64 * h);
+      for (int j = 0; j < NB; ++j) {
+        e[j] = __builtin_amdgcn_readfirstlane(e[j]);
+        row0[j] = __builtin_amdgcn_readfirstlane(row0[j]);
+        rows[j] = __builtin_amdgcn_readfirstlane(rows[j]);
+        const bool shared = e[j] >= a.n_routed;
+        const size_t mat = shared ? e[j] - a.n_routed : e[j];
+        const uint8_t* const base = static_cast<const uint8_t*>(shared ? a.ws_down : a.w_down) + (mat * a.d + d0) * ld;
+        const rsrc_t rw = make_rsrc(base, 16 * ld);
+        const uint32_t oh = row_at(row0[j], rows[j], 0);
+        if constexpr (FMT == FMT_E4M3) {
+          sw[j] = (shared ? a.ss_down : a.s_down)[(mat * a.d + d0) / 128 * runs + at[j].p];
+          sh[j] = a.hs[static_cast<size_t>(row0[j] + min(lr, rows[j] - 1)) * runs + at[j].p];
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          wf[j][h] = load16(rw, ow, 128 * at[j].p + 64 * h);
+          x[j][h] = load16(rh, oh, 128 * at[j].p + 64 * h);
+        }
       }
-    }
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      if (j >= left) continue;
-      if (at[j].k != cur) {
-        if (cur >= 0) flush(cur, cur_rows);
-        cur = at[j].k;
-        cur_rows = rows[j];
-      }
-      auto product = [&](int t, const i32x4(&v)[2], float s) {
-        if constexpr (FMT == FMT_E4M3)
-          acc[t] += run_product<FMT>(wf[j], v, f32x4{0.f, 0.f, 0.f, 0.f}) * (s * sw[j]);
-        else
-          acc[t] = run_product<FMT>(wf[j], v, acc[t]);
-      };
-      product(0, x[j], sh[j]);
+      for (int j = 0; j < NB; ++j) {
+        if (j >= left) continue;
+        if (at[j].k != cur) {
+          if (cur >= 0) flush(cur, cur_rows);
+          cur = at[j].k;
+          cur_rows = rows[j];
+        }
+        auto product = [&](int t, const i32x4(&v)[2], float s) {
+          if constexpr (FMT == FMT_E4M3)
+            acc[t] += run_product<FMT>(wf[j], v, f32x4{0.f, 0.f, 0.f, 0.f}) * (s * sw[j]);
+          else
+            acc[t] = run_product<FMT>(wf[j], v, acc[t]);
+        };
+        product(0, x[j], sh[j]);
 #pragma unroll
-      for (int t = 1; t < TILES; ++t) {   // more rows than a tile's: few experts have them
-        if (rows[j] <= TR * t) continue;
-        const uint32_t oh = row_at(row0[j], rows[j], t);
-        i32x4 v[2];
+        for (int t0 = 1; t0 < TILES; t0 += 4) {   // more rows than a tile's: four tiles' loads together
+          if (rows[j] <= TR * t0) continue;
+          i32x4 v[4][2];
+          float s[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) v[h] = load16(rh, oh, 128 * at[j].p + 64 * h);
-        float s = 0.f;
-        if constexpr (FMT == FMT_E4M3) s = a.hs[static_cast<size_t>(row0[j] + min(TR * t + lr, rows[j] - 1)) * runs + at[j].p];
-        product(t, v, s);
+          for (int i = 0; i < 4 && t0 + i < TILES; ++i) {
+            const uint32_t oh = row_at(row0[j], rows[j], t0 + i);   // past the last row: zeros
+            if constexpr (FMT == FMT_E4M3)
+              s[i] = a.hs[static_cast<size_t>(row0[j] + min(TR * (t0 + i) + lr, rows[j] - 1)) * runs + at[j].p];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) v[i][h] = load16(rh, oh, 128 * at[j].p + 64 * h);
+          }
+#pragma unroll
+          for (int i = 0; i < 4 && t0 + i < TILES; ++i) product(t0 + i, v[i], s[i]);
+        }
       }
     }
   }
@@ -728,21 +760,19 @@ __global__ __launch_bounds__(THREADS, 4) void few_down_kernel(FewArgs a) {
 #pragma unroll
   for (int k = 1; k < WAVES; ++k) y += sums[k][t][g];
   const size_t off = static_cast<size_t>(t) * a.d + d0 + 4 * g;
-  float v[4];
-  if (a.x_fmt == FMT_F32) {
-    const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(a.u) + off);
-    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
-  } else {
-    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.u) + off);
-    v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
-    v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
-  }
-#pragma unroll
-  for (int r = 0; r < 4; ++r) v[r] += y[r];
-  if (a.out_fmt == FMT_F32)
-    *reinterpret_cast<float4*>(static_cast<float*>(a.y) + off) = make_float4(v[0], v[1], v[2], v[3]);
+  if (a.splits > 1)
+    *reinterpret_cast<f32x4*>(a.part + static_cast<size_t>(blockIdx.y) * a.T * a.d + off) = y;
   else
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + off) = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
+    store_y(a, off, y);
+}
+
+// The splits' sums, in order, and the residual: four columns a thread.
+__global__ __launch_bounds__(256) void few_sum_kernel(FewArgs a) {
+  const size_t off = 4 * (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x), n = static_cast<size_t>(a.T) * a.d;
+  if (off >= n) return;
+  f32x4 y = *reinterpret_cast<const f32x4*>(a.part + off);
+  for (int k = 1; k < a.splits; ++k) y += *reinterpret_cast<const f32x4*>(a.part + k * n + off);
+  store_y(a, off, y);
 }
 
 template <class F>
@@ -787,7 +817,9 @@ struct Launch {
   }
   template <int FMT>
   static void down(const FewArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL((few_down_kernel<FMT, NT>), dim3(a.d / 16), dim3(THREADS), 0, s, a);
+    hipLaunchKernelGGL((few_down_kernel<FMT, NT>), dim3(a.d / 16, a.splits), dim3(THREADS), 0, s, a);
+    if (a.splits > 1)
+      hipLaunchKernelGGL(few_sum_kernel, dim3(ceil_div(a.T * (a.d / 4), 256)), dim3(256), 0, s, a);
   }
 };
 

@@ -17,8 +17,8 @@ int validate_few(const moe_shape* s) {
 
 // Workspace map (byte offsets, each 256-byte aligned).
 struct Layout {
-  size_t logits, idx, gate, h, hq, hs, uq, us, total;
-  int slices;
+  size_t logits, idx, gate, h, hq, hs, uq, us, part, total;
+  int slices, splits;
 };
 
 Layout make_layout(const moe_shape& s) {
@@ -37,6 +37,8 @@ Layout make_layout(const moe_shape& s) {
   L.hs = take(fp8 ? R * (I / 128) * 4 : 0);
   L.uq = take(fp8 ? T * d : 0);
   L.us = take(fp8 ? T * (d / 128) * 4 : 0);
+  L.splits = moe::few_splits(s.T, s.d, s.n_routed, s.n_shared, s.inter, s.top_k, fmt_of(s.w_dtype));
+  L.part = take(L.splits > 1 ? L.splits * T * d * 4 : 0);
   L.total = o;
   return L;
 }
@@ -88,6 +90,7 @@ int moe_forward_few(const moe_shape* shape, const void* u, const void* centroids
   a.w_fmt = fmt_of(s.w_dtype);
   a.out_fmt = fmt_of(s.out_dtype);
   a.slices = L.slices;
+  a.splits = L.splits;
   a.counts = r.expert_counts;
   a.offsets = r.expert_offsets;
   a.perm_token = r.perm_token;
@@ -103,6 +106,7 @@ int moe_forward_few(const moe_shape* shape, const void* u, const void* centroids
     a.hs = at<float>(workspace, L.hs);
     a.uq = at<uint8_t>(workspace, L.uq);
     a.us = at<float>(workspace, L.us);
+    a.part = at<float>(workspace, L.part);
   }
   // an empty batch still has a routing: no expert has a row
   const bool rows = s.T > 0, fp8 = s.w_dtype == MOE_DTYPE_E4M3;

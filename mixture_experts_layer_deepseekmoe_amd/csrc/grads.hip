@@ -131,7 +131,10 @@ __global__ __launch_bounds__(THREADS) void grad_sumsq_kernel(GradArgs a, double*
     const int k = tensor_of(a, c);
     if (!MOE_CHECK(c >= a.first[k] && c < a.first[k + 1], 1001)) continue;
     const long long i0 = static_cast<long long>(c - a.first[k]) * GRAD_CHUNK;
-    sum = a.bf16[k] & 1 ? chunk_sumsq<true>(a.data[k], i0, a.numel[k], sum) : chunk_sumsq<false>(a.data[k], i0, a.numel[k], sum);
+    if (a.bf16[k] & 1)
+      sum = chunk_sumsq<true>(a.data[k], i0, a.numel[k], sum);
+    else
+      sum = chunk_sumsq<false>(a.data[k], i0, a.numel[k], sum);
   }
   sum = block_sum(sum, red);
   if (threadIdx.x == 0) part[blockIdx.x] = sum;
