@@ -266,18 +266,20 @@ int moe_forward_static(const moe_shape* shape, const void* u, const void* centro
 
 /*
  * moe_forward for up to MOE_FEW_TOKENS tokens (single tokens, a decode batch, the
- * drafted tokens of a request): the same layer, arguments and routing, in three
- * launches (E4M3: four), each chosen expert's weights read once.  All dtype
- * combinations, shared experts and group-limited routing as moe_forward has
- * them.  The expert outputs are not rounded between the kernels (BF16 weights:
- * H enters the down product as a pair of bf16 values), so y may differ from
- * moe_forward's by the roundings that it makes: 2^-9 of H and of Y (E4M3: of Y).
- * A token's y is the same whatever other tokens stand in the batch, but for
- * the order in which its logits and its experts' sums are formed.
+ * drafted tokens of a request): the same layer, arguments and routing, in three to
+ * six launches, each chosen expert's weights read once.  All dtype combinations,
+ * shared experts and group-limited routing as moe_forward has them.  Nothing but H
+ * is rounded between the kernels, and H by the FP8 path alone (its 1x128 codes;
+ * with BF16 weights H enters the down product as a pair of bf16 values), so y may
+ * differ from moe_forward's by the roundings that it makes: 2^-9 of H and of Y
+ * (E4M3: of Y, and what 8-bit matrix instructions leave).  A token's y is the same
+ * whatever other tokens stand in the batch, but for the order of its sums.
  * MOE_STAGE_ROUTE, MOE_STAGE_GATE_UP (with the selection), MOE_STAGE_QUANT (E4M3:
  * of h; u is quantised by the first launch) and MOE_STAGE_DOWN (with gates and
- * residual) are traced.
+ * residual) are traced.  Calls that may overlap take a workspace each.
  * Limits beside the layer's: T at most MOE_FEW_TOKENS, d and inter at most 32768.
+ * One token takes 0.5 to 0.6 of moe_forward's time, 16 tokens 0.8 to 0.95; from about
+ * 32 tokens on the two are level, and moe_forward is ahead by up to 15% at 64.
  */
 #define MOE_FEW_TOKENS 64
 int moe_few_workspace_size(const moe_shape* shape, size_t* bytes);

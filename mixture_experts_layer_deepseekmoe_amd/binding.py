@@ -400,9 +400,9 @@ def moe_forward_few(shape: LayerShape, u: torch.Tensor, centroids: torch.Tensor,
                     weights: ExpertWeights, y: Optional[torch.Tensor] = None,
                     routing: Optional[Dict[str, torch.Tensor]] = None, workspace: Optional[torch.Tensor] = None,
                     trace: Optional[Trace] = None) -> torch.Tensor:
-    """moe_forward for up to FEW_TOKENS tokens, in three launches (e4m3: four): the
-    weights of each chosen expert are read once, and its outputs are not rounded
-    between the kernels.  The workspace is few_workspace_size(shape) bytes."""
+    """moe_forward for up to FEW_TOKENS tokens, in few launches: the weights of each
+    chosen expert are read once, and its outputs are not rounded between the
+    kernels.  The workspace is few_workspace_size(shape) bytes."""
     T, d, N, x = shape.T, shape.d, shape.n_routed, shape.x_dtype
     if y is None:
         y = torch.empty((T, d), dtype=_TORCH_DT[DTYPE_CODE[shape.out_dtype]], device=u.device)
@@ -802,13 +802,18 @@ class TensorList:
         devices = {t.get_device() for t in ts}
         if -1 in devices:
             raise ValueError("tensors passed to the MoE library must live on the GPU")
-        if devices and devices != {torch._C._cuda_getDevice()}:
-            raise ValueError(f"tensors live on devices {sorted(devices)}, not all of them the current one")
+        if len(devices) > 1:
+            raise ValueError(f"tensors live on several devices: {sorted(devices)}")
         if not all([t.is_contiguous() for t in ts]):
             raise ValueError("tensors passed to the MoE library must be contiguous")
         # packed at once: an array of ctypes structures takes five times as long
         flat = [v for t in ts for v in (t.data_ptr(), t.numel(), _TENSOR_DT[t.dtype])]
         self.c = ctypes.create_string_buffer(struct.pack("<" + "Qqi4x" * len(ts), *flat))
+        self.devices = devices
+
+    def check_device(self) -> None:
+        if self.devices and self.devices != {torch._C._cuda_getDevice()}:
+            raise ValueError(f"the tensors live on cuda:{min(self.devices)}, which is not the current device")
 
     def __len__(self) -> int:
         return len(self.tensors)
@@ -834,6 +839,7 @@ def moe_grad_sumsq(grads, sumsq: Optional[torch.Tensor] = None, workspace: Optio
     ws = workspace
     if ws is None:
         ws = torch.empty(grad_workspace_size(len(grads)), dtype=torch.uint8, device=device)
+    grads.check_device()
     _same_device(sumsq, ws)
     rc = load_library().moe_grad_sumsq(grads.c, len(grads), _arg(sumsq, "sumsq", "f64", 1), _ptr(ws), ws.numel(), _stream())
     _check(rc, "moe_grad_sumsq")
@@ -850,6 +856,9 @@ def moe_grad_clip(grads, sumsq: torch.Tensor, max_norm: float, out=None, norm: O
         raise ValueError(f"out: expected {len(grads)} tensors, got {len(out)}")
     if norm is None:
         norm = torch.empty((1,), dtype=torch.float32, device=sumsq.device)
+    grads.check_device()
+    if out is not None:
+        out.check_device()
     _same_device(sumsq, norm)
     rc = load_library().moe_grad_clip(grads.c, None if out is None else out.c, len(grads), _arg(sumsq, "sumsq", "f64", 1),
                                       float(max_norm), _arg(norm, "norm", "f32", 1), _stream())

@@ -40,8 +40,23 @@ constexpr int GATEUP_BLOCKS = 512;   // two to a CU, each taking units in turn
 __device__ __forceinline__ i32x4 load16(rsrc_t r, uint32_t off, uint32_t soff) {
   return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, 0));
 }
+// Eight of a lane's 8-bit codes as bf16 values (exact).
+__device__ __forceinline__ i32x4 codes_bf16(int lo, int hi) {
+  typedef __bf16 pair __attribute__((ext_vector_type(2)));
+  auto two = [](int c, auto upper) {
+    const pair p = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, decltype(upper)::value);
+    return __builtin_bit_cast(int, p);
+  };
+  constexpr std::false_type l{};
+  constexpr std::true_type u{};
+  return i32x4{two(lo, l), two(lo, u), two(hi, l), two(hi, u)};
+}
+
 // One 128-byte run of K: the products of 16 weight rows with 16 tokens.  A lane holds
 // bytes 16 lg .. +15 of each half of the run, of its weight row and of its token alike.
+// 8-bit codes go through the bf16 matrix instructions, which sum them as exactly as
+// fp32 does (1e-8 of a run's product); the 8-bit ones keep 1.4e-5, and the matrix cores
+// wait for HBM either way (4 tokens, d = 7168: 256 us with either).
 template <int FMT>
 __device__ __forceinline__ f32x4 run_product(const i32x4 (&w)[2], const i32x4 (&x)[2], f32x4 c) {
   if constexpr (FMT == FMT_BF16) {
@@ -53,13 +68,11 @@ __device__ __forceinline__ f32x4 run_product(const i32x4 (&w)[2], const i32x4 (&
       for (int e = 0; e < 4; ++e) c = mfma_f32(__int_as_float(w[k][e]), __int_as_float(x[k][e]), c);
     return c;
   } else {
-    i32x8 a, b;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      a[e] = w[e / 4][e % 4];
-      b[e] = x[e / 4][e % 4];
-    }
-    return mfma_e4m3(a, b, c);
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) c = mfma_bf16(codes_bf16(w[k][e], w[k][e + 1]), codes_bf16(x[k][e], x[k][e + 1]), c);
+    return c;
   }
 }
 
@@ -486,7 +499,7 @@ __device__ __forceinline__ void gateup_unit(const FewArgs& a, int e, int row0, i
   }
   float h[4];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) h[r] = silu_f32(g[r]) * u[r];
+  for (int r = 0; r < 4; ++r) h[r] = g[r] / (1.0f + expf(-g[r])) * u[r];
   const int row = row0 + 16 * w + lr;
   if (!MOE_CHECK(row < TK + a.n_shared * a.T, 803)) return;
   const size_t off = static_cast<size_t>(row) * a.inter + i0 + 4 * lg;
