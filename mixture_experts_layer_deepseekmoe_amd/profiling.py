@@ -76,8 +76,8 @@ def _run(args):
 
 
 def _operators(args):
-    """Runs cases of perf/operators.py with the framework's calls, and losses of other sizes, on three sets of inputs
-    in turn."""
+    """Runs cases of perf/operators.py (--more: of perf/more_operators.py) with the framework's calls, and losses of
+    other sizes, on three sets of inputs in turn."""
     sys.path.insert(0, ROOT)
     import importlib.util
 
@@ -85,7 +85,8 @@ def _operators(args):
 
     import mixture_experts_layer_deepseekmoe_amd as moe
 
-    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
+    file = "more_operators" if args.more else "operators"
+    spec = importlib.util.spec_from_file_location(file, os.path.join(ROOT, "perf", file + ".py"))
     ops = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(ops)
     ops.own = True
@@ -116,7 +117,7 @@ def _operators(args):
 
 
 def _short(name: str) -> str:
-    for key in ("dgrad_down_kernel", "dgrad_gateup_kernel", "wgrad_down_kernel", "wgrad_gateup_kernel",
+    for key in () if "::few_" in name else ("dgrad_down_kernel", "dgrad_gateup_kernel", "wgrad_down_kernel", "wgrad_gateup_kernel",
                 "wgrad8_down_kernel", "wgrad8_gateup_kernel", "colquant_kernel", "swiglu_bwd_kernel",
                 "bwd_prep_kernel", "bwd_dz_kernel", "bwd_du_kernel", "bwd_de_kernel",
                 "gateup_kernel", "down_kernel", "route_part_kernel", "route_finish_kernel", "route_scores_kernel",
@@ -341,6 +342,7 @@ def main():
     r.add_argument("--steps", type=int, default=3)
     r.add_argument("--train", action="store_true", help="training steps (moe_forward_train + moe_backward)")
     o = sub.add_parser("operators")
+    o.add_argument("--more", action="store_true")
     o.add_argument("--case", nargs="*")
     o.add_argument("--loss", nargs="*", metavar="T,d,V,DTYPE")
     o.add_argument("--steps", type=int, default=3)

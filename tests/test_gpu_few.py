@@ -43,6 +43,12 @@ CASES = [_case("small_bf16", t) for t in (1, 2, 16, 17, 32, 33, 64)] + [
     _case("small_bf16", 11, n_routed=1, top_k=1, n_shared=0, d=64, inter=64),
     _case("small_bf16", 19, d=448, inter=704, n_routed=67, top_k=7),
     _case("small_fp32", 21, d=160, inter=224, n_routed=13, top_k=5, n_shared=3),
+    # either side of where a launch of its own selects; 64, 128, 256 and 512 experts to a selection
+    _case("small_bf16", 8, n_routed=64), _case("small_bf16", 9, n_routed=65), _case("small_fp8", 8, n_routed=130),
+    _case("small_fp8", 8, n_routed=300, top_k=9), _case("small_bf16", 8, n_routed=320, n_groups=64, topk_groups=5),
+    # columns shared among blocks, as many as there are
+    _case("small_fp32", 30, n_routed=64, inter=256), _case("small_fp8", 50, d=128, n_routed=100, top_k=8, n_shared=2),
+    _case("small_bf16", 64, d=64, inter=2048, n_routed=90, top_k=8, n_shared=2),
 ]
 
 
@@ -218,6 +224,65 @@ def test_few_repeats_streams_graph(name, T):
         torch.cuda.synchronize()
         assert torch.equal(y, want[k]), k
         assert torch.equal(moe.moe_forward_few(shape, us[2], E, b, w), want[2])
+
+
+def test_few_calls_at_once():
+    """Two calls on two streams, a workspace each, over and over: each as alone."""
+    say("case: moe_forward_few, two calls at once")
+    cases = [(_case("small_bf16_ns2", 40), 1), (_case("small_fp8", 7), 2)]
+    runs = []
+    for cfg, seed in cases:
+        inp = make_inputs(cfg, seed)
+        w, shape = moe.prepare_weights(cfg, inp), moe.LayerShape.from_config(cfg)
+        args = (shape, inp.u.to(DEV), inp.centroids.to(DEV), inp.bias.to(DEV), w)
+        runs.append((args, moe.moe_forward_few(*args), moe.alloc_few_workspace(shape), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for args, _, ws, stream in runs:
+            with torch.cuda.stream(stream):
+                got.append(moe.moe_forward_few(*args, workspace=ws))
+    torch.cuda.synchronize()
+    for k, y in enumerate(got):
+        assert torch.equal(y, runs[k % 2][1]), k
+
+
+def test_few_graphs_share_a_workspace():
+    """Two captured calls of different shapes on one workspace, replayed in turn."""
+    say("case: moe_forward_few, two graphs, one workspace")
+    cases = [_case("small_bf16", 64), _case("small_bf16", 2)]
+    inp = make_inputs(cases[0], 4)
+    w = moe.prepare_weights(cases[0], inp)
+    E, b = inp.centroids.to(DEV), inp.bias.to(DEV)
+    shapes = [moe.LayerShape.from_config(c) for c in cases]
+    ws = torch.zeros(max(moe.few_workspace_size(s) for s in shapes), dtype=torch.uint8, device=DEV)
+    us = [inp.u.to(DEV), inp.u[5:7].to(DEV).contiguous()]
+    want = [moe.moe_forward_few(s, u, E, b, w) for s, u in zip(shapes, us)]
+    ys = [torch.empty_like(y) for y in want]
+    graphs = []
+    for s, u, y in zip(shapes, us, ys):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            moe.moe_forward_few(s, u, E, b, w, y=y, workspace=ws)
+    for k in (0, 1, 1, 0, 1, 0):
+        ys[k].zero_()
+        graphs[k].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(ys[k], want[k])
+
+
+def test_few_routing_in_part():
+    """Any of the routing's fields alone, y the same."""
+    cfg = _case("small_bf16", 12)
+    say("case: moe_forward_few, routing in part")
+    inp = make_inputs(cfg, 7)
+    w, shape = moe.prepare_weights(cfg, inp), moe.LayerShape.from_config(cfg)
+    y, whole = _run(cfg, inp, w)
+    u, E, b = (t.to(DEV) for t in (inp.u, inp.centroids, inp.bias))
+    for name in whole:
+        part = {name: torch.full_like(whole[name], -3)}
+        assert torch.equal(moe.moe_forward_few(shape, u, E, b, w, routing=part), y)
+        assert torch.equal(part[name], whole[name]), name
 
 
 def test_few_writes_nothing_else():
