@@ -408,7 +408,12 @@ def moe_forward_few(shape: LayerShape, u: torch.Tensor, centroids: torch.Tensor,
         y = torch.empty((T, d), dtype=_TORCH_DT[DTYPE_CODE[shape.out_dtype]], device=u.device)
     ws = alloc_few_workspace(shape, u.device) if workspace is None else workspace
     _same_device(u, centroids, bias, weights.w_gate_up, weights.w_down, weights.ws_gate_up, weights.ws_down, y, ws)
-    rs = _routing_struct(routing)
+    rs = None
+    if routing is not None:
+        sizes = {"topk_idx": (T, shape.top_k), "topk_gate": (T, shape.top_k), "expert_counts": (N,),
+                 "expert_offsets": (N + 1,), "perm_token": (T * shape.top_k,), "pos": (T, shape.top_k)}
+        _same_device(*routing.values())
+        rs = Routing(*[_arg(routing.get(k), k, "f32" if k == "topk_gate" else "i32", *size) for k, size in sizes.items()])
     rc = load_library().moe_forward_few(
         ctypes.byref(shape.c()), _arg(u, "u", x, T, d), _arg(centroids, "centroids", x, N, d), _arg(bias, "bias", "f32", N),
         ctypes.byref(_few_weights(shape, weights)), _arg(y, "y", shape.out_dtype, T, d), _ref(rs), _ptr(ws), ws.numel(),

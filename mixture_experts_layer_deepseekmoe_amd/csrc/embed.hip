@@ -12,6 +12,10 @@
 // named rows are then written over.  (One pass that finds each row's run by a search
 // and writes every row once took 417 us for 65536 x 7168 in fp32, where clearing takes
 // 290 and the sums 80: its waves wait for their searches, loads and stores in turn.)
+//
+// Measured, us: 8192 rows of 7168 into 65536 in fp32, 466 with the forward: forward with
+// the norm 54, clearing beside the sort 303 (6.2 TB/s), sums 27 + 5 + 84; 4096 rows of
+// 2048 into 65536 in bf16, 80: 12.5, 42, 7, 20.
 #include "ends.hpp"
 #include "gemm_core.hpp"
 #include "rows.hpp"

@@ -22,6 +22,13 @@
 //                      that leaves CUs idle, blocks share the experts' runs, and
 //   few_sum_kernel     adds their sums
 //
+// Measured, us (reading alone reaches 6.2 TB/s here): 1 token, d = 7168 in bf16, 9
+// experts of 88 MB: 155 in all, gate and up 102 (5.2 TB/s), down 53 (5.0), the router
+// 4.7; 4 tokens in 8 bits, 33 experts of 44 MB: 256, gate and up 168 (5.7), down 97
+// (4.9); 32 tokens, 164 experts: 2430, gate and up 1720 (5.6), down 925 (5.2).  1 token,
+// d = 2048, 8 experts of 17 MB: 42, gate and up 20.6, down 14.2, the rest launches; of
+// the 20.6, 8 are not loads (the selection, a block's sums, the last blocks).
+//
 // Sums are fp32.  With bf16 weights the operand h is a pair of bf16 values, what
 // the first rounds off in the second (2^-16 is left): the MFMAs wait for HBM
 // anyway, so y is as exact as with fp32 products.
@@ -35,7 +42,10 @@ namespace moe {
 namespace {
 
 constexpr int THREADS = 512, WAVES = 8;
-constexpr int GATEUP_BLOCKS = 512;   // two to a CU, each taking units in turn
+// Two blocks to a CU, each taking units in turn: a third round of blocks would select
+// again.  1 token, d = 7168: 159 us with 512, 160 with 256, 169 with 384, 164 with 1152;
+// 32 tokens: 2430, 2445, 2724, 2520.
+constexpr int GATEUP_BLOCKS = 512;
 
 __device__ __forceinline__ i32x4 load16(rsrc_t r, uint32_t off, uint32_t soff) {
   return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, 0));

@@ -108,7 +108,8 @@ def test_embed_backward_follows_the_oracle(T, d, V, grad, kind):
 
 
 @pytest.mark.parametrize("kind", ["text", "one", "none"])
-@pytest.mark.parametrize("T,d,V,grad", [(1, 64, 10, "f32"), (100, 1032, 40, "bf16"), (700, 128, 100000, "f32")])
+@pytest.mark.parametrize("T,d,V,grad", [(1, 64, 10, "f32"), (100, 1032, 40, "bf16"), (700, 128, 100000, "f32"),
+                                        (9000, 8, 300, "f32"), (17000, 8, 300, "bf16")])
 def test_embed_backward_accumulates(T, d, V, grad, kind):
     say(f"case: embed backward, added, {T} x {d}, {V} entries, {grad}, {kind}")
     _backward(T, d, V, kind, grad, accumulate=True)

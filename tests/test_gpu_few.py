@@ -307,6 +307,8 @@ def test_few_refuses_on_the_gpu():
     for kw in (dict(u=u[:3]), dict(u=u.float()), dict(centroids=E[:-1]), dict(bias=b.double()), dict(y=torch.empty(4, 8, device=DEV)),
                dict(weights=moe.ExpertWeights(w.w_gate_up[1:], w.w_down, w.ws_gate_up, w.ws_down)),
                dict(weights=moe.ExpertWeights(w.w_gate_up, w.w_down, w.ws_gate_up, w.w_down)),
+               dict(routing={"topk_idx": torch.empty(4, 1, dtype=torch.int32, device=DEV)}),
+               dict(routing={"expert_counts": torch.empty(cfg.n_routed, device=DEV)}),
                dict(u=torch.zeros(4, 2 * cfg.d, device=DEV).bfloat16()[:, ::2])):
         with pytest.raises(ValueError):
             moe.moe_forward_few(shape, **{**dict(u=u, centroids=E, bias=b, weights=w), **kw})
