@@ -6,8 +6,8 @@
     python -m mixture_experts_layer_deepseekmoe_amd.profiling peaks
     # the vendor library (hipBLASLt through torch) on GEMMs of the same sizes -> profiles/library_reference.json:
     python -m mixture_experts_layer_deepseekmoe_amd.profiling library --workload bf16_d7168
-    # the operators around the layer (cases of perf/operators.py, by name, and training passes of the loss of any
-    # size and gradient type; default: all the cases):
+    # the operators around the layer (cases of perf/operators.py, with --more of perf/more_operators.py, by name, and
+    # training passes of the loss of any size and gradient type; default: all the cases):
     python -m mixture_experts_layer_deepseekmoe_amd.profiling operators --case loss_train_d7168 --loss 48,7168,10000,f32 --steps 3
     # turn rocprofv3's CSV output into the summaries kept under profiles/:
     python -m mixture_experts_layer_deepseekmoe_amd.profiling summarize --trace DIR --pmc DIR [DIR...] \
