@@ -47,10 +47,12 @@ struct FewArgs {
 inline int few_runs(int cols, int fmt) { return cols * (fmt == FMT_F32 ? 4 : fmt == FMT_BF16 ? 2 : 1) / 128; }
 
 // The router's K slices: a block takes 16 experts and a slice of K, a run of 128
-// bytes a wave at a time, so one run for each of its 8 waves at least.  Every block of
-// the next kernel reads the slices of all tokens again: 64 of them together at most.
+// bytes a wave at a time, so one run for each of its 8 waves at least.  Up to 8 tokens
+// every block of the next kernel reads the slices of all tokens again, 64 of them
+// together at most; beyond, the selection reads them once, and 8 take the router of 64
+// tokens at d = 7168 from 39 us (one slice: 16 blocks) to 10.
 inline int few_slices(int T, int d, int x_fmt) {
-  const int most = (few_runs(d, x_fmt) + 7) / 8, want = 64 / (T > 0 ? T : 1);
+  const int most = (few_runs(d, x_fmt) + 7) / 8, want = T > 8 ? 8 : 64 / (T > 0 ? T : 1);
   const int s = want < most ? want : most;
   return s > 1 ? s : 1;
 }
@@ -59,11 +61,17 @@ inline int few_slices(int T, int d, int x_fmt) {
 // columns alone leave CUs idle (two blocks to a CU are asked for) and each block has a
 // number of runs left: with 64 at least, without splits and with 32, us, d = 2048 in
 // bf16: 1 token 40.1, 42.9, 44.5; 8 tokens 138, 163, 136; 32 tokens 242, 296, 237; 64
-// tokens 304, 422, 305.
-constexpr int FEW_SPLITS = 16, FEW_SPLIT_RUNS = 64;
+// tokens 304, 422, 305.  More than one block but less than two to a CU: four splits even
+// the CUs' shares out, once there is work for them; one split and four, us: d = 7168
+// (448 blocks) in bf16 1 token (288 runs) 153, 164, 2 tokens (544) 292, 289, 32 tokens
+// 2389, 2357, 64 tokens 3358, 3198, in 8 bits 2 tokens (272 runs) 171, 179, 64 tokens
+// 1734, 1667; d = 5120 (320 blocks) in bf16 2 tokens (336 runs) 151, 147, 64 tokens 818,
+// 692.  From 512 blocks on it does not pay: 768, 2 tokens 194, 236.
+constexpr int FEW_SPLITS = 16, FEW_SPLIT_RUNS = 64, FEW_EVEN_RUNS = 320;
 inline int few_splits(int T, int d, int n_routed, int n_shared, int inter, int top_k, int w_fmt) {
   const int blocks = d / 16, tk = T * top_k;
   const long long runs = static_cast<long long>((tk < n_routed ? tk : n_routed) + n_shared) * few_runs(inter, w_fmt);
+  if (blocks > 256 && blocks < 512) return runs >= FEW_EVEN_RUNS ? 4 : 1;
   int s = 512 / blocks;
   if (s > FEW_SPLITS) s = FEW_SPLITS;
   while (s > 1 && runs < static_cast<long long>(s) * FEW_SPLIT_RUNS) --s;
