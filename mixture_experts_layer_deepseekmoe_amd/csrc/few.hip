@@ -337,6 +337,7 @@ __global__ __launch_bounds__(THREADS) void few_route_kernel(FewArgs a, int block
     }
     return;
   }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.taken = 0;   // for the next kernel
   const int tiles = (a.n_routed + 15) / 16, tile = blockIdx.x % tiles, slice = blockIdx.x / tiles;
   if (!MOE_CHECK(slice < a.slices, 802)) return;
   const uint32_t ld = a.d * (FMT == FMT_F32 ? 4 : 2);
@@ -465,7 +466,7 @@ __device__ __forceinline__ void split4(const float (&v)[4], uint2& hi, uint2& lo
 
 template <int FMT, int NT>
 __device__ __forceinline__ void gateup_unit(const FewArgs& a, int e, int row0, int rows, const int32_t* token, int i0,
-                                            f32x4 (*red)[2][64]) {
+                                            f32x4 (*red)[2][64], int taken, int32_t* next) {
   constexpr int ES = FMT == FMT_F32 ? 4 : FMT == FMT_BF16 ? 2 : 1;
   const int w = wave_id(), lane = threadIdx.x & 63, lr = lane & 15, lg = lane >> 4;
   const bool shared = e >= a.n_routed;
@@ -498,6 +499,7 @@ __device__ __forceinline__ void gateup_unit(const FewArgs& a, int e, int row0, i
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int s = 0; s < 2; ++s) red[w * NT + t][s][lane] = q.acc[s][t];
+  if (next != nullptr && threadIdx.x == 0) *next = taken;   // the block's next unit
   __syncthreads();
   // wave t: row 16 t + lr, columns i0 + 4 lg .. +3
   if (w >= NT || 16 * w + lr >= rows) return;
@@ -530,6 +532,7 @@ __global__ __launch_bounds__(THREADS, 4) void few_gateup_kernel(FewArgs a) {
   __shared__ Lists L;
   __shared__ int32_t idx[16 * NT * MAX_TOPK], token[16 * NT * MAX_TOPK];
   __shared__ float gate[NQ > 0 ? WAVES * MAX_TOPK : 1];
+  __shared__ int32_t next[2];   // this unit's successor, and the last one's while waves still read it
   __shared__ union {
     float keys[WAVES][64 * NQ + 1];
     f32x4 red[WAVES * NT][2][64];
@@ -563,24 +566,34 @@ __global__ __launch_bounds__(THREADS, 4) void few_gateup_kernel(FewArgs a) {
     }
     if (a.offsets != nullptr && threadIdx.x == 0) a.offsets[a.n_routed] = TK;
   }
-  const int cols = a.inter / 16;
-  for (int i = blockIdx.x; i < L.n * cols; i += gridDim.x) {
-    const int k = i / cols, i0 = 16 * (i - k * cols);
+  // Above 16 tokens units differ: a shared expert's take longest and come first, and a
+  // block takes its next unit when it begins one.  In turn, that way, us: 64 tokens, d =
+  // 2048 in bf16 319, 299, in 8 bits 171, 169, d = 7168 3202, 3190 and 1728, 1675; 32
+  // tokens, d = 2048 in bf16 250, 241, but with longer units d = 7168 2377, 2409.  Of equal
+  // units the counter's latency is all that is left: 16 tokens, 8 bits, d = 2048 116, 124.
+  constexpr int ES = FMT == FMT_F32 ? 4 : FMT == FMT_BF16 ? 2 : 1;
+  const bool take = NT == 4 || (NT == 2 && a.d * ES <= 64 * 128);
+  const int cols = a.inter / 16, units = L.n * cols;
+  auto after = [&](int i, int turn) { return take ? __builtin_amdgcn_readfirstlane(next[turn]) : i + static_cast<int>(gridDim.x); };
+  for (int i = blockIdx.x, turn = 0; i < units; i = after(i, turn), turn ^= 1) {
+    const int k0 = i / cols, k = take ? L.n - 1 - k0 : k0, i0 = 16 * (i - k0 * cols);
+    int taken = 0;
+    if (take && threadIdx.x == 0) taken = gridDim.x + atomicAdd(a.taken, 1);
     const int e = __builtin_amdgcn_readfirstlane(L.expert[k]), row0 = __builtin_amdgcn_readfirstlane(L.row0[k]);
     const int rows = __builtin_amdgcn_readfirstlane(__popcll(L.mask[k]));
     if constexpr (NT >= 4) {
       if (rows > 32) {
-        gateup_unit<FMT, 4>(a, e, row0, rows, token, i0, s.red);
+        gateup_unit<FMT, 4>(a, e, row0, rows, token, i0, s.red, taken, take ? next + turn : nullptr);
         continue;
       }
     }
     if constexpr (NT >= 2) {
       if (rows > 16) {
-        gateup_unit<FMT, 2>(a, e, row0, rows, token, i0, s.red);
+        gateup_unit<FMT, 2>(a, e, row0, rows, token, i0, s.red, taken, take ? next + turn : nullptr);
         continue;
       }
     }
-    gateup_unit<FMT, 1>(a, e, row0, rows, token, i0, s.red);
+    gateup_unit<FMT, 1>(a, e, row0, rows, token, i0, s.red, taken, take ? next + turn : nullptr);
   }
 }
 

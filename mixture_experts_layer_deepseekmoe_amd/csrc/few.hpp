@@ -39,6 +39,7 @@ struct FewArgs {
   uint8_t* uq;              // e4m3: [T][d] codes and [T][d/128] scales
   float* us;
   int splits;               // few_splits(...)
+  int32_t* taken;           // gate/up units taken beyond the first round
   float* part;              // [splits][T][d] (more than one split)
   void* y;                  // [T][d] out_fmt
 };

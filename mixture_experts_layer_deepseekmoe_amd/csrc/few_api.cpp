@@ -17,7 +17,7 @@ int validate_few(const moe_shape* s) {
 
 // Workspace map (byte offsets, each 256-byte aligned).
 struct Layout {
-  size_t logits, idx, gate, h, hq, hs, uq, us, part, total;
+  size_t taken, logits, idx, gate, h, hq, hs, uq, us, part, total;
   int slices, splits;
 };
 
@@ -29,6 +29,7 @@ Layout make_layout(const moe_shape& s) {
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o += align_up(bytes); return at; };
   L.slices = moe::few_slices(s.T, s.d, fmt_of(s.x_dtype));
+  L.taken = take(4);
   L.logits = take(L.slices * T * s.n_routed * 4);
   L.idx = take(T * K * 4);
   L.gate = take(T * K * 4);
@@ -97,6 +98,7 @@ int moe_forward_few(const moe_shape* shape, const void* u, const void* centroids
   a.pos = r.pos;
   a.y = y;
   if (s.T > 0) {
+    a.taken = at<int32_t>(workspace, L.taken);
     a.logits = at<float>(workspace, L.logits);
     a.idx = r.topk_idx != nullptr ? r.topk_idx : at<int32_t>(workspace, L.idx);
     a.gate = r.topk_gate != nullptr ? r.topk_gate : at<float>(workspace, L.gate);
