@@ -799,7 +799,8 @@ _TENSOR_DT = {torch.float32: F32, torch.bfloat16: BF16}
 class TensorList:
     """Tensors for moe_grad_sumsq and moe_grad_clip: contiguous fp32 or bf16 tensors
     on the current device (slices of a larger buffer among them).  It keeps them
-    alive, and may be used for any number of steps."""
+    alive, and may be used for any number of steps that use these tensors (a
+    gradient that a step makes anew is another one)."""
 
     def __init__(self, tensors):
         # by columns, each read by one map over the tensors: 211 tensors take 100 us, attribute by attribute 190

@@ -23,11 +23,11 @@
 //   few_sum_kernel     adds their sums
 //
 // Measured, us (reading alone reaches 6.2 TB/s here): 1 token, d = 7168 in bf16, 9
-// experts of 88 MB: 155 in all, gate and up 102 (5.2 TB/s), down 53 (5.0), the router
-// 4.7; 4 tokens in 8 bits, 33 experts of 44 MB: 256, gate and up 168 (5.7), down 97
-// (4.9); 32 tokens, 164 experts: 2430, gate and up 1720 (5.6), down 925 (5.2).  1 token,
-// d = 2048, 8 experts of 17 MB: 42, gate and up 20.6, down 14.2, the rest launches; of
-// the 20.6, 8 are not loads (the selection, a block's sums, the last blocks).
+// experts of 88 MB: 154 in all, gate and up 102 (5.2 TB/s), down 55 (4.8), the router
+// 4.7; 4 tokens in 8 bits, 33 experts of 44 MB: 258, gate and up 162 (5.9), down 86
+// (5.6); 32 tokens, 164 experts: 2376, gate and up 1547 (6.2), down 802 (6.0).  1 token,
+// d = 2048, 8 experts of 17 MB: 40, gate and up 22, down 14, the rest launches; of the
+// 22, 8 are not loads (the selection, a block's sums, the last blocks).
 //
 // Sums are fp32.  With bf16 weights the operand h is a pair of bf16 values, what
 // the first rounds off in the second (2^-16 is left): the MFMAs wait for HBM

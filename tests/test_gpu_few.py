@@ -49,6 +49,8 @@ CASES = [_case("small_bf16", t) for t in (1, 2, 16, 17, 32, 33, 64)] + [
     # columns shared among blocks, as many as there are
     _case("small_fp32", 30, n_routed=64, inter=256), _case("small_fp8", 50, d=128, n_routed=100, top_k=8, n_shared=2),
     _case("small_bf16", 64, d=64, inter=2048, n_routed=90, top_k=8, n_shared=2),
+    # 17 to 32 tokens of more than 64 runs of K
+    _case("small_bf16", 20, d=4160, inter=64),
 ]
 
 
