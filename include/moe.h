@@ -501,7 +501,8 @@ int moe_embed_backward(const moe_embed_shape* shape, const int32_t* tokens, cons
  *                    sees it in `norm`.
  * moe_tensor: `numel` consecutive elements, F32 or BF16, at any address of an
  * element (16-byte alignment is not needed here); numel may be 0.  The structs
- * are host memory, read before the call returns.  No two tensors may share memory, but out[i] may be tensors[i].
+ * are host memory, read before the call returns.  No two tensors may share memory,
+ * nor the sum or the norm with any or each other, but out[i] may be tensors[i].
  * max_norm > 0 (infinity: never clips).
  */
 typedef struct {

@@ -64,15 +64,17 @@ struct Range {
   uintptr_t lo, hi;
 };
 
-// Every tensor is valid, `out` (nullable) fits, and no two share memory, but for an
-// output that is its input.
-int tensors_ok(const moe_tensor* in, const moe_tensor* out, int n) {
+// Every tensor is valid, `out` (nullable) fits, and no two share memory, nor the sum or
+// the norm (nullable) with any, but for an output that is its input.
+int tensors_ok(const moe_tensor* in, const moe_tensor* out, int n, const double* sumsq, const float* norm) {
   if (n < 0 || (n > 0 && in == nullptr)) return MOE_ERR_INVALID_ARG;
-  if (n == 0) return MOE_OK;
-  Range* const r = new (std::nothrow) Range[2 * static_cast<size_t>(n)];
+  Range* const r = new (std::nothrow) Range[2 * static_cast<size_t>(n) + 2];
   if (r == nullptr) return MOE_ERR_UNSUPPORTED;
   int rc = MOE_OK;
   size_t m = 0;
+  const uintptr_t s0 = reinterpret_cast<uintptr_t>(sumsq), n0 = reinterpret_cast<uintptr_t>(norm);
+  r[m++] = {s0, s0 + sizeof(double)};
+  if (norm != nullptr) r[m++] = {n0, n0 + sizeof(float)};
   long long total = 0;
   for (int i = 0; i < n && rc == MOE_OK; ++i) {
     rc = tensor_ok(in[i]);
@@ -188,9 +190,9 @@ int moe_grad_workspace_size(int32_t n, size_t* bytes) {
 
 int moe_grad_sumsq(const moe_tensor* tensors, int32_t n, double* sumsq, void* workspace, size_t workspace_bytes,
                    hipStream_t stream) {
-  int rc = tensors_ok(tensors, nullptr, n);
-  if (rc != MOE_OK) return rc;
   if (sumsq == nullptr || (reinterpret_cast<uintptr_t>(sumsq) & 7u) != 0) return MOE_ERR_INVALID_ARG;
+  int rc = tensors_ok(tensors, nullptr, n, sumsq, nullptr);
+  if (rc != MOE_OK) return rc;
   if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < grad_bytes(n)) return MOE_ERR_WORKSPACE;
   double* const part = static_cast<double*>(workspace);
   long long parts = 0;
@@ -206,10 +208,10 @@ int moe_grad_sumsq(const moe_tensor* tensors, int32_t n, double* sumsq, void* wo
 
 int moe_grad_clip(const moe_tensor* tensors, const moe_tensor* out, int32_t n, const double* sumsq, double max_norm,
                   float* norm, hipStream_t stream) {
-  int rc = tensors_ok(tensors, out, n);
-  if (rc != MOE_OK) return rc;
   if (sumsq == nullptr || (reinterpret_cast<uintptr_t>(sumsq) & 7u) != 0 || !aligned4(norm) || !(max_norm > 0.0))
     return MOE_ERR_INVALID_ARG;
+  int rc = tensors_ok(tensors, out, n, sumsq, norm);
+  if (rc != MOE_OK) return rc;
   // from the last tensors to the first, as the kernel goes through a launch's: what the sum read last
   moe::GradArgs a;
   const int launches = (n + moe::GRAD_TENSORS - 1) / moe::GRAD_TENSORS;

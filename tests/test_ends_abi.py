@@ -10,6 +10,7 @@ import mixture_experts_layer_deepseekmoe_amd as moe
 from mixture_experts_layer_deepseekmoe_amd import binding as B
 
 FAKE = 1 << 20   # 16-byte aligned, never dereferenced
+SUM, NORM = FAKE + (1 << 16), FAKE + (1 << 16) + 64   # the gradients' sum, their norm
 BAD = FAKE + 4
 INVALID, UNSUPPORTED, WORKSPACE = B.MOE_ERR_INVALID_ARG, B.MOE_ERR_UNSUPPORTED, B.MOE_ERR_WORKSPACE
 r = ctypes.byref
@@ -178,31 +179,36 @@ def test_grad_workspace():
 ])
 def test_grad_refuses_tensors(ts):
     lib, c = moe.load_library(), _tensors(*ts)
-    assert lib.moe_grad_sumsq(c, len(ts), FAKE, FAKE, 1 << 20, None) == INVALID
-    assert lib.moe_grad_clip(c, None, len(ts), FAKE, 1.0, FAKE, None) == INVALID
+    assert lib.moe_grad_sumsq(c, len(ts), SUM, FAKE, 1 << 20, None) == INVALID
+    assert lib.moe_grad_clip(c, None, len(ts), SUM, 1.0, NORM, None) == INVALID
 
 
 def test_grad_refusals():
     lib = moe.load_library()
     two = _tensors((FAKE, 5, B.F32), (FAKE + 20, 5, B.F32))
     need = 1 << 20
-    assert lib.moe_grad_sumsq(None, 1, FAKE, FAKE, need, None) == INVALID
-    assert lib.moe_grad_sumsq(two, -1, FAKE, FAKE, need, None) == INVALID
+    assert lib.moe_grad_sumsq(None, 1, SUM, FAKE, need, None) == INVALID
+    assert lib.moe_grad_sumsq(two, -1, SUM, FAKE, need, None) == INVALID
     assert lib.moe_grad_sumsq(two, 2, None, FAKE, need, None) == INVALID
     assert lib.moe_grad_sumsq(two, 2, BAD, FAKE, need, None) == INVALID
-    assert lib.moe_grad_sumsq(two, 2, FAKE, None, need, None) == WORKSPACE
-    assert lib.moe_grad_sumsq(two, 2, FAKE, FAKE, 100, None) == WORKSPACE
+    assert lib.moe_grad_sumsq(two, 2, SUM, None, need, None) == WORKSPACE
+    assert lib.moe_grad_sumsq(two, 2, SUM, FAKE, 100, None) == WORKSPACE
     for m in (0.0, -1.0, float("nan")):
-        assert lib.moe_grad_clip(two, None, 2, FAKE, m, FAKE, None) == INVALID
-    assert lib.moe_grad_clip(two, None, 2, None, 1.0, FAKE, None) == INVALID
-    assert lib.moe_grad_clip(two, None, 2, FAKE, 1.0, FAKE + 2, None) == INVALID
+        assert lib.moe_grad_clip(two, None, 2, SUM, m, NORM, None) == INVALID
+    assert lib.moe_grad_clip(two, None, 2, None, 1.0, NORM, None) == INVALID
+    assert lib.moe_grad_clip(two, None, 2, SUM, 1.0, NORM + 2, None) == INVALID
     # outputs: another size, over an input that is not theirs, over each other, in place in another type
     for out in ([(FAKE + 400, 5, B.F32), (FAKE + 800, 4, B.F32)], [(FAKE + 20, 5, B.F32), (FAKE, 5, B.F32)],
                 [(FAKE + 400, 5, B.F32), (FAKE + 404, 5, B.F32)], [(FAKE, 5, B.BF16), (FAKE + 20, 5, B.F32)],
                 [(None, 5, B.F32), (FAKE + 20, 5, B.F32)]):
-        assert lib.moe_grad_clip(two, _tensors(*out), 2, FAKE, 1.0, FAKE, None) == INVALID, out
+        assert lib.moe_grad_clip(two, _tensors(*out), 2, SUM, 1.0, NORM, None) == INVALID, out
     huge = _tensors((FAKE, (1 << 44) + 1, B.BF16))
-    assert lib.moe_grad_sumsq(huge, 1, FAKE, FAKE, need, None) == UNSUPPORTED
+    assert lib.moe_grad_sumsq(huge, 1, SUM, FAKE, need, None) == UNSUPPORTED
+    # the sum or the norm in a tensor, or in each other
+    assert lib.moe_grad_sumsq(two, 2, FAKE + 16, FAKE, need, None) == INVALID
+    for at, norm in ((FAKE + 32, NORM), (SUM, FAKE + 36), (SUM, SUM), (SUM, SUM + 4)):
+        assert lib.moe_grad_clip(two, None, 2, at, 1.0, norm, None) == INVALID, (at, norm)
+    assert lib.moe_grad_clip(None, None, 0, SUM, 1.0, SUM + 4, None) == INVALID
 
 
 def test_tensor_list_refuses():
