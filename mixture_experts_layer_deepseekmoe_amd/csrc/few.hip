@@ -435,7 +435,7 @@ struct GateUp {
   // 158, two 162; d = 2048 (4 runs) 43.8, 41.9.  Two of 8-bit runs, which come with
   // scales: 4 tokens, d = 7168 265, four 300.
   __device__ __forceinline__ void all(int n) {
-    constexpr int NB = FMT == FMT_E4M3 ? 2 : 4 / NT;
+    constexpr int NB = FMT == FMT_E4M3 ? (NT == 4 ? 1 : 2) : 4 / NT;
     const int w = wave_id(), per = (n + WAVES - 1) / WAVES, p1 = min(n, (w + 1) * per);
     int p = w * per;
     if (NB <= 2 || per > NB)
@@ -530,17 +530,23 @@ __device__ __forceinline__ void gateup_unit(const FewArgs& a, int e, int row0, i
 template <int FMT, int NT, int NQ>
 __global__ __launch_bounds__(THREADS, 4) void few_gateup_kernel(FewArgs a) {
   __shared__ Lists L;
-  __shared__ int32_t idx[16 * NT * MAX_TOPK], token[16 * NT * MAX_TOPK];
+  __shared__ int32_t token[16 * NT * MAX_TOPK];
   __shared__ float gate[NQ > 0 ? WAVES * MAX_TOPK : 1];
   __shared__ int32_t next[2];   // this unit's successor, and the last one's while waves still read it
   __shared__ union {
-    float keys[WAVES][64 * NQ + 1];
-    f32x4 red[WAVES * NT][2][64];
+    struct {
+      float keys[WAVES][64 * NQ + 1];
+      // here, for two blocks' memory to fit a CU with NT = 4: 64 tokens, d = 2048, us, in
+      // bf16 287 (one block), 278, in 8 bits 169, 163
+      int32_t idx[16 * NT * MAX_TOPK];
+    } select;
+    f32x4 red[WAVES * NT][2][64];   // written after a barrier of its own
   } s;
+  int32_t* const idx = s.select.idx;
   const int w = wave_id();
   if (!MOE_CHECK(a.T <= (NQ > 0 ? WAVES : 16 * NT), 804)) return;
   if constexpr (NQ > 0) {
-    if (w < a.T) few_select<NQ>(a, w, s.keys[w], idx + w * a.top_k, gate + w * a.top_k);
+    if (w < a.T) few_select<NQ>(a, w, s.select.keys[w], idx + w * a.top_k, gate + w * a.top_k);
   } else {
     load_selection(a, idx);
   }
@@ -566,13 +572,14 @@ __global__ __launch_bounds__(THREADS, 4) void few_gateup_kernel(FewArgs a) {
     }
     if (a.offsets != nullptr && threadIdx.x == 0) a.offsets[a.n_routed] = TK;
   }
-  // Above 16 tokens units differ: a shared expert's take longest and come first, and a
-  // block takes its next unit when it begins one.  In turn, that way, us: 64 tokens, d =
-  // 2048 in bf16 319, 299, in 8 bits 171, 169, d = 7168 3202, 3190 and 1728, 1675; 32
-  // tokens, d = 2048 in bf16 250, 241, but with longer units d = 7168 2377, 2409.  Of equal
-  // units the counter's latency is all that is left: 16 tokens, 8 bits, d = 2048 116, 124.
+  // Above 16 tokens units differ: a shared expert's take longest.  Where rows are short (8
+  // KB) they come first, and a block takes its next unit when it begins one.  In turn, that
+  // way, us: d = 2048 in bf16 32 tokens 250, 241, 64 tokens 319, 299; d = 7168 in 8 bits 64
+  // tokens 1728, 1675.  Longer rows are read faster in turn: d = 7168 in bf16 32 tokens
+  // 2377, 2409, 64 tokens 3184, 3220.  Of equal units the counter's latency is all that is
+  // left: 16 tokens, 8 bits, d = 2048 116, 124.
   constexpr int ES = FMT == FMT_F32 ? 4 : FMT == FMT_BF16 ? 2 : 1;
-  const bool take = NT == 4 || (NT == 2 && a.d * ES <= 64 * 128);
+  const bool take = NT > 1 && a.d * ES <= 64 * 128;
   const int cols = a.inter / 16, units = L.n * cols;
   auto after = [&](int i, int turn) { return take ? __builtin_amdgcn_readfirstlane(next[turn]) : i + static_cast<int>(gridDim.x); };
   for (int i = blockIdx.x, turn = 0; i < units; i = after(i, turn), turn ^= 1) {
