@@ -62,6 +62,21 @@ __device__ __forceinline__ i32x4 codes_bf16(int lo, int hi) {
   return i32x4{two(lo, l), two(lo, u), two(hi, l), two(hi, u)};
 }
 
+// Codes of four values of a tile, times its factor, whose largest size has the bits `top`
+// (over the bits, where NaN and infinity stand above the rest; fmaxf would drop a NaN).
+// A tile that holds one gets the scale NaN or infinity, and the code NaN wherever value
+// times factor is NaN (e4m3x4 alone makes -448 of it): what reads the tile is not finite.
+__device__ __forceinline__ uint32_t codes_of(float a, float b, float c, float d, uint32_t top) {
+  uint32_t q = e4m3x4(a, b, c, d);
+  if (top >= 0x7f800000u) {
+    const float t[4] = {a, b, c, d};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (t[e] != t[e]) q = (q & ~(0xffu << 8 * e)) | 0x7fu << 8 * e;
+  }
+  return q;
+}
+
 // One 128-byte run of K: the products of 16 weight rows with 16 tokens.  A lane holds
 // bytes 16 lg .. +15 of each half of the run, of its weight row and of its token alike.
 // 8-bit codes go through the bf16 matrix instructions, which sum them as exactly as
@@ -321,16 +336,19 @@ __global__ __launch_bounds__(THREADS) void few_route_kernel(FewArgs a, int block
     const size_t off = static_cast<size_t>(i) * 128 + (lane & 15) * 8;
     if (live) raw = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.u) + off);
     const uint32_t words[4] = {raw.x, raw.y, raw.z, raw.w};
-    float v[8], m = 0.f;
+    float v[8];
+    uint32_t top = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       v[e] = __uint_as_float(e % 2 ? words[e / 2] & 0xffff0000u : words[e / 2] << 16);
-      m = fmaxf(m, fabsf(v[e]));
+      top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
     }
-    m = wave_max_16(m);
+#pragma unroll
+    for (int o = 1; o <= 8; o <<= 1) top = max(top, __shfl_xor(top, o));
+    const float m = __uint_as_float(top);
     const float inv = m == 0.f ? 0.f : 448.f / m;
-    const uint32_t lo = e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-    const uint32_t hi = e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+    const uint32_t lo = codes_of(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv, top);
+    const uint32_t hi = codes_of(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv, top);
     if (live) {
       *reinterpret_cast<uint2*>(a.uq + off) = make_uint2(lo, hi);
       if ((lane & 15) == 0) a.us[i] = m == 0.f ? 1.f : m / 448.f;
@@ -612,11 +630,13 @@ __global__ __launch_bounds__(256) void few_quant_kernel(FewArgs a) {
   if (i >= tiles) return;
   const size_t off = static_cast<size_t>(i) * 128 + 4 * l;
   const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.h) + off);
-  float m = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+  uint32_t top = max(max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu),
+                     max(__float_as_uint(v.z) & 0x7fffffffu, __float_as_uint(v.w) & 0x7fffffffu));
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
+  for (int o = 1; o < 32; o <<= 1) top = max(top, __shfl_xor(top, o));
+  const float m = __uint_as_float(top);
   const float inv = m == 0.f ? 0.f : 448.f / m;
-  *reinterpret_cast<uint32_t*>(a.hq + off) = e4m3x4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+  *reinterpret_cast<uint32_t*>(a.hq + off) = codes_of(v.x * inv, v.y * inv, v.z * inv, v.w * inv, top);
   if (l == 0) a.hs[i] = m == 0.f ? 1.f : m / 448.f;
 }
 

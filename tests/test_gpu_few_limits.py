@@ -1,0 +1,60 @@
+"""moe_forward_few where numbers end: what is not finite, scores below fp32's range,
+scores that are level, and a token's selection in batches of other sizes."""
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_layer_deepseekmoe_amd as moe
+from moe_workloads import PARITY_CONFIGS, make_inputs, to_numpy_f32
+from tests.parity import say
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def _inputs(name, T, seed, **kw):
+    cfg = PARITY_CONFIGS[name].replace(T=T, **kw)
+    return cfg, make_inputs(cfg, seed)
+
+
+def _call(cfg, inp, w, lib=moe.moe_forward_few):
+    shape = moe.LayerShape.from_config(cfg)
+    routing = moe.alloc_routing(shape)
+    y = lib(shape, inp.u.to(DEV), inp.centroids.to(DEV), inp.bias.to(DEV), w, routing=routing)
+    torch.cuda.synchronize()
+    return y.cpu(), routing["topk_idx"].cpu()
+
+
+@pytest.mark.parametrize("where", ["scale", "code", "down scale", "shared scale", "token"])
+def test_few_fp8_keeps_what_is_not_finite(where):
+    """A NaN among 8-bit weights or scales, an infinite token: no row that uses it is
+    finite anywhere (its 1x128 tiles of H or u read as NaN), every other row keeps its bits."""
+    cfg, inp = _inputs("small_fp8", 20, 2)
+    say(f"case: moe_forward_few, 8 bits, not finite, {where}")
+    w = moe.prepare_weights(cfg, inp)
+    y, idx = _call(cfg, inp, w)
+    e = int(idx[0, 0])
+    uses = (idx == e).any(1)
+    assert bool(torch.isfinite(y).all()) and 0 < int(uses.sum()) < cfg.T
+    cols = slice(None)
+    if where == "scale":          # 128 rows of the gate
+        w.s_gate_up[e, 0, 0] = float("nan")
+    elif where == "code":         # one column of H
+        w.w_gate_up[e, 5, 7] = 0x7f
+    elif where == "down scale":   # 128 columns of y
+        w.s_down[e, 0, 0] = float("nan")
+        cols = slice(0, 128)
+    elif where == "shared scale":
+        w.ss_gate_up[0, 0, 0] = float("nan")
+        uses[:] = True
+    else:
+        inp.u = inp.u.clone()
+        inp.u[7, 3] = float("inf")
+        uses[:] = False
+        uses[7] = True
+    y2, idx2 = _call(cfg, inp, w)
+    assert torch.equal(y2[~uses], y[~uses]) and torch.equal(idx2[~uses], idx[~uses])
+    assert not bool(torch.isfinite(y2[uses][:, cols]).any())
+    if where == "down scale":
+        assert torch.equal(y2[:, 128:], y[:, 128:])
