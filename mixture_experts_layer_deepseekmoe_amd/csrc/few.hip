@@ -725,8 +725,12 @@ __global__ __launch_bounds__(THREADS, 4) void few_down_kernel(FewArgs a) {
       acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
       if constexpr (TR == 8) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)   // the second values' column stands 8 lanes on
-          v[e] += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v[e]), 0x128, 0xf, 0xf, false));
+        for (int e = 0; e < 4; ++e) {
+          // the second values' column stands 8 lanes on; it says nothing where the first is not
+          // finite (an infinite weight times a second value of 0 or of the other sign: NaN)
+          const float lo = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v[e]), 0x128, 0xf, 0xf, false));
+          v[e] = fabsf(v[e]) < INFINITY ? v[e] + lo : v[e];
+        }
       }
       const int r = TR * t + lr;
       if (lr < TR && r < rows) {

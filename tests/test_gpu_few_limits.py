@@ -58,3 +58,25 @@ def test_few_fp8_keeps_what_is_not_finite(where):
     assert not bool(torch.isfinite(y2[uses][:, cols]).any())
     if where == "down scale":
         assert torch.equal(y2[:, 128:], y[:, 128:])
+
+
+@pytest.mark.parametrize("name,T", [("small_bf16", 20), ("small_fp32", 20), ("small_bf16_ns2", 50)])
+def test_few_infinite_weights(name, T):
+    """An infinite element of w_down makes an infinity of its column of y, of
+    moe_forward's sign, for the rows that use it; nothing else changes."""
+    cfg, inp = _inputs(name, T, 4)
+    say(f"case: moe_forward_few, an infinite weight, {name}")
+    w = moe.prepare_weights(cfg, inp)
+    y, idx = _call(cfg, inp, w)
+    e = int(idx[0, 0])
+    uses = (idx == e).any(1)
+    assert 0 < int(uses.sum()) < cfg.T
+    w.w_down[e, 4, 9] = float("inf")
+    w.w_down[e, 17, 2] = -float("inf")
+    y2, _ = _call(cfg, inp, w)
+    want, _ = _call(cfg, inp, w, lib=moe.moe_forward)
+    for col in (4, 17):
+        assert bool(torch.isinf(y2[uses, col]).all()) and torch.equal(y2[uses, col], want[uses, col])
+        assert torch.equal(y2[~uses, col], y[~uses, col])
+    rest = [c for c in range(cfg.d) if c not in (4, 17)]
+    assert torch.equal(y2[:, rest], y[:, rest])
