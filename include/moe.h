@@ -272,8 +272,10 @@ int moe_forward_static(const moe_shape* shape, const void* u, const void* centro
  * is rounded between the kernels, and H by the FP8 path alone (its 1x128 codes;
  * with BF16 weights H enters the down product as a pair of bf16 values), so y may
  * differ from moe_forward's by the roundings that it makes: 2^-9 of H and of Y
- * (E4M3: of Y, and what 8-bit matrix instructions leave).  A token's y is the same
- * whatever other tokens stand in the batch, but for the order of its sums.
+ * (E4M3: of Y, and what 8-bit matrix instructions leave).  A token's experts and
+ * gates are the same, bit for bit, whatever other tokens stand in the batch, and its
+ * y but for the order of its sums.  moe_forward sums the logits in another order:
+ * between scores that are level to fp32's rounding it may choose the other.
  * MOE_STAGE_ROUTE, MOE_STAGE_GATE_UP (with the selection), MOE_STAGE_QUANT (E4M3:
  * of h; u is quantised by the first launch) and MOE_STAGE_DOWN (with gates and
  * residual) are traced.  Calls that may overlap take a workspace each.

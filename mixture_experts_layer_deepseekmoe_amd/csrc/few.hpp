@@ -48,14 +48,14 @@ struct FewArgs {
 inline int few_runs(int cols, int fmt) { return cols * (fmt == FMT_F32 ? 4 : fmt == FMT_BF16 ? 2 : 1) / 128; }
 
 // The router's K slices: a block takes 16 experts and a slice of K, a run of 128
-// bytes a wave at a time, so one run for each of its 8 waves at least.  Up to 8 tokens
-// every block of the next kernel reads the slices of all tokens again, 64 of them
-// together at most; beyond, the selection reads them once, and 8 take the router of 64
-// tokens at d = 7168 from 39 us (one slice: 16 blocks) to 10.
-inline int few_slices(int T, int d, int x_fmt) {
-  const int most = (few_runs(d, x_fmt) + 7) / 8, want = T > 8 ? 8 : 64 / (T > 0 ? T : 1);
-  const int s = want < most ? want : most;
-  return s > 1 ? s : 1;
+// bytes a wave at a time, so one run for each of its 8 waves at least.  They go by the
+// row alone: a token's logits, and with them its experts and gates, are then the same,
+// bit for bit, in every batch (scores may be level to fp32's rounding).  At most 16, us:
+// d = 7168 in bf16 1 token 153.6, 8 tokens 897, 64 tokens 3191; at most 8: 154.0, 898,
+// 3192; one slice of 64 tokens (16 blocks) takes 29 more.
+inline int few_slices(int d, int x_fmt) {
+  const int most = (few_runs(d, x_fmt) + 7) / 8;
+  return most < 16 ? most : 16;
 }
 
 // Blocks that share 16 columns of y, each a part of the experts' runs, where the

@@ -28,7 +28,7 @@ Layout make_layout(const moe_shape& s) {
   const bool fp8 = s.w_dtype == MOE_DTYPE_E4M3;
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o += align_up(bytes); return at; };
-  L.slices = moe::few_slices(s.T, s.d, fmt_of(s.x_dtype));
+  L.slices = moe::few_slices(s.d, fmt_of(s.x_dtype));
   L.taken = take(4);
   L.logits = take(L.slices * T * s.n_routed * 4);
   L.idx = take(T * K * 4);

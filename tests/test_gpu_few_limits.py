@@ -80,3 +80,32 @@ def test_few_infinite_weights(name, T):
         assert torch.equal(y2[~uses, col], y[~uses, col])
     rest = [c for c in range(cfg.d) if c not in (4, 17)]
     assert torch.equal(y2[:, rest], y[:, rest])
+
+
+@pytest.mark.parametrize("dtype,kw", [("bf16", {}), ("f32", {}), ("bf16", dict(n_groups=8, topk_groups=3))])
+def test_few_selection_in_any_batch(dtype, kw):
+    """A token's experts and gates are the same bits in every batch, also where scores
+    are level: centroids [p, q] and [q, p] have the same score for rows [v, v], and the
+    order of its sum alone says which is larger."""
+    say(f"case: moe_forward_few, selection in batches of other sizes, {dtype} {kw}")
+    T, d, N, K = 64, 8192, 48, 5
+    shape = moe.LayerShape(T, d, N, 0, 64, K, dtype, dtype, "f32", kw.get("n_groups", 1), kw.get("topk_groups", 1))
+    g = torch.Generator().manual_seed(11)
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    half = lambda *s: torch.randn(s, generator=g).to(dt)  # noqa: E731
+    v, p, q = half(T, d // 2), 0.02 * half(N // 2, d // 2), 0.02 * half(N // 2, d // 2)
+    u = torch.cat([v, v], 1).to(DEV).contiguous()
+    E = torch.stack([torch.cat([p, q], 1), torch.cat([q, p], 1)], 1).view(N, d).to(DEV).contiguous()
+    b = torch.zeros(N, device=DEV)
+    w = moe.ExpertWeights((0.01 * half(N, 128, d)).to(DEV), (0.01 * half(N, d, 64)).to(DEV))
+
+    def run(n, at):
+        s = moe.LayerShape(n, d, N, 0, 64, K, dtype, dtype, "f32", shape.n_groups, shape.topk_groups)
+        r = moe.alloc_routing(s)
+        moe.moe_forward_few(s, u[at:at + n].contiguous(), E, b, w, routing=r)
+        return r["topk_idx"], r["topk_gate"]
+
+    idx, gate = run(T, 0)
+    for n, at in ((1, 0), (1, 63), (2, 5), (4, 30), (5, 17), (8, 40), (9, 3), (17, 20), (33, 31)):
+        i2, g2 = run(n, at)
+        assert torch.equal(i2, idx[at:at + n]) and torch.equal(g2, gate[at:at + n]), (n, at)
