@@ -160,8 +160,8 @@ __device__ __forceinline__ void few_select(const FewArgs& a, int t, float* keys,
     id[q] = q;
     const int e = lane + 64 * q;
     if (e >= N) continue;
-    s[q] = sigmoid_f32(s[q]);
-    const float v = s[q] + b[q];
+    s[q] = kept_score(s[q]);
+    const float v = score_of(s[q]) + b[q];
     key[q] = ordered(v);
     if (a.topk_groups < a.n_groups) keys[e] = v != v ? -INFINITY : v;
   }
@@ -232,7 +232,7 @@ __device__ __forceinline__ void few_select(const FewArgs& a, int t, float* keys,
     }
     if (!MOE_CHECK(be >= 0 && be < N, 801)) be = 0;
     const float bs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s[0]), l));
-    sum += bs;
+    sum += score_of(bs);
     if (lane == k) { chosen = be; chosen_s = bs; }
     if (lane == l) {
 #pragma unroll
@@ -240,9 +240,10 @@ __device__ __forceinline__ void few_select(const FewArgs& a, int t, float* keys,
       key[NQ - 1] = 0;
     }
   }
+  const float gate = selected_gate(chosen_s, sum, lane, a.top_k);
   if (lane < a.top_k) {
     idx_out[lane] = chosen;
-    gate_out[lane] = chosen_s / sum;
+    gate_out[lane] = gate;
   }
 }
 

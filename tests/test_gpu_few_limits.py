@@ -7,6 +7,7 @@ import torch
 
 import mixture_experts_layer_deepseekmoe_amd as moe
 from moe_workloads import PARITY_CONFIGS, make_inputs, to_numpy_f32
+from oracle import moe_oracle as O
 from tests.parity import say
 
 pytestmark = pytest.mark.gpu
@@ -109,3 +110,46 @@ def test_few_selection_in_any_batch(dtype, kw):
     for n, at in ((1, 0), (1, 63), (2, 5), (4, 30), (5, 17), (8, 40), (9, 3), (17, 20), (33, 31)):
         i2, g2 = run(n, at)
         assert torch.equal(i2, idx[at:at + n]) and torch.equal(g2, gate[at:at + n]), (n, at)
+
+
+def _tiny_scores(T, d, N, dtype):
+    """Rows f_t times ones and centroids whose entries are all z_e / d: with powers of two for
+    f_t and d every logit is exact in fp32, whatever its sum's order.  z_e from -84 to
+    -91.5: at f = 1 fp32 holds some scores and not others, at f = 2 none, at 1/2 all.
+    The bias alone decides who is chosen."""
+    f = 2.0 ** (np.arange(T) % 4 - 2)
+    u = torch.tensor(f, dtype=torch.float32)[:, None].expand(T, d)
+    z = -84.0 - 0.5 * ((7 * np.arange(N) + 5 * (np.arange(N) // 16)) % 16)
+    E = (torch.tensor(z, dtype=torch.float32) / d)[:, None].expand(N, d)
+    b = torch.tensor(0.01 * ((5 * np.arange(N)) % 16), dtype=torch.float32) + 1e-4 * torch.arange(N)
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    return u.to(dt).contiguous().to(DEV), E.to(dt).contiguous().to(DEV), b.to(DEV)
+
+
+def _check_tiny_gates(u, E, b, idx, gate, K):
+    """Gates to 1e-4: logf and the logits' differences leave a few units in the last place of
+    88 (2^-18 each, 4e-6), and 2^-21 of a score below the normal range; expf and the
+    quotient a few 2^-24."""
+    r = O.route(to_numpy_f32(u.cpu()).astype(np.float64), to_numpy_f32(E.cpu()), b.cpu().numpy(), K)
+    assert np.array_equal(np.sort(r["idx"], 1), np.sort(idx, 1))
+    s = O.affinities(to_numpy_f32(u.cpu()), to_numpy_f32(E.cpu()))
+    want = O.normalised_gates(s, idx)
+    assert np.isfinite(gate).all() and np.abs(gate - want).max() <= 1e-4, np.abs(gate - want).max()
+    assert (np.abs(gate - want) <= 1e-4 * want + 2e-8).all()
+
+
+@pytest.mark.parametrize("T,N,K,dtype", [(4, 16, 6, "bf16"), (1, 16, 4, "f32"), (40, 300, 8, "bf16"), (64, 100, 3, "f32")])
+def test_few_scores_below_fp32(T, N, K, dtype):
+    """Tokens whose selected scores are all, or in part, below what fp32 holds: the gates are
+    still the scores' shares, and y is finite."""
+    say(f"case: moe_forward_few, tiny scores, {T} tokens, {N} experts, {dtype}")
+    d = 256
+    u, E, b = _tiny_scores(T, d, N, dtype)
+    shape = moe.LayerShape(T, d, N, 0, 64, K, dtype, dtype)
+    g = torch.Generator().manual_seed(5)
+    w = moe.ExpertWeights((0.1 * torch.randn((N, 128, d), generator=g)).to(u.dtype).to(DEV),
+                          (0.1 * torch.randn((N, d, 64), generator=g)).to(u.dtype).to(DEV))
+    r = moe.alloc_routing(shape)
+    y = moe.moe_forward_few(shape, u, E, b, w, routing=r)
+    assert bool(torch.isfinite(y).all())
+    _check_tiny_gates(u, E, b, r["topk_idx"].cpu().numpy(), r["topk_gate"].cpu().numpy().astype(np.float64), K)
