@@ -14,7 +14,8 @@
 // Ordering is by v = s + b descending, exact ties to the lower expert index;
 // a NaN score ranks below every number, so K distinct in-range experts are
 // always produced.  Gates are s_k / sum of the K selected s, summed in
-// selection order in fp32.
+// selection order in fp32 (of scores that fp32 does not hold, by their logits:
+// selected_gate).
 #include "gemm_core.hpp"
 #include "kernels.hpp"
 
@@ -46,7 +47,7 @@ __device__ __forceinline__ uint64_t keep_groups(const float* srow, const float* 
       int be = 0x7fffffff;
       for (int m = 0; m < gsize; ++m) {
         const int e = lane * gsize + m;
-        float x = srow[e] + bias[e];
+        float x = score_of(srow[e]) + bias[e];
         if (x != x) x = -INFINITY;
         const bool after = x < pv || (x == pv && e > pe);
         if (after && (x > bv || (x == bv && e < be))) { bv = x; be = e; }
@@ -73,8 +74,8 @@ __device__ __forceinline__ uint64_t keep_groups(const float* srow, const float* 
   return kept;
 }
 
-// Top-K of one token by one wave: srow holds the token's N_r sigmoid scores
-// (LDS or global), bq[q] the bias of expert lane + 64 q.  Lane k < K writes
+// Top-K of one token by one wave: srow holds the token's N_r scores as kept_score
+// makes them (LDS or global), bq[q] the bias of expert lane + 64 q.  Lane k < K writes
 // the k-th selected expert and its gate.  With grouped routing
 // (1 < topk_groups < n_groups) only the kept groups' experts take part.
 template <int NQ>
@@ -88,7 +89,7 @@ __device__ __forceinline__ void select_topk(const float* srow, const float (&bq)
     const int e = lane + 64 * q;
     float v = -INFINITY;
     if (e < n_routed) {
-      v = srow[e] + bq[q];
+      v = score_of(srow[e]) + bq[q];
       if (v != v) v = -INFINITY;
     }
     key[q] = v;
@@ -125,13 +126,14 @@ __device__ __forceinline__ void select_topk(const float* srow, const float (&bq)
     if (!MOE_CHECK(be >= 0 && be < n_routed, 101)) be = 0;
     if ((be & 63) == lane) taken |= 1u << (be >> 6);
     const float s_sel = srow[be];
-    sum += s_sel;
+    sum += score_of(s_sel);
     if (lane == k) { chosen = be; chosen_s = s_sel; }
   }
+  const float gate = selected_gate(chosen_s, sum, lane, top_k);
   if (lane < top_k) {
     idx_out[lane] = chosen;
-    gate_out[lane] = chosen_s / sum;
-    if (a.sel_score != nullptr) a.sel_score[(idx_out - a.idx) + lane] = chosen_s;
+    gate_out[lane] = gate;
+    if (a.sel_score != nullptr) a.sel_score[(idx_out - a.idx) + lane] = score_of(chosen_s);
   }
 }
 
@@ -218,12 +220,12 @@ __global__ __launch_bounds__(64 * RouteCfg<NRMAX>::NW) void route_kernel(RouteAr
         const int e = ec + C::EW * w + 16 * j + 4 * lg;
         float* dst = sbuf + (16 * i + lr) * SSTRIDE + e;
         if (e + 3 < a.n_routed) {
-          *reinterpret_cast<float4*>(dst) = make_float4(sigmoid_f32(acc[i][j][0]), sigmoid_f32(acc[i][j][1]),
-                                                        sigmoid_f32(acc[i][j][2]), sigmoid_f32(acc[i][j][3]));
+          *reinterpret_cast<float4*>(dst) = make_float4(kept_score(acc[i][j][0]), kept_score(acc[i][j][1]),
+                                                        kept_score(acc[i][j][2]), kept_score(acc[i][j][3]));
         } else {
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            if (e + r < a.n_routed) dst[r] = sigmoid_f32(acc[i][j][r]);
+            if (e + r < a.n_routed) dst[r] = kept_score(acc[i][j][r]);
         }
       }
   }
@@ -289,7 +291,7 @@ __global__ __launch_bounds__(512) void route_scores_kernel(RouteArgs a) {
     float* dst = a.scores + static_cast<size_t>(t) * a.n_routed + e;
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      if (e + r < a.n_routed) dst[r] = sigmoid_f32(acc[i][0][r]);
+      if (e + r < a.n_routed) dst[r] = kept_score(acc[i][0][r]);
   }
 }
 
@@ -382,7 +384,7 @@ __global__ __launch_bounds__(256) void route_finish_kernel(RouteArgs a) {
     if (e < a.n_routed) {
       float z = 0.f;
       for (int sl = 0; sl < a.ksplit; ++sl) z += src[sl * slice_stride + e];
-      srow[e] = sigmoid_f32(z);
+      srow[e] = kept_score(z);
     }
   }
   __builtin_amdgcn_wave_barrier();
