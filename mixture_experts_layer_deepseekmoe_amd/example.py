@@ -71,10 +71,17 @@ class Model:
     def _norm_after(self, k: int) -> torch.Tensor:
         return self.params[f"{k + 1}.w_in" if k + 1 < self.s.layers else "w_final"]
 
+    def _tokens(self, tokens: torch.Tensor) -> torch.Tensor:
+        """Tokens of any integer type, strides and device as moe_embed takes them (outside the vocabulary: a row of zeros)."""
+        tokens = tokens.to(self.params["embed"].device)
+        if tokens.dtype is not torch.int32:   # what int32 does not hold must not wrap into the vocabulary
+            tokens = torch.where((tokens >= 0) & (tokens < self.s.vocab), tokens, -1).to(torch.int32)
+        return tokens.contiguous()
+
     def forward(self, tokens: torch.Tensor, train: bool):
         """The final normed rows and, for training, what the backward needs."""
         s, p, T = self.s, self.params, tokens.numel()
-        bs, ls = s.block(T), s.layer(T)
+        bs, ls, tokens = s.block(T), s.layer(T), self._tokens(tokens)
         keep: List[dict] = []
         new_save = lambda: moe.alloc_block_save(bs, e4m3=True) if train else None  # noqa: E731
         s_in = new_save()
@@ -121,7 +128,7 @@ class Model:
                           f"{k}.ws_gate_up": gw.dws_gate_up, f"{k}.ws_down": gw.dws_down})
             # n feeds the layer (du) and, negated, the skip (dy); x feeds the norm and the residual (dx)
             dx, grads[f"{k}.w_in"] = moe.moe_block_in_backward(bs, du, p[f"{k}.w_in"], f["s_in"], dn_sub=dy, do=dx)
-        grads["embed"] = moe.moe_embed_backward(s.embed(), tokens, dx)
+        grads["embed"] = moe.moe_embed_backward(s.embed(), self._tokens(tokens), dx)
         return loss.sum() / count, grads
 
 
