@@ -7,7 +7,7 @@ Each block is norm -> MoE layer -> norm, gate and residual; the loss is the
 cross entropy over the vocabulary.  The forward keeps 8-bit checkpoints of the
 normed rows, so a block's x, y and its output are not kept for the backward.
 The embedding brings the first block's norm; the gradients are clipped by their
-common norm (--max-norm); up to 64 tokens at a time are scored by the layer's
+common norm (--max-norm); up to 48 tokens at a time are scored by the layer's
 forward for a few tokens.
 The task: the next token is a fixed function of the current one.
 """
@@ -45,6 +45,16 @@ class ModelShape:
 
     def loss(self, T=None) -> moe.LossShape:
         return moe.LossShape(self.T if T is None else T, self.d, self.vocab)
+
+
+# moe_forward_few is ahead or level up to here; its and moe_forward's time, bf16, us: d = 2048 48 tokens 257, 264, 56
+# tokens 270, 264; d = 7168 48 tokens 2764, 2755, 64 tokens 3193, 3166; d = 256 64 tokens 32, 36.
+FEW = 48
+
+
+def layer_forward(s: ModelShape, T: int):
+    """The layer's forward that scores T tokens: few ones by moe_forward_few, within its limit on the experts' width."""
+    return moe.moe_forward_few if T <= FEW and s.inter <= 32768 else moe.moe_forward
 
 
 class Model:
@@ -93,8 +103,7 @@ class Model:
                 y = moe.moe_forward_train(ls, n, cen, self.bias[k], w, ws)
             else:
                 ws = None
-                forward = moe.moe_forward_few if T <= moe.FEW_TOKENS else moe.moe_forward
-                y = forward(ls, n, cen, self.bias[k], w)
+                y = layer_forward(s, T)(ls, n, cen, self.bias[k], w)
             s_out, s_next = new_save(), new_save()
             x, n_next = moe.moe_block_out(bs, x, y, w=p[f"{k}.w_out"], gate=p[f"{k}.gate"], skip=n,
                                           w_next=self._norm_after(k), save=s_out, save_next=s_next)

@@ -34,3 +34,14 @@ def test_tokens_of_any_integer_type(T):
         for t in (tokens.long(), strided):
             _, g = model.step(t, labels)
             assert all(torch.equal(g[k], ref[k]) for k in ref)
+
+
+def test_wide_experts_score():
+    """Experts beyond the width that moe_forward_few takes."""
+    say("case: example, wide experts")
+    s = X.ModelShape(T=64, d=64, layers=1, vocab=50, n_routed=2, inter=32832, top_k=1)
+    model = X.Model(s, seed=1)
+    tokens, labels = X.make_batch(s, 2, ignored=0.0)
+    loss = model.loss(tokens[:3].contiguous(), labels[:3].contiguous())
+    assert loss.shape == (3,) and bool(torch.isfinite(loss).all()) and bool((loss > 0).all())
+    assert torch.equal(loss, model.loss(tokens, labels)[:3])
