@@ -157,12 +157,14 @@ def make_batch(s: ModelShape, seed: int, ignored: float = 0.1):
 
 
 def train(s: ModelShape, steps: int, lr: float = 0.01, log=lambda *a: None, max_norm: float = float("inf")) -> Model:
-    """``max_norm``: the gradients are scaled down to this norm (all of them together) where theirs is larger."""
+    """``max_norm``: the gradients are scaled down to this norm (all of them together) where theirs is larger; infinite:
+    their norm is not formed."""
     model = Model(s)
     opt = torch.optim.Adam(list(model.params.values()), lr=lr, betas=(0.9, 0.99))
     for k in range(steps):
         loss, grads = model.step(*make_batch(s, 100 + k))
-        clip(grads, max_norm)
+        if max_norm != float("inf"):
+            clip(grads, max_norm)
         for name, q in model.params.items():
             q.grad = grads[name]
         opt.step()

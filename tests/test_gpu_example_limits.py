@@ -45,3 +45,16 @@ def test_wide_experts_score():
     loss = model.loss(tokens[:3].contiguous(), labels[:3].contiguous())
     assert loss.shape == (3,) and bool(torch.isfinite(loss).all()) and bool((loss > 0).all())
     assert torch.equal(loss, model.loss(tokens, labels)[:3])
+
+
+def test_training_without_a_limit_forms_no_norm(monkeypatch):
+    say("case: example, training without a limit")
+    calls = []
+    whole = X.clip
+    monkeypatch.setattr(X, "clip", lambda *a: calls.append(a) or whole(*a))
+    X.train(SMALL, 2)
+    assert not calls
+    X.train(SMALL, 2, max_norm=1.0)
+    assert len(calls) == 2
+    with pytest.raises(moe.MoEError):
+        X.train(SMALL, 1, max_norm=float("nan"))
