@@ -15,6 +15,7 @@ The task: the next token is a fixed function of the current one.
 from __future__ import annotations
 
 import argparse
+import math
 from dataclasses import dataclass
 from typing import List
 
@@ -158,13 +159,16 @@ def make_batch(s: ModelShape, seed: int, ignored: float = 0.1):
 
 def train(s: ModelShape, steps: int, lr: float = 0.01, log=lambda *a: None, max_norm: float = float("inf")) -> Model:
     """``max_norm``: the gradients are scaled down to this norm (all of them together) where theirs is larger; infinite:
-    their norm is not formed."""
+    their norm is not formed.  A step whose norm is not finite is left out."""
     model = Model(s)
     opt = torch.optim.Adam(list(model.params.values()), lr=lr, betas=(0.9, 0.99))
     for k in range(steps):
         loss, grads = model.step(*make_batch(s, 100 + k))
         if max_norm != float("inf"):
-            clip(grads, max_norm)
+            norm = clip(grads, max_norm).item()
+            if not math.isfinite(norm):   # nothing was clipped: such gradients must not reach the parameters
+                log(f"step {k}: no step, the gradients' norm is {norm}")
+                continue
         for name, q in model.params.items():
             q.grad = grads[name]
         opt.step()

@@ -58,3 +58,33 @@ def test_training_without_a_limit_forms_no_norm(monkeypatch):
     assert len(calls) == 2
     with pytest.raises(moe.MoEError):
         X.train(SMALL, 1, max_norm=float("nan"))
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_step_that_is_not_finite_is_left_out(bad, monkeypatch):
+    """One bad gradient element in the first of two steps: the parameters are those of the
+    second step alone (the optimiser has seen nothing before)."""
+    say(f"case: example, a gradient with {bad}")
+    step, seen = X.Model.step, []
+
+    def one_bad(self, tokens, labels):
+        loss, grads = step(self, tokens, labels)
+        if not seen:
+            grads["0.w_down"][1, 2, 3] = bad
+        seen.append(1)
+        return loss, grads
+
+    lines = []
+    monkeypatch.setattr(X.Model, "step", one_bad)
+    model = X.train(SMALL, 2, max_norm=0.5, log=lines.append)
+    assert len(seen) == 2 and len(lines) == 2 and "no step" in lines[0]
+    assert all(bool(torch.isfinite(p).all()) for p in model.params.values())
+    monkeypatch.setattr(X.Model, "step", step)
+    ref = X.Model(SMALL)
+    opt = torch.optim.Adam(list(ref.params.values()), lr=0.01, betas=(0.9, 0.99))
+    _, grads = ref.step(*X.make_batch(SMALL, 101))
+    X.clip(grads, 0.5)
+    for name, q in ref.params.items():
+        q.grad = grads[name]
+    opt.step()
+    assert all(torch.equal(model.params[k], ref.params[k]) for k in ref.params)
