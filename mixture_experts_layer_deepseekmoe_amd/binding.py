@@ -408,7 +408,8 @@ def moe_forward_few(shape: LayerShape, u: torch.Tensor, centroids: torch.Tensor,
     if y is None:
         y = torch.empty((T, d), dtype=_TORCH_DT[DTYPE_CODE[shape.out_dtype]], device=u.device)
     ws = alloc_few_workspace(shape, u.device) if workspace is None else workspace
-    _same_device(u, centroids, bias, weights.w_gate_up, weights.w_down, weights.ws_gate_up, weights.ws_down, y, ws)
+    scales = (weights.s_gate_up, weights.s_down, weights.ss_gate_up, weights.ss_down) if shape.w_dtype == "e4m3" else ()
+    _same_device(u, centroids, bias, weights.w_gate_up, weights.w_down, weights.ws_gate_up, weights.ws_down, *scales, y, ws)
     rs = None
     if routing is not None:
         sizes = {"topk_idx": (T, shape.top_k), "topk_gate": (T, shape.top_k), "expert_counts": (N,),

@@ -216,3 +216,28 @@ def test_tensor_list_refuses():
         moe.TensorList([torch.zeros(3, dtype=torch.float16)])
     with pytest.raises(ValueError, match="GPU"):
         moe.TensorList([torch.zeros(3)])
+
+
+# ---------------------------------------------------------------- devices
+
+
+def _compared(monkeypatch, fn):
+    """The tensors whose devices a call compares before it takes their addresses (which host tensors do not have)."""
+    seen = []
+    monkeypatch.setattr(B, "_same_device", lambda *ts: seen.extend(id(t) for t in ts if t is not None))
+    with pytest.raises(ValueError, match="GPU"):
+        fn()
+    return seen
+
+
+@pytest.mark.parametrize("w_dtype", ["bf16", "e4m3"])
+def test_few_compares_every_device(monkeypatch, w_dtype):
+    s = _few(w_dtype=w_dtype)
+    code = torch.uint8 if w_dtype == "e4m3" else torch.bfloat16
+    w = [torch.zeros(n, dtype=code) for n in ((8, 256, 256), (8, 256, 128), (1, 256, 256), (1, 256, 128))]
+    if w_dtype == "e4m3":
+        w += [torch.zeros(n) for n in ((8, 2, 2), (8, 2, 1), (1, 2, 2), (1, 2, 1))]
+    rest = dict(u=torch.zeros(4, 256).bfloat16(), centroids=torch.zeros(8, 256).bfloat16(), bias=torch.zeros(8),
+                y=torch.zeros(4, 256), workspace=torch.zeros(1 << 20, dtype=torch.uint8))
+    seen = _compared(monkeypatch, lambda: moe.moe_forward_few(s, weights=moe.ExpertWeights(*w), **rest))
+    assert {id(t) for t in [*w, *rest.values()]} <= set(seen)
