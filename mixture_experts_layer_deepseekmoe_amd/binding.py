@@ -765,7 +765,8 @@ def moe_embed(shape: EmbedShape, tokens: torch.Tensor, table: torch.Tensor, w_ne
         x = torch.empty((T, d), dtype=_ARG_DT[shape.x_dtype], device=tokens.device)
     if n_next is None and w_next is not None:
         n_next = torch.empty((T, d), dtype=_ARG_DT[shape.n_dtype], device=tokens.device)
-    _same_device(tokens, table, w_next, x, n_next)
+    saved = () if save_next is None else (save_next.rstd, save_next.codes, save_next.scales)
+    _same_device(tokens, table, w_next, x, n_next, *saved)
     rc = load_library().moe_embed(
         ctypes.byref(shape.c()), _arg(tokens, "tokens", "i32", T), _arg(table, "table", shape.table_dtype, V, d),
         _arg(w_next, "w_next", "f32", d), _arg(x, "x", shape.x_dtype, T, d), _arg(n_next, "n_next", shape.n_dtype, T, d),

@@ -241,3 +241,22 @@ def test_few_compares_every_device(monkeypatch, w_dtype):
                 y=torch.zeros(4, 256), workspace=torch.zeros(1 << 20, dtype=torch.uint8))
     seen = _compared(monkeypatch, lambda: moe.moe_forward_few(s, weights=moe.ExpertWeights(*w), **rest))
     assert {id(t) for t in [*w, *rest.values()]} <= set(seen)
+
+
+def test_embed_compares_every_device(monkeypatch):
+    s = _es()
+    args = dict(tokens=torch.zeros(5, dtype=torch.int32), table=torch.zeros(100, 256), w_next=torch.zeros(256),
+                x=torch.zeros(5, 256), n_next=torch.zeros(5, 256).bfloat16())
+    save = [torch.zeros(5), torch.zeros(5, 256, dtype=torch.uint8), torch.zeros(5, 2)]
+    seen = _compared(monkeypatch, lambda: moe.moe_embed(s, save_next=moe.BlockSave(*save), **args))
+    assert {id(t) for t in [*args.values(), *save]} <= set(seen)
+
+
+def test_other_calls_compare_every_device(monkeypatch):
+    tokens, dx = torch.zeros(5, dtype=torch.int32), torch.zeros(5, 256)
+    dt, ws = torch.zeros(100, 256), torch.zeros(1 << 20, dtype=torch.uint8)
+    seen = _compared(monkeypatch, lambda: moe.moe_embed_backward(_es(), tokens, dx, dtable=dt, workspace=ws))
+    assert {id(t) for t in (tokens, dx, dt, ws)} <= set(seen)
+    sumsq, norm = torch.zeros(1, dtype=torch.float64), torch.zeros(1)
+    assert {id(sumsq), id(ws)} <= set(_compared(monkeypatch, lambda: moe.moe_grad_sumsq([], sumsq=sumsq, workspace=ws)))
+    assert {id(sumsq), id(norm)} <= set(_compared(monkeypatch, lambda: moe.moe_grad_clip([], sumsq, 1.0, norm=norm)))
