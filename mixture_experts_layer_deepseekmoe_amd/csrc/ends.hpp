@@ -21,8 +21,9 @@ struct EmbedArgs {
 };
 
 // A token of many rows is summed by many waves: the sums of 16 sorted rows that are all
-// of one token are formed apart, and of batches of some size those of 256 from them, so
-// that the longest sum of one wave is 30 rows, 30 sums of 16 and one of 256 for every 256.
+// of one token are formed apart, and of batches of some size those of 256 from them.  Of n
+// rows the longest sum of one wave is then 30 rows, 30 sums of 16 and n / 256 of 256; of
+// smaller batches 30 rows and n / 16 sums of 16 (543 terms at most).
 constexpr int EMBED_CHUNK = 16, EMBED_CHUNK2 = 256, EMBED_PART2_T = 8192;
 constexpr int EMBED_RADIX_BLOCK = 4096;   // rows of a radix block
 // Rows are ranked by comparing each with all others up to this many (one launch, T^2
