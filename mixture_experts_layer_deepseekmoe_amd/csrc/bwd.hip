@@ -1119,22 +1119,19 @@ __global__ __launch_bounds__(256) void bwd_prep_kernel(BwdArgs a) {
 }
 
 // Per token: ds_k = (dg_k - sum_j g_j dg_j) / S, dz_k = ds_k s_k (1 - s_k);
-// dz also by grouped row (for dE).  Where S is tiny and fp32's s is 0 for some
-// (selected_gate), s_k / S is the gate and 1 - s_k is 1.
+// dz also by grouped row (for dE).
 __global__ __launch_bounds__(256) void bwd_dz_kernel(BwdArgs a) {
   const int t = blockIdx.x * 256 + threadIdx.x;
   if (t >= a.T) return;
   const size_t o = static_cast<size_t>(t) * a.top_k;
-  float S = 0.f, gd = 0.f, least = 1.f;
+  float S = 0.f, gd = 0.f;
   for (int k = 0; k < a.top_k; ++k) {
     S += a.sel_score[o + k];
-    least = fminf(least, a.sel_score[o + k]);
     gd = fmaf(a.gate[o + k], a.dg[o + k], gd);
   }
   for (int k = 0; k < a.top_k; ++k) {
     const float s = a.sel_score[o + k];
-    const float dz = S < 0x1p-100f && least == 0.f ? (a.dg[o + k] - gd) * a.gate[o + k]
-                                                   : (a.dg[o + k] - gd) / S * (s * (1.f - s));
+    const float dz = (a.dg[o + k] - gd) / S * (s * (1.f - s));
     a.dz[o + k] = dz;
     a.dzr[a.pos[o + k]] = dz;
   }

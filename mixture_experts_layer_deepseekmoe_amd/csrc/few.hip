@@ -34,6 +34,7 @@
 // anyway, so y is as exact as with fp32 products.
 #include "few.hpp"
 #include "gemm_core.hpp"
+#include "scores.hpp"
 
 #include <type_traits>
 
@@ -240,7 +241,7 @@ __device__ __forceinline__ void few_select(const FewArgs& a, int t, float* keys,
       key[NQ - 1] = 0;
     }
   }
-  const float gate = selected_gate(chosen_s, sum, lane, a.top_k);
+  const float gate = selected(chosen_s, sum, lane, a.top_k).gate;
   if (lane < a.top_k) {
     idx_out[lane] = chosen;
     gate_out[lane] = gate;

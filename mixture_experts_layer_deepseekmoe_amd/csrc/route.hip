@@ -15,9 +15,10 @@
 // a NaN score ranks below every number, so K distinct in-range experts are
 // always produced.  Gates are s_k / sum of the K selected s, summed in
 // selection order in fp32 (of scores that fp32 does not hold, by their logits:
-// selected_gate).
+// scores.hpp).
 #include "gemm_core.hpp"
 #include "kernels.hpp"
+#include "scores.hpp"
 
 namespace moe {
 
@@ -129,11 +130,11 @@ __device__ __forceinline__ void select_topk(const float* srow, const float (&bq)
     sum += score_of(s_sel);
     if (lane == k) { chosen = be; chosen_s = s_sel; }
   }
-  const float gate = selected_gate(chosen_s, sum, lane, top_k);
+  const Selected sel = selected(chosen_s, sum, lane, top_k);
   if (lane < top_k) {
     idx_out[lane] = chosen;
-    gate_out[lane] = gate;
-    if (a.sel_score != nullptr) a.sel_score[(idx_out - a.idx) + lane] = score_of(chosen_s);
+    gate_out[lane] = sel.gate;
+    if (a.sel_score != nullptr) a.sel_score[(idx_out - a.idx) + lane] = sel.score;
   }
 }
 
