@@ -28,7 +28,8 @@
  *     touched.  MOE_ERR_LAUNCH reports a failed kernel launch (the outputs
  *     are then undefined).
  *   - Inputs are expected to be finite.  Should a score be NaN the router
- *     still returns K distinct in-range experts per token.
+ *     still returns K distinct in-range experts per token.  Scores are fp32; of
+ *     logits below -88, where they are 0, the gates go by the logits.
  *   - Repeated calls with the same inputs give bit-identical outputs.
  */
 #ifndef MOE_MI355X_H
@@ -269,10 +270,12 @@ int moe_forward_static(const moe_shape* shape, const void* u, const void* centro
  * drafted tokens of a request): the same layer, arguments and routing, in three to
  * six launches, each chosen expert's weights read once.  All dtype combinations,
  * shared experts and group-limited routing as moe_forward has them.  Nothing but H
- * is rounded between the kernels, and H by the FP8 path alone (its 1x128 codes;
- * with BF16 weights H enters the down product as a pair of bf16 values), so y may
- * differ from moe_forward's by the roundings that it makes: 2^-9 of H and of Y
- * (E4M3: of Y, and what 8-bit matrix instructions leave).  A token's experts and
+ * is rounded between the kernels: to its 1x128 codes with E4M3 weights; with BF16
+ * weights it enters the down product as a pair of bf16 values, which leaves 2^-17 of
+ * it; with F32 weights not at all.  So y may differ from moe_forward's by the
+ * roundings that it makes: 2^-8 of H and of Y (E4M3: of Y, and what 8-bit matrix
+ * instructions leave).  Infinite and NaN weights reach the tokens that use them and
+ * no others, an infinity as moe_forward has it.  A token's experts and
  * gates are the same, bit for bit, whatever other tokens stand in the batch, and its
  * y but for the order of its sums.  moe_forward sums the logits in another order:
  * between scores that are level to fp32's rounding it may choose the other.
@@ -280,8 +283,9 @@ int moe_forward_static(const moe_shape* shape, const void* u, const void* centro
  * of h; u is quantised by the first launch) and MOE_STAGE_DOWN (with gates and
  * residual) are traced.  Calls that may overlap take a workspace each.
  * Limits beside the layer's: T at most MOE_FEW_TOKENS, d and inter at most 32768.
- * One token takes 0.5 to 0.6 of moe_forward's time, 16 tokens 0.8 to 0.95; from about
- * 32 tokens on the two are level, and moe_forward is ahead by up to 15% at 64.
+ * One token takes 0.4 (F32) to 0.6 of moe_forward's time, 16 tokens 0.75 to 0.96, 48
+ * tokens 0.7 (F32) to 1.  At 64 tokens moe_forward is ahead in BF16 (1% at d = 7168,
+ * 4% at d = 2048), not with E4M3 or F32 weights.
  */
 #define MOE_FEW_TOKENS 64
 int moe_few_workspace_size(const moe_shape* shape, size_t* bytes);

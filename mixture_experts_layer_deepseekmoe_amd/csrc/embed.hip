@@ -14,8 +14,9 @@
 // 290 and the sums 80: its waves wait for their searches, loads and stores in turn.)
 //
 // Measured, us: 8192 rows of 7168 into 65536 in fp32, 466 with the forward: forward with
-// the norm 54, clearing beside the sort 303 (6.2 TB/s), sums 27 + 5 + 84; 4096 rows of
-// 2048 into 65536 in bf16, 80: 12.5, 42, 7, 20.
+// the norm 54, clearing beside the sort 300 (6.3 TB/s), sums 26 + 5 + 82; 4096 rows of
+// 2048 into 65536 in bf16, 84: 13, 40.5, 7, 21.  Added to a table, the backward alone 108
+// of 414 and 25 of 60.
 #include "ends.hpp"
 #include "gemm_core.hpp"
 #include "rows.hpp"

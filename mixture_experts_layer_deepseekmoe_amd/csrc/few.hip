@@ -22,16 +22,19 @@
 //                      that leaves CUs idle, blocks share the experts' runs, and
 //   few_sum_kernel     adds their sums
 //
-// Measured, us (reading alone reaches 6.2 TB/s here): 1 token, d = 7168 in bf16, 9
-// experts of 88 MB: 154 in all, gate and up 102 (5.2 TB/s), down 55 (4.8), the router
-// 4.7; 4 tokens in 8 bits, 33 experts of 44 MB: 258, gate and up 162 (5.9), down 86
-// (5.6); 32 tokens, 164 experts: 2376, gate and up 1547 (6.2), down 802 (6.0).  1 token,
-// d = 2048, 8 experts of 17 MB: 40, gate and up 22, down 14, the rest launches; of the
-// 22, 8 are not loads (the selection, a block's sums, the last blocks).
+// Measured, us, with other inputs in every call (reading alone reaches 6.2 TB/s here): 1
+// token, d = 7168 in bf16, 9 experts of 88 MB: 154 in all, gate and up 102 (5.2 TB/s),
+// down 55 (4.8), the router 4.6; 4 tokens in 8 bits, 33 experts of 44 MB: 253, gate and
+// up 162 (5.9), down 87 (5.6); 32 tokens, 164 experts: 2388, gate and up 1543 (6.2),
+// down 801 (6.0).  1 token, d = 2048, 8 experts of 17 MB: 44 (40 where the last call's
+// weights still lie in the caches), gate and up 26 (23 at best), down 15, the rest
+// launches; of the 23, 8 are not loads (the selection, a block's sums, the last blocks).
 //
-// Sums are fp32.  With bf16 weights the operand h is a pair of bf16 values, what
-// the first rounds off in the second (2^-16 is left): the MFMAs wait for HBM
-// anyway, so y is as exact as with fp32 products.
+// Sums are fp32.  With bf16 weights the operand h is a pair of bf16 values, what the
+// first rounds off in the second; 2^-17 of it is left at most.  The experts' part of y
+// is then 2.5e-6 from 64 bits, where fp32 values and products (fp32 weights) leave 3e-7
+// and a single bf16 value would leave about 1e-3: the pair costs the MFMAs nothing, which
+// wait for HBM, and fp32 products would take eight times as many.
 #include "few.hpp"
 #include "gemm_core.hpp"
 #include "scores.hpp"

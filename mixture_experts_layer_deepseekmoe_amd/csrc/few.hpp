@@ -61,13 +61,13 @@ inline int few_slices(int d, int x_fmt) {
 // Blocks that share 16 columns of y, each a part of the experts' runs, where the
 // columns alone leave CUs idle (two blocks to a CU are asked for) and each block has a
 // number of runs left: with 64 at least, without splits and with 32, us, d = 2048 in
-// bf16: 1 token 40.1, 42.9, 44.5; 8 tokens 138, 163, 136; 32 tokens 242, 296, 237; 64
+// bf16 (the one width at which the number was measured): 1 token 40.1, 42.9, 44.5; 8 tokens 138, 163, 136; 32 tokens 242, 296, 237; 64
 // tokens 304, 422, 305.  More than one block but less than two to a CU: four splits even
 // the CUs' shares out, once there is work for them; one split and four, us: d = 7168
 // (448 blocks) in bf16 1 token (288 runs) 153, 164, 2 tokens (544) 292, 289, 32 tokens
 // 2389, 2357, 64 tokens 3358, 3198, in 8 bits 2 tokens (272 runs) 171, 179, 64 tokens
 // 1734, 1667; d = 5120 (320 blocks) in bf16 2 tokens (336 runs) 151, 147, 64 tokens 818,
-// 692.  From 512 blocks on it does not pay: 768, 2 tokens 194, 236.
+// 692: the border lies between 288 and 336 runs, in 8 bits between 272 and 64 tokens'.  From 512 blocks on it does not pay: 768, 2 tokens 194, 236.
 constexpr int FEW_SPLITS = 16, FEW_SPLIT_RUNS = 64, FEW_EVEN_RUNS = 320;
 inline int few_splits(int T, int d, int n_routed, int n_shared, int inter, int top_k, int w_fmt) {
   const int blocks = d / 16, tk = T * top_k;

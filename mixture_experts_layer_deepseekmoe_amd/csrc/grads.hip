@@ -11,8 +11,8 @@
 // the chunks from the last to the first, so it begins with what the caches still
 // hold, and does nothing in place where nothing is to be clipped.
 //
-// Measured, 571M fp32 elements: the sum 358 us (6.4 TB/s; chunks of 8192, more
-// registers and fewer waves: 449), clipping into other tensors 733 us (6.2 TB/s; with
+// Measured, 571M fp32 elements: the sum 362 us (6.3 TB/s; chunks of 8192, more
+// registers and fewer waves: 449), clipping into other tensors 727 us (6.3 TB/s; with
 // 4096 blocks in turns 793, with 2048 and without the streaming hints 890).
 #include "ends.hpp"
 
